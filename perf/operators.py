@@ -1,0 +1,590 @@
+"""The operators around the weight products of a decode step, as measured work.
+
+Four operators that a program calls between the quantized products: the
+root-mean-square norm that makes their int8 inputs (rmsnorm_quant_run), the
+block tables and slot maps of a paged cache (kv_tables_run), the writing of
+new keys and values into that cache in 8 bits (kv_append_run) and the
+attention that reads it for one token or a tile of draft tokens
+(kv_attention_run).
+
+A case is a dict of plain values; prepare() makes its inputs on the GPU from a
+seed; run() makes one pass through the operator, in its plain form (elementary
+torch operations in 32 bits, in 64 where a rounding border is decided) or,
+where `own` is true, through the framework's call.  exact() computes the same
+outputs in 64 bits, written apart from both.
+
+Byte order of a cache block (one page and head, tokens t, dimensions d):
+ keys    [t/16][d/16][t%16][d%16]
+ values  [t/32][d/32][(t%16)/4][d%16][(d/16)%2][(t/16)%2][t%4]
+"""
+import math
+
+import numpy as np
+import torch
+
+own = False
+
+DEV = "cuda"
+
+
+# ------------------------------------------------------------------ the cases
+def listed():
+    return [
+        # one decode step of one stream: the norm before a projection, bf16 out for the 4-bit product
+        dict(name="norm decode", op="norm", M=1, K=4096, x="bf16", res="bf16", y=True, q=False, rot=False),
+        # a 32-row verification tile before the int8 product: rotated, int8 with row scales
+        dict(name="norm verify rotated", op="norm", M=32, K=12288, x="f32", res="f32", y=False, q=True, rot=True),
+        # a long prompt: bf16 and int8 outputs from one read
+        dict(name="norm prompt", op="norm", M=5003, K=7168, x="bf16", res="bf16", y=True, q=True, rot=False),
+        # one stream's draft of 16 tokens: the step where only latency counts
+        dict(name="tables draft", op="tables", R=1, page=64, len_max=4001, add_max=16, blocks=2048),
+        # a serving batch taking draft tiles and a few new prompts at once
+        dict(name="tables batch", op="tables", R=1024, page=32, len_max=30000, add_max=900, blocks=1024),
+        # a decode step of 64 streams, one token each, e4m3 codes
+        dict(name="append decode", op="append", R=64, page=64, len_max=255, add_max=1, Hkv=8, D=128, fmt="e4m3"),
+        # ragged prompts written at once
+        dict(name="append prompts", op="append", R=7, page=128, len_max=90, add_max=4001, Hkv=8, D=128, fmt="int8"),
+        # one stream early in its answer: launch latency
+        dict(name="attn short", op="attn", R=1, T=1, len_min=1021, len_max=1021, page=64, Hkv=8, G=4, D=128, fmt="int8", tree=False, window=0),
+        # one stream verifying a 16-token draft tree over a medium context
+        dict(name="attn tree", op="attn", R=1, T=16, len_min=20011, len_max=20011, page=64, Hkv=8, G=4, D=128, fmt="int8", tree=True, window=0),
+        # one stream, very long context, wide heads
+        dict(name="attn long", op="attn", R=1, T=1, len_min=131072, len_max=131072, page=128, Hkv=4, G=8, D=256, fmt="e4m3", tree=False, window=0),
+        # a ragged serving batch, one token each
+        dict(name="attn batch", op="attn", R=48, T=1, len_min=300, len_max=32768, page=64, Hkv=8, G=4, D=128, fmt="int8", tree=False, window=0),
+        # a batch of streams verifying 32-token drafts each: many rows a head
+        dict(name="attn verify", op="attn", R=9, T=32, len_min=2000, len_max=9001, page=32, Hkv=8, G=4, D=128, fmt="int8", tree=False, window=0),
+    ]
+
+
+def _log(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    op = rng.choice(["norm", "tables", "append", "attn", "attn"])
+    if op == "norm":
+        K = 32 * _log(rng, 1, 768)
+        M = max(1, min(_log(rng, 1, 8192), 5003 * 7168 // K))
+        y, q = rng.choice([(True, False), (False, True), (True, True)])
+        return dict(op=op, M=M, K=K, x=rng.choice(["bf16", "f32"]), res=rng.choice(["none", "bf16", "f32"]),
+                    y=y, q=q, rot=q and rng.random() < 0.5)
+    if op == "tables":
+        page = rng.choice([32, 64, 128, 256])
+        R = _log(rng, 1, 1024)
+        add = _log(rng, 1, 900)
+        ln = _log(rng, 1, 30000)
+        return dict(op=op, R=R, page=page, len_max=ln, add_max=add, blocks=(ln + add) // page + rng.randint(1, 100))
+    D = rng.choice([64, 128, 256])
+    page = rng.choice([32, 64, 128, 256])
+    fmt = rng.choice(["int8", "e4m3"])
+    if op == "append":
+        Hkv = _log(rng, 1, 16)
+        R = _log(rng, 1, 200)
+        add = _log(rng, 1, max(1, 7 * 4001 * 1024 // (R * Hkv * D)))
+        return dict(op=op, R=R, page=page, len_max=_log(rng, 1, 600), add_max=min(add, 8000), Hkv=Hkv, D=D, fmt=fmt)
+    R = _log(rng, 1, 48)
+    Hkv = _log(rng, 1, 8)
+    ln = min(_log(rng, 1, 131072), 48 * 32768 * 1024 // (R * Hkv * D))
+    G = rng.choice([1, 2, 3, 4, 5, 7, 8])
+    T = 1 if rng.random() < 0.4 else min(_log(rng, 2, 32), max(1, 48 * 32768 * 1024 * 4 // (R * Hkv * D * ln * G)))
+    tree = T > 1 and rng.random() < 0.5
+    return dict(op=op, R=R, T=T, len_min=rng.randint(1, ln), len_max=ln, page=page, Hkv=Hkv, G=G, D=D, fmt=fmt,
+                tree=tree, window=0 if tree else rng.choice([0, 0, 512]))
+
+
+# ------------------------------------------------------------------ inputs
+def _rng(seed, item=0):
+    return np.random.default_rng([int(seed), item])
+
+
+def _gen(seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(int(seed))
+    return g
+
+
+def _dt(name):
+    return {"bf16": torch.bfloat16, "f32": torch.float32}[name]
+
+
+def _lens(case, seed):
+    """Lengths of the requests before the step and their new tokens: the same
+    ones for every seed, in another order (so that sizes stay a case's own)."""
+    r = _rng(case["len_max"], case["R"])
+    R = case["R"]
+    old = np.exp(r.uniform(0, math.log(case["len_max"] + 1), R)).astype(np.int64) if R > 1 else np.array([case["len_max"]])
+    old = np.minimum(old, case["len_max"])
+    add = np.exp(r.uniform(0, math.log(case["add_max"] + 1), R)).astype(np.int64) if R > 1 else np.array([case["add_max"]])
+    add = np.clip(add, 1, case["add_max"])
+    if R > 1:
+        old[r.random(R) < 0.1] = 0      # requests that just came in
+        add[r.random(R) < 0.05] = 0     # and idle ones
+        old[0], add[0] = case["len_max"], case["add_max"]
+    order = _rng(seed).permutation(R)
+    return old[order], add[order]
+
+
+def _i32(a):
+    return torch.from_numpy(np.ascontiguousarray(a, dtype=np.int32)).to(DEV)
+
+
+def _codes(shape, fmt, g):
+    """Codes as a quantizer leaves them: int8 near a normal's, e4m3 likewise."""
+    n = math.prod(shape)
+    out = torch.empty(n, dtype=torch.uint8, device=DEV)
+    step = 1 << 27
+    for a in range(0, n, step):
+        b = min(n, a + step)
+        z = torch.randn(b - a, device=DEV, generator=g)
+        if fmt == "int8":
+            out[a:b] = z.mul_(40).round_().clamp_(-127, 127).to(torch.int8).view(torch.uint8)
+        else:
+            out[a:b] = z.mul_(140).clamp_(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+        del z
+    return out.view(torch.int8 if fmt == "int8" else torch.float8_e4m3fn).view(shape)
+
+
+def prepare(case, seed):
+    s = dict(case)
+    g = _gen(seed)
+    op = case["op"]
+    if op == "norm":
+        M, K = case["M"], case["K"]
+        x = torch.randn(M, K, device=DEV, generator=g)
+        x[:, :: max(1, K // 7)] *= 20  # outlier channels
+        s["xin"] = x.to(_dt(case["x"]))
+        if case["res"] != "none":
+            s["residual"] = (2 * torch.randn(M, K, device=DEV, generator=g)).to(_dt(case["res"]))
+            s["residual_out"] = torch.empty_like(s["residual"])
+        s["weight"] = (1 + 0.2 * torch.randn(K, device=DEV, generator=g)).to(torch.bfloat16)
+        if case["rot"]:
+            s["signs"] = (torch.randint(0, 2, (K,), device=DEV, generator=g) * 2 - 1).to(torch.int8)
+        s["yout"] = torch.empty(M, K, dtype=torch.bfloat16, device=DEV) if case["y"] else None
+        s["Xq"] = torch.empty(M, K, dtype=torch.int8, device=DEV) if case["q"] else None
+        s["x_scales"] = torch.empty(M, device=DEV) if case["q"] else None
+    elif op == "tables":
+        R, page, nb = case["R"], case["page"], case["blocks"]
+        old, add = _lens(case, seed)
+        have = -(-old // page)
+        pages = int(have.sum() + (-(-(old + add) // page) - have).sum()) + 37
+        perm = _rng(seed, 1).permutation(pages).astype(np.int32)
+        table = np.full((R, nb), -1, np.int32)
+        table[np.arange(nb)[None, :] < have[:, None]] = perm[: have.sum()]
+        free = np.full(pages, -1, np.int32)
+        free[: pages - have.sum()] = perm[have.sum():]
+        s.update(lens=_i32(old), add=_i32(add), keep=_i32(old), table=_i32(table), free_pages=_i32(free),
+                 free_count=_i32([pages - have.sum()]), none=_i32(np.zeros(R)), max_tokens=int(add.sum()) + 5)
+        for k, n in (("q_start", R + 1), ("slots", s["max_tokens"]), ("positions", s["max_tokens"]), ("status", 1)):
+            s[k] = torch.empty(n, dtype=torch.int32, device=DEV)
+            s[k + "_back"] = torch.empty(n if k in ("q_start", "status") else 1, dtype=torch.int32, device=DEV)
+    elif op == "append":
+        page, Hkv, D = case["page"], case["Hkv"], case["D"]
+        old, add = _lens(case, seed)
+        need = -(-(old + add) // page)
+        pages = int(need.sum()) + 5
+        perm = _rng(seed, 1).permutation(pages)
+        first = np.concatenate([[0], np.cumsum(need)])
+        slots = [perm[first[r] + p // page] * page + p % page
+                 for r, p in ((r, np.arange(old[r], old[r] + add[r])) for r in range(case["R"]))]
+        slots = np.concatenate(slots + [np.full(2, -1)])  # two rows of padding, as in a captured step
+        M = len(slots)
+        kv = torch.randn(M, 2, Hkv, D, device=DEV, generator=g)
+        kv[:, 0, :, :: max(1, D // 3)] *= 6  # keys have outlier channels
+        s["kv"] = kv.to(torch.bfloat16)      # one buffer, as a joint projection writes it
+        s["slots"] = _i32(slots)
+        for n in ("k", "v"):
+            s[n] = _codes((pages, Hkv, page, D), case["fmt"], g)
+            s[n + "_scales"] = torch.rand(pages, Hkv, device=DEV, generator=g) * (0.04 if case["fmt"] == "int8" else 0.01)
+    else:
+        R, page, Hkv, G, D = (case[k] for k in ("R", "page", "Hkv", "G", "D"))
+        r = _rng(case["len_max"], R)
+        ln = np.exp(r.uniform(math.log(case["len_min"]), math.log(case["len_max"]), R)).astype(np.int64)
+        ln = np.clip(ln, case["len_min"], case["len_max"])
+        ln[-1] = case["len_max"]
+        T = np.full(R, case["T"])
+        T[1:] = np.where(r.random(R - 1) < 0.7, case["T"], r.integers(1, case["T"] + 1, R - 1))
+        T = np.minimum(T, ln)
+        r = _rng(seed)
+        order = r.permutation(R)
+        ln, T = ln[order], T[order]
+        nb = -(-ln // page)
+        pages = int(nb.sum()) + 3
+        perm = r.permutation(pages)
+        cols = int(nb.max())
+        table = np.full((R, cols), -1, np.int32)
+        table[np.arange(cols)[None, :] < nb[:, None]] = perm[: nb.sum()]
+        q_start = np.concatenate([[0], np.cumsum(T)])
+        M = int(q_start[-1])
+        s.update(lens=_i32(ln), q_start=_i32(q_start), table=_i32(table), M=M, cols=cols, max_q=int(T.max()))
+        s["q"] = torch.randn(M, Hkv * G, D, device=DEV, generator=g).to(torch.bfloat16)
+        for n in ("k", "v"):
+            s[n] = _codes((pages, Hkv, page, D), case["fmt"], g)
+            s[n + "_scales"] = (0.5 + torch.rand(pages, Hkv, device=DEV, generator=g)) * (0.025 if case["fmt"] == "int8" else 0.007)
+        if case["tree"]:  # random trees: each draft token's parent is an earlier one, or the context
+            masks = []
+            for n in T:
+                seen = []
+                for j in range(n):
+                    p = int(r.integers(-1, j)) if j else -1
+                    seen.append((seen[p] if p >= 0 else 0) | (1 << j))
+                masks += seen
+            s["tree_mask"] = _i32(np.array(masks, dtype=np.uint32).view(np.int32))
+        s["out"] = torch.empty(M, Hkv * G, D, dtype=torch.bfloat16, device=DEV)
+    return s
+
+
+# ------------------------------------------------------------------ one pass
+def run(s):
+    if own:
+        return _run_own(s)
+    return {"norm": _norm, "tables": _tables, "append": _append, "attn": _attn}[s["op"]](s)
+
+
+def _run_own(s):
+    import quantized_weight_decode_dequant_amd as qg
+    if s["op"] == "norm":
+        qg.rmsnorm_quant_run(s["xin"], s["weight"], 1e-6, residual=s.get("residual"), residual_out=s.get("residual_out"),
+                             signs=s.get("signs"), y=s["yout"], Xq=s["Xq"], x_scales=s["x_scales"])
+        return [t for t in (s.get("residual_out"), s["yout"], s["Xq"], s["x_scales"]) if t is not None]
+    if s["op"] == "tables":
+        # a step's new tokens, then all of them rolled back (every draft rejected, every prompt given up)
+        qg.kv_tables_run(s["page"], s["lens"], s["add"], s["table"], s["free_pages"], s["free_count"], s["max_tokens"],
+                         q_start=s["q_start"], slots=s["slots"], positions=s["positions"], status=s["status"])
+        qg.kv_tables_run(s["page"], s["lens"], s["none"], s["table"], s["free_pages"], s["free_count"], 0, keep=s["keep"],
+                         q_start=s["q_start_back"], slots=s["slots_back"], positions=s["positions_back"], status=s["status_back"])
+        return [s[k] for k in ("q_start", "slots", "positions", "status", "lens", "table", "free_pages", "free_count", "q_start_back", "status_back")]
+    cache = qg.KVCache(s["k"], s["v"], s["k_scales"], s["v_scales"])
+    if s["op"] == "append":
+        qg.kv_append_run(cache, s["kv"][:, 0], s["kv"][:, 1], s["slots"])
+        return [s["k"], s["v"], s["k_scales"], s["v_scales"]]
+    return qg.kv_attention_run(cache, s["q"], s["q_start"], s["lens"], s["table"], s["max_q"], max_len=s["len_max"],
+                               tree_mask=s.get("tree_mask"), window=s["window"], out=s["out"])
+
+
+def _h32():
+    i = torch.arange(32, device=DEV)
+    b = i[:, None] & i[None, :]
+    parity = sum((b >> k) & 1 for k in range(5)) % 2
+    return (1 - 2 * parity).double()
+
+
+def _norm(s):
+    M, K = s["M"], s["K"]
+    out = []
+    r = s["xin"].float()
+    if "residual" in s:
+        r = r + s["residual"].float()
+        out.append(r.to(s["residual"].dtype))
+    rs = torch.rsqrt((r * r).mean(1, keepdim=True) + 1e-6)
+    if s["y"]:
+        out.append((r * rs * s["weight"].float()).to(torch.bfloat16))
+    if s["q"]:
+        # the codes do not depend on rs; 64 bits, so that no value falls on the wrong side of a border
+        z = s["xin"].double()
+        if "residual" in s:
+            z = z + s["residual"].double()
+        z = z * s["weight"].double()
+        if s["rot"]:
+            z = ((z * s["signs"].double()).view(M, K // 32, 32) @ _h32()).view(M, K)
+        amax = z.abs().amax(1, keepdim=True)
+        out.append(torch.where(amax > 0, torch.round(z * 127 / amax), 0.0).to(torch.int8))
+        out.append((amax.float() * rs / (127 * math.sqrt(32) if s["rot"] else 127)).view(M))
+    return out
+
+
+def _tables_once(s, lens, add, keep, max_tokens):
+    """New lengths, table, free list and maps after one step; nothing changes where it cannot be done."""
+    R, page, nbmax = s["R"], s["page"], s["blocks"]
+    kept = torch.minimum(keep.clamp(min=0), lens).long() if keep is not None else lens.long()
+    add = add.clamp(min=0).long()
+    new = kept + add
+    have, want = (lens.long() + page - 1) // page, (new + page - 1) // page
+    free, n = s["free_pages"], s["free_count"].long()
+    rel, get = (have - want).clamp(min=0), (want - have).clamp(min=0)
+    rel0, get0 = rel.cumsum(0) - rel, get.cumsum(0) - get
+    Rel, A = rel.sum(), get.sum()
+    q_start = torch.cat([torch.zeros_like(add[:1]), add.cumsum(0)])
+    status = (A > n + Rel).int() + 2 * (want > nbmax).any().int() + 4 * (q_start[-1] > max_tokens).int()
+    ok = status.view(1) == 0
+    col = torch.arange(nbmax, device=DEV)[None, :]
+    leaves = ok & (col >= want[:, None]) & (col < have[:, None])
+    comes = ok & (col >= have[:, None]) & (col < want[:, None])
+    i = torch.where(leaves, rel0[:, None] + col - want[:, None], free.numel())
+    released = torch.full((free.numel() + 1,), -1, dtype=torch.int32, device=DEV)
+    released.scatter_(0, i.view(-1), s["table"].view(-1))
+    j = get0[:, None] + col - have[:, None]
+    taken = torch.where(j < Rel, released[j.clamp(0, free.numel())], free[(n - 1 - (j - Rel)).clamp(0, free.numel() - 1)])
+    table = torch.where(comes, taken, torch.where(leaves, -1, s["table"]))
+    # what nobody took goes back on the list, the first released on top
+    k = torch.arange(free.numel(), device=DEV)
+    back = n + Rel - 1 - k
+    free = torch.where(ok & (back >= A) & (back < Rel), released[back.clamp(0, free.numel())], free)
+    count = torch.where(ok, n + Rel - A, n).int()
+    q_start = torch.where(ok, q_start, 0)
+    t = torch.arange(max_tokens, device=DEV)
+    r = torch.searchsorted(q_start[1:].contiguous(), t, right=True)
+    valid = r < R
+    r = r.clamp(max=R - 1)
+    pos = kept[r] + t - q_start[r]
+    slot = table[r, (pos // page).clamp(0, nbmax - 1)].long() * page + pos % page
+    slots, positions = torch.where(valid, slot, -1).int(), torch.where(valid, pos, 0).int()
+    return torch.where(ok, new, lens.long()).int(), table, free, count, q_start.int(), slots, positions, status.view(1)
+
+
+def _tables(s):
+    lens, table, free, count, q_start, slots, positions, status = _tables_once(s, s["lens"], s["add"], None, s["max_tokens"])
+    s = dict(s, table=table, free_pages=free, free_count=count)
+    lens, table, free, count, q_back, _, _, status_back = _tables_once(s, lens, s["none"], s["keep"], 0)
+    return [q_start, slots, positions, status, lens, table, free, count, q_back, status_back]
+
+
+def _rows_k(c, D):
+    """Key blocks [..., page, D] in the cache's byte order -> row-major."""
+    lead, page = c.shape[:-2], c.shape[-2]
+    n = len(lead)
+    c = c.reshape(*lead, page // 16, D // 16, 16, 16)
+    return c.permute(*range(n), n, n + 2, n + 1, n + 3).reshape(*lead, page, D)
+
+
+def _rows_v(c, D):
+    """Value blocks in the cache's byte order -> row-major."""
+    lead, page = c.shape[:-2], c.shape[-2]
+    n = len(lead)
+    c = c.reshape(*lead, page // 32, D // 32, 4, 16, 2, 2, 4)
+    return c.permute(*range(n), n, n + 5, n + 2, n + 6, n + 1, n + 4, n + 3).reshape(*lead, page, D)
+
+
+def _tiles_k(c, D):
+    """Row-major key blocks -> the cache's byte order."""
+    lead, page = c.shape[:-2], c.shape[-2]
+    n = len(lead)
+    c = c.reshape(*lead, page // 16, 16, D // 16, 16)
+    return c.permute(*range(n), n, n + 2, n + 1, n + 3).reshape(*lead, page, D)
+
+
+def _tiles_v(c, D):
+    """Row-major value blocks -> the cache's byte order."""
+    lead, page = c.shape[:-2], c.shape[-2]
+    n = len(lead)
+    c = c.reshape(*lead, page // 32, 2, 4, 4, D // 32, 2, 16)
+    return c.permute(*range(n), n, n + 4, n + 2, n + 6, n + 5, n + 1, n + 3).reshape(*lead, page, D)
+
+
+def _append(s):
+    page, Hkv, D, int8 = s["page"], s["Hkv"], s["D"], s["fmt"] == "int8"
+    top = 127.0 if int8 else 448.0
+    pages = s["k"].shape[0]
+    slots = s["slots"].long()
+    at = torch.where(slots >= 0, slots // page, pages)  # row `pages` takes what is skipped
+    fresh = torch.zeros(pages + 1, dtype=torch.int32, device=DEV).scatter_reduce(0, at, (slots % page == 0).int(), "amax")[:pages] > 0
+    # whole pages are requantized: the tokens' own pages where those are few, else all
+    few = len(slots) < min(pages, 257)
+    idx = at.clamp(max=pages - 1) if few else torch.arange(pages, device=DEV)
+    out = []
+    for name, x in (("k", s["kv"][:, 0]), ("v", s["kv"][:, 1])):
+        x = x.float()
+        codes, scales = s[name], s[name + "_scales"]
+        amax = torch.zeros(pages + 1, Hkv, device=DEV).scatter_reduce(0, at[:, None].expand(-1, Hkv), x.abs().amax(2), "amax")[:pages]
+        amax = torch.where(amax < 2.0 ** -100, 0.0, amax)
+        old = torch.where(fresh[:, None], 0.0, scales)
+        touched = torch.zeros(pages + 1, dtype=torch.bool, device=DEV).scatter(0, at, True)[:pages, None]
+        new = torch.where(touched, torch.maximum(old, amax / top), scales)
+        grown = touched & (new > old) & ~fresh[:, None]
+        ratio = torch.where(grown, old / new, 1.0)[idx][:, :, None, None]
+        rows = (_rows_k if name == "k" else _rows_v)(codes.view(torch.uint8)[idx], D).view(codes.dtype).float() * ratio
+        rows = torch.where(grown[idx][:, :, None, None], rows.round() if int8 else rows, rows).to(codes.dtype)
+        inv = torch.where(new > 0, 1.0 / new, 0.0)
+        z = x * torch.cat([inv, inv[:1]])[at][:, :, None]
+        z = (z.round() if int8 else z).clamp(-top, top).to(codes.dtype).view(torch.uint8)
+        # the tokens' rows, into their pages: row r of `rows` is page idx[r]
+        rows = rows.view(torch.uint8)
+        codes8 = codes.view(torch.uint8)
+        if few:
+            # one page for each token, with all of the page's tokens in it
+            same = (at[:, None] == at[None, :]) & (slots >= 0)[:, None]
+            off = torch.where(same, (slots % page)[None, :], page)
+            pad = torch.cat([rows, torch.zeros_like(rows[:, :, :1])], 2)
+            pad.scatter_(2, off[:, None, :, None].expand(-1, Hkv, -1, D), z.permute(1, 0, 2)[None].expand(len(slots), -1, -1, -1))
+            rows = pad[:, :, :page]
+        else:
+            pad = torch.cat([rows, torch.zeros_like(rows[:1])])
+            pad[at, :, slots % page] = z
+            rows = pad[:pages]
+        tiles = (_tiles_k if name == "k" else _tiles_v)(rows, D)
+        kept = torch.where(touched[idx][:, :, None, None], tiles, codes8[idx])
+        target = torch.where(slots >= 0, at, pages) if few else idx
+        codes8.copy_(torch.cat([codes8, codes8[:1]]).index_copy(0, target, kept)[:pages])
+        scales.copy_(new)
+        out += [codes, scales]
+    return [out[0], out[2], out[1], out[3]]
+
+
+def _attn(s):
+    R, page, Hkv, G, D, M, T, cols = (s[k] for k in ("R", "page", "Hkv", "G", "D", "M", "max_q", "cols"))
+    L = cols * page
+    ids = s["table"].clamp(min=0).long()
+    K = _rows_k(s["k"].view(torch.uint8)[ids], D).view(s["k"].dtype).transpose(1, 2).reshape(R, Hkv, L, D).float()
+    ks = s["k_scales"][ids].transpose(1, 2).repeat_interleave(page, 2, output_size=L)
+    q0, ln = s["q_start"][:-1].long(), s["lens"].long()
+    n = s["q_start"][1:].long() - q0
+    j = torch.arange(T, device=DEV)
+    row = (q0[:, None] + j).clamp(max=M - 1)
+    q = s["q"].float()[row].view(R, T, Hkv, G, D).transpose(1, 2).reshape(R, Hkv, T * G, D)
+    S = (q @ K.transpose(2, 3)) * (ks[:, :, None, :] / math.sqrt(D))
+    del K
+    base = (ln - n)[:, None, None]  # tokens before this step's
+    t = torch.arange(L, device=DEV)
+    pos = base + j[None, :, None]
+    see = (t <= pos) & (t < ln[:, None, None])
+    if s["tree"]:
+        bits = s["tree_mask"].long()[row][:, :, None] >> (t - base).clamp(0, 31)
+        see = (t < base) | (((bits & 1) > 0) & (t < ln[:, None, None]))
+    if s["window"]:
+        see = see & (t > pos - s["window"])
+    see = see[:, None, :, None, :].expand(R, 1, T, G, L).reshape(R, 1, T * G, L)
+    S = torch.where(see, S, -math.inf)
+    m = S.amax(3, keepdim=True)
+    P = torch.exp(S - torch.where(m == -math.inf, 0.0, m))
+    l = P.sum(3, keepdim=True)
+    V = _rows_v(s["v"].view(torch.uint8)[ids], D).view(s["v"].dtype).transpose(1, 2).reshape(R, Hkv, L, D).float()
+    vs = s["v_scales"][ids].transpose(1, 2).repeat_interleave(page, 2, output_size=L)
+    o = (P * vs[:, :, None, :]) @ V
+    o = torch.where(l > 0, o / l, 0.0).view(R, Hkv, T, G, D).transpose(1, 2).reshape(R * T, Hkv * G, D)
+    # padded rows go to a spare last one
+    to = torch.where(j < n[:, None], q0[:, None] + j, M).view(-1)
+    return torch.zeros(M + 1, Hkv * G, D, dtype=torch.bfloat16, device=DEV).index_copy(0, to, o.to(torch.bfloat16))[:M]
+
+
+# ------------------------------------------------------------------ what a pass needs
+def work(case):
+    op = case["op"]
+    if op == "norm":
+        n = case["M"] * case["K"]
+        size = {"none": 0, "bf16": 2, "f32": 4}
+        b = n * (size[case["x"]] + 2 * size[case["res"]] + 2 * case["y"] + case["q"]) + case["K"] * (2 + case["rot"]) + 4 * case["M"] * case["q"]
+        return {"bytes": b, "flops": n * (6 + 4 * case["q"] + 6 * case["rot"])}
+    mean = lambda lo, hi: hi if lo == hi else (hi - lo) / math.log(hi / lo)  # noqa: E731  of a log-uniform length
+    if op == "tables":
+        add = case["R"] * mean(1, case["add_max"] + 1)
+        return {"bytes": case["R"] * 4 * 8 + add * 8 + 24 * add / case["page"], "flops": 0}
+    if op == "append":
+        add = case["R"] * (case["add_max"] if case["R"] == 1 else mean(1, case["add_max"] + 1))
+        return {"bytes": add * case["Hkv"] * case["D"] * 2 * 3 + add * 4, "flops": add * case["Hkv"] * case["D"] * 2 * 4}
+    tokens = case["R"] * (case["len_max"] if case["R"] == 1 else mean(case["len_min"], case["len_max"]))
+    if case["window"]:
+        tokens = min(tokens, case["R"] * (case["window"] + case["T"]))
+    b = tokens * case["Hkv"] * case["D"] * 2 + case["R"] * case["T"] * case["Hkv"] * case["G"] * case["D"] * 4
+    return {"bytes": b, "flops": 4 * tokens * case["T"] * case["Hkv"] * case["G"] * case["D"]}
+
+
+# ------------------------------------------------------------------ the definition, in 64 bits
+def exact(case, seed):
+    s = prepare(case, seed)
+    return {"norm": _norm64, "tables": lambda s: None, "append": _append64, "attn": _attn64}[case["op"]](s)
+
+
+def _norm64(s):
+    v = s["xin"].double()
+    out = []
+    if "residual" in s:
+        v += s["residual"].double()
+        out.append(v.clone())
+    mean = torch.einsum("mk,mk->m", v, v) / s["K"]
+    scale = (mean + 1e-6) ** -0.5
+    w = s["weight"].double()
+    if s["y"]:
+        out.append(v * w * scale[:, None])
+    if s["q"]:
+        v = v * w
+        if s["rot"]:
+            v = v * s["signs"].double()
+            for h in (1, 2, 4, 8, 16):  # butterflies
+                a = v.view(s["M"], -1, 2, h)
+                v = torch.stack([a[:, :, 0] + a[:, :, 1], a[:, :, 0] - a[:, :, 1]], 2).view(s["M"], s["K"])
+        top = v.abs().max(1).values
+        out += [None, top * scale / 127 / (32 ** 0.5 if s["rot"] else 1)]
+    return out
+
+
+def _place(page, D, value):
+    """Byte offset of (token, dimension) in a block."""
+    t, d = np.arange(page)[:, None], np.arange(D)[None, :]
+    if not value:
+        off = (t // 16) * 16 * D + (d // 16) * 256 + (t % 16) * 16 + d % 16
+    else:
+        off = (t // 32) * 32 * D + (d // 32) * 1024 + (t % 16 // 4) * 256 + (d % 16) * 16 + (d // 16 % 2) * 8 + (t // 16 % 2) * 4 + t % 4
+    return torch.from_numpy(off.reshape(-1)).to(DEV)
+
+
+def _grid(v, int8):
+    """The nearest code's value, in 64 bits."""
+    if int8:
+        return v.round().clamp(-127, 127)
+    v = v.clamp(-448, 448)
+    e = torch.floor(torch.log2(v.abs().clamp(min=2.0 ** -30))).clamp(min=-6)
+    ulp = 2.0 ** (e - 3)
+    return torch.round(v / ulp) * ulp
+
+
+def _append64(s):
+    page, Hkv, D, int8 = s["page"], s["Hkv"], s["D"], s["fmt"] == "int8"
+    top = 127.0 if int8 else 448.0
+    slots = s["slots"].cpu().numpy()
+    runs = []
+    for m, slot in enumerate(slots):
+        if slot < 0:
+            continue
+        if runs and slot == runs[-1][1] + runs[-1][2] and slot % page:
+            runs[-1][2] += 1
+        else:
+            runs.append([m, int(slot), 1])
+    out = []
+    for n, name in enumerate(("k", "v")):
+        place = _place(page, D, name == "v")
+        codes = s[name].double().view(-1, Hkv, page * D).clone()
+        scales = s[name + "_scales"].double().clone()
+        for m, slot, count in runs:
+            p, o = slot // page, slot % page
+            x = s["kv"][m:m + count, n].double()                              # [count, Hkv, D]
+            peak = x.abs().amax((0, 2)) / top
+            before = scales[p] if o else torch.zeros_like(peak)
+            now = torch.maximum(before, peak)
+            block = codes[p][:, place].view(Hkv, page, D)
+            grown = (now > before)[:, None, None] & (o > 0)
+            block = torch.where(grown, _grid(block * (before / now)[:, None, None], int8), block)
+            block[:, o:o + count] = _grid(x / now[None, :, None], int8).transpose(0, 1)
+            codes[p] = codes[p].scatter(1, place.expand(Hkv, -1), block.reshape(Hkv, -1))
+            scales[p] = now
+        out.append((codes.view(s[name].shape), scales))
+    return [None if int8 else out[0][0], None if int8 else out[1][0], out[0][1], out[1][1]]
+
+
+def _attn64(s):
+    R, page, Hkv, G, D = (s[k] for k in ("R", "page", "Hkv", "G", "D"))
+    start, lens = s["q_start"].tolist(), s["lens"].tolist()
+    pk, pv = _place(page, D, False), _place(page, D, True)
+    out = torch.zeros(s["M"], Hkv * G, D, dtype=torch.float64, device=DEV)
+    for r in range(R):
+        a, b, n = start[r], start[r + 1], lens[r]
+        T = b - a
+        ids = s["table"][r, : -(-n // page)].long()
+        t = torch.arange(n, device=DEV)
+        j = torch.arange(T, device=DEV)[:, None]
+        if s["tree"]:
+            new = t[None, :] - (n - T)
+            seen = torch.where(new < 0, 1, (s["tree_mask"][a:b].long()[:, None] >> new.clamp(min=0)) & 1).bool()
+        else:
+            seen = t[None, :] <= n - T + j
+            if s["window"]:
+                seen = seen & (t[None, :] + s["window"] > n - T + j)
+        for h in range(Hkv):
+            k = (s["k"].view(torch.uint8)[ids, h].view(len(ids), -1)[:, pk].view(s["k"].dtype).double().view(-1, page, D)
+                 * s["k_scales"][ids, h].double()[:, None, None]).view(-1, D)[:n]
+            v = (s["v"].view(torch.uint8)[ids, h].view(len(ids), -1)[:, pv].view(s["v"].dtype).double().view(-1, page, D)
+                 * s["v_scales"][ids, h].double()[:, None, None]).view(-1, D)[:n]
+            q = s["q"][a:b, h * G:(h + 1) * G].double().reshape(T * G, D)
+            w = torch.mm(q, k.t().contiguous()) * D ** -0.5
+            w = w.masked_fill(~seen.repeat_interleave(G, 0), -math.inf)
+            out[a:b, h * G:(h + 1) * G] = torch.mm(torch.softmax(w, 1), v).view(T, G, D)
+    return out
