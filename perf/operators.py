@@ -254,7 +254,9 @@ def _run_own(s):
         qg.kv_tables_run(s["page"], s["lens"], s["none"], s["table"], s["free_pages"], s["free_count"], 0, keep=s["keep"],
                          q_start=s["q_start_back"], slots=s["slots_back"], positions=s["positions_back"], status=s["status_back"])
         return [s[k] for k in ("q_start", "slots", "positions", "status", "lens", "table", "free_pages", "free_count", "q_start_back", "status_back")]
-    cache = qg.KVCache(s["k"], s["v"], s["k_scales"], s["v_scales"])
+    if "cache" not in s:  # the handle a program makes once for a layer
+        s["cache"] = qg.KVCache(s["k"], s["v"], s["k_scales"], s["v_scales"])
+    cache = s["cache"]
     if s["op"] == "append":
         qg.kv_append_run(cache, s["kv"][:, 0], s["kv"][:, 1], s["slots"])
         return [s["k"], s["v"], s["k_scales"], s["v_scales"]]
