@@ -460,6 +460,194 @@ int qg_batch_run(const qg_batch_plan *plan, void *stream);
  */
 int qg_plain_read(const void *buf, size_t bytes, uint32_t *sink, int grid, void *stream);
 
+/*
+ * rmsnorm_quant_run -- the norm in front of a decode step's products, with
+ * the residual's addition: per row of K values
+ *     r = x + residual,  rs = 1 / sqrt(mean(r^2) + eps),  y = r * rs * weight
+ * written as bf16 (what the 4-bit products read), as int8 with one scale per
+ * row (what qgemm_skinny_run(QG_FMT_Q8_SYM_G32) reads), or both.  The int8
+ * output quantizes z = r * weight (unrounded), or its block-diagonal
+ * randomized Hadamard-32 rotation as in hadamard32_quant_run when `signs` is
+ * given: amax = max |z|, Xq = round-half-even(z * 127 / amax) decided in
+ * fp64, x_scales = amax * rs / 127 (/ sqrt(32) when rotated), so that
+ * x_scales * Xq approximates y (or its orthonormal rotation).
+ *
+ *  x            device [M][K], bf16 (x_dtype = QG_OUT_BF16) or fp32
+ *               (QG_OUT_F32), 16-B.  Read only.
+ *  residual     device [M][K] of res_dtype, 16-B, or NULL (r = x).
+ *  residual_out device [M][K] of res_dtype, 16-B, receives r rounded to it;
+ *               may be `residual` itself.  NULL: not written.  Must be NULL
+ *               when residual is.
+ *  weight       device bf16 [K], 16-B.
+ *  eps          > 0, finite.
+ *  signs        device int8 [K], 16-B, each +1 or -1, or NULL (no rotation);
+ *               NULL when Xq is.
+ *  M, K         M >= 0; K a multiple of 32, 32..24576.
+ *  y            device bf16 [M][K], 16-B, or NULL.
+ *  Xq, x_scales device int8 [M][K], 16-B, and fp32 [M], or both NULL; one of
+ *               y and Xq is required.
+ * The sum of squares is fp32.  A row of zeros gives Xq = 0, scale 0; a row
+ * whose sum of squares is not finite gives Xq = 0 and scale NaN.  Outputs may
+ * not overlap each other or the inputs, residual_out = residual apart.
+ * Errors: QG_EINVAL, QG_ESHAPE, QG_EALIGN, QG_EUNSUPPORTED (QG_OUT_I32_GROUPS
+ * as a type), QG_EHIP.
+ */
+int rmsnorm_quant_run(const void *x, int x_dtype, const void *residual, void *residual_out,
+                      int res_dtype, const void *weight, float eps, const int8_t *signs,
+                      int64_t M, int64_t K, void *y, int8_t *Xq, float *x_scales, void *stream);
+
+/*
+ * A cache of keys and values in 8 bits, in pages.
+ *
+ * A decode pass reads the weights and the cache ("Real engines fall below the
+ * ceiling because each pass also reads the KV cache": Uzu page, section "Why
+ * batch-one decoding is memory-bound").  The cache is a pool of pages of 32,
+ * 64, 128 or 256 tokens; request r's token p lies in page table[r][p / page]
+ * at place p % page, i.e. in slot table[r][p / page] * page + p % page.  Each
+ * (page, KV head) block holds page * D one-byte codes with one fp32 scale:
+ *  - QG_KV_INT8: int8 codes in [-127, 127], value = scale * code;
+ *  - QG_KV_E4M3: OCP E4M3 codes, value = scale * code.
+ * Byte order of a block (token t of the page, dimension d), chosen for
+ * 128-bit loads that are matrix-core operands:
+ *  - keys   [t/16][d/16][t%16][d%16]
+ *  - values [t/32][d/32][(t%16)/4][d%16][(d/16)%2][(t/16)%2][t%4]
+ * One struct describes one layer's cache; the block tables and slot maps are
+ * shared by all layers.
+ */
+typedef enum { QG_KV_INT8 = 0, QG_KV_E4M3 = 1 } qg_kv_format;
+
+typedef struct qg_kv_cache {
+    void *k, *v;                  /* device codes [pages][Hkv][page * D], 16-B */
+    float *k_scales, *v_scales;   /* device fp32 [pages][Hkv] */
+    int64_t pages;                /* >= 1, pages * page < 2^31 */
+    int32_t page;                 /* 32, 64, 128 or 256 */
+    int32_t Hkv;                  /* 1..1024 */
+    int32_t D;                    /* head dimension: 64, 128 or 256 */
+    int32_t fmt;                  /* a qg_kv_format */
+} qg_kv_cache;
+
+/*
+ * kv_tables_run -- one step of the cache's bookkeeping, on the GPU: block
+ * tables, slot map and lengths from the requests' lengths, with no value read
+ * back.  Request r keeps the first min(keep[r], lens[r]) of its tokens and
+ * gets add[r] new ones; pages are taken from, and given back to, a stack of
+ * free pages.  A decode step is add = 1, a verification tile add = T with the
+ * next step's keep dropping the rejected drafts, a prompt add = its length, a
+ * finished request keep = 0, add = 0.
+ *
+ *  R            requests, 0..4096.
+ *  page, pages  as in qg_kv_cache.
+ *  max_blocks   columns of the table, >= 1; max_blocks * page <= 2^30.
+ *  max_tokens   entries of slots and positions, >= 0.
+ *  lens         device int32 [R], in/out: tokens held.
+ *  keep         device int32 [R], or NULL (keep all).  Read only.
+ *  add          device int32 [R].  Read only; negative values count as 0.
+ *  table        device int32 [R][max_blocks], in/out: page ids; entries of
+ *               released pages become -1, others are left as they are.
+ *  free_pages   device int32 [pages], in/out: the stack of free pages.
+ *  free_count   device int32 [1], in/out: how many it holds.
+ *  q_start      device int32 [R + 1], written: prefix sums of add.
+ *  slots        device int32 [max_tokens], written: the slot of each new
+ *               token, requests in order; -1 behind the last one.
+ *  positions    device int32 [max_tokens], written: its position in its
+ *               request; 0 behind the last one.
+ *  status       device int32 [1], written: 0, or a sum of 1 (not enough free
+ *               pages, or a free_count that cannot be), 2 (a request longer
+ *               than max_blocks pages), 4 (more than max_tokens new tokens).
+ * With a status other than 0 nothing is changed: lens, table and the free
+ * list stay, q_start is all 0 and slots all -1, so that the calls below, run
+ * behind it, do nothing.  With the requests in order and a request's pages in
+ * order, wanted page j is released page j while there is one, then the
+ * stack's next; the released pages nobody takes go back so that the first of
+ * them is on top.  A release right after an extension restores the list.
+ * The buffers may not overlap.
+ * Errors: QG_EINVAL, QG_ESHAPE, QG_EALIGN, QG_EHIP.
+ */
+int kv_tables_run(int64_t R, int64_t page, int64_t pages, int64_t max_blocks, int64_t max_tokens,
+                  int32_t *lens, const int32_t *keep, const int32_t *add, int32_t *table,
+                  int32_t *free_pages, int32_t *free_count, int32_t *q_start, int32_t *slots,
+                  int32_t *positions, int32_t *status, void *stream);
+
+/*
+ * kv_append_run -- write M tokens' keys and values into the cache in 8 bits.
+ * For each (page, KV head) touched: s = max(s_old, amax / top) with amax over
+ * the new tokens, top = 127 (int8) or 448 (E4M3), and s_old = the block's
+ * scale, or 0 if the first of the new tokens is the page's first; the new
+ * codes are x * (1 / s) rounded to nearest even; if s grew, the block's codes
+ * become code * (s_old / s), rounded likewise.  Every quotient and product is
+ * one fp32 operation.
+ *
+ *  cache        written.
+ *  M            tokens, 0..2^30.
+ *  K, V         device bf16 [M][Hkv][D], 16-B; token m at K + m * k_stride
+ *               elements (a multiple of 8, at least Hkv * D), so a joint
+ *               projection's output can be given as it is.  Read only.
+ *  slots        device int32 [M] (kv_tables_run's).  Tokens of one page must
+ *               be neighbours with slots that rise by 1; a slot outside
+ *               [0, pages * page) is skipped.
+ * amax is over finite values; infinities are stored as the largest code, NaN
+ * as 0.  A block whose amax is below 2^-100 is stored as zeros.  Two calls
+ * that write the same page must not overlap in time.
+ * Errors: QG_EINVAL, QG_ESHAPE, QG_EALIGN, QG_EHIP.
+ */
+int kv_append_run(const qg_kv_cache *cache, int64_t M, const void *K, int64_t k_stride,
+                  const void *V, int64_t v_stride, const int32_t *slots, void *stream);
+
+/*
+ * Bytes of workspace kv_attention_run needs (0 where a request's tokens are
+ * not split).  Pure host function; 0 for arguments the call would refuse.
+ */
+size_t qg_kv_attention_workspace_bytes(int64_t R, int64_t M, int64_t Hq, int64_t Hkv, int64_t D,
+                                       int64_t page, int64_t max_q, int64_t max_len,
+                                       int64_t window);
+
+/*
+ * kv_attention_run -- attention of 1..32 new tokens a request over its cached
+ * tokens: one decode step, or the verification of a draft ("Producing several
+ * tokens from one model pass", Uzu page).  Query token j of request r (row
+ * q_start[r] + j, T = q_start[r + 1] - q_start[r] of them) is the token at
+ * position lens[r] - T + j, whose key and value are in the cache already:
+ *     o = softmax_t(scale * q . k_t) over the visible t, times v_t.
+ * Visible are t <= its position (and > its position - window, if window > 0),
+ * or, with a tree, all tokens before the new ones and those of the new ones
+ * whose bit is set in the query token's mask.  A row that sees nothing is 0.
+ * Query head i reads KV head i / (Hq / Hkv).
+ *
+ *  cache        read only.
+ *  R, M         requests, 0..65535, and rows of q and out, 0..2^30.
+ *  Hq           query heads, a multiple of Hkv, at most 8192.
+ *  q            device bf16 [M][Hq][D], 16-B; rows q_stride elements apart (a
+ *               multiple of 8, at least Hq * D).
+ *  q_start      device int32 [R + 1], ascending, the last at most M.
+ *  lens         device int32 [R]: tokens held, the new ones included.
+ *  table        device int32 [R][max_blocks]; a page id outside [0, pages)
+ *               is not attended to.  max_blocks * page <= 2^30.
+ *  tree_mask    device uint32 [M] or NULL: bit i = the request's new token i.
+ *  window       0 (none), or 1..2^30; with tree_mask: 0 only.
+ *  scale        of the scores, finite; usually 1 / sqrt(D).
+ *  max_q        1..32: no request has more new tokens.  Rows past it are not
+ *               computed.
+ *  max_len      1..max_blocks * page: no request is longer.  A longer one may
+ *               get rows of NaN.
+ *  workspace    device buffer, 16-B, of qg_kv_attention_workspace_bytes; NULL
+ *               if that is 0.  Scratch: calls that may overlap, or graphs
+ *               that may run at once, need one each.
+ *  out          device [M][Hq][D] bf16 or fp32, 16-B, rows out_stride
+ *               elements apart (a multiple of 8, at least Hq * D).  Rows of
+ *               no request are left as they are.
+ * Sums and the softmax's statistics are fp32, probabilities enter the second
+ * product in f16.  A row's result does not depend on other rows; it is the
+ * same in every run.
+ * Errors: QG_EINVAL, QG_ESHAPE, QG_EALIGN, QG_ESIZE, QG_EUNSUPPORTED (a tree
+ * with a window, QG_OUT_I32_GROUPS), QG_EHIP.
+ */
+int kv_attention_run(const qg_kv_cache *cache, int64_t R, int64_t M, int64_t Hq, const void *q,
+                     int64_t q_stride, const int32_t *q_start, const int32_t *lens,
+                     const int32_t *table, int64_t max_blocks, const uint32_t *tree_mask,
+                     int64_t window, float scale, int64_t max_q, int64_t max_len,
+                     void *workspace, size_t workspace_bytes, void *out, int64_t out_stride,
+                     int out_dtype, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -31,6 +31,9 @@ OUT_BF16 = 0
 OUT_F32 = 1
 OUT_I32_GROUPS = 2
 
+KV_INT8 = 0
+KV_E4M3 = 1
+
 KERNEL_AUTO = 0
 KERNEL_VALU = 1
 KERNEL_MFMA = 2
@@ -61,6 +64,11 @@ EXPORTS = (
     "qg_batch_plan_build",
     "qg_batch_run",
     "qg_plain_read",
+    "rmsnorm_quant_run",
+    "kv_tables_run",
+    "kv_append_run",
+    "qg_kv_attention_workspace_bytes",
+    "kv_attention_run",
 )
 
 
@@ -76,6 +84,14 @@ class BatchPlan(C.Structure):
                 ("out_dtype", C.c_int32), ("grid", C.c_int32), ("kmax", C.c_int32),
                 ("kernel", C.c_int32), ("reserved1", C.c_int32), ("worklist", C.c_void_p),
                 ("worklist_bytes", C.c_size_t)]
+
+
+class CacheDesc(C.Structure):
+    """struct qg_kv_cache"""
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("k_scales", C.c_void_p),
+                ("v_scales", C.c_void_p), ("pages", C.c_int64), ("page", C.c_int32),
+                ("Hkv", C.c_int32), ("D", C.c_int32), ("fmt", C.c_int32)]
+
 
 _lock = threading.Lock()
 _lib = None
@@ -132,6 +148,17 @@ def raw():
             lib.qg_batch_run.restype = i
             lib.qg_plain_read.argtypes = [p, sz, p, i, p]
             lib.qg_plain_read.restype = i
+            lib.rmsnorm_quant_run.argtypes = [p, i, p, p, i, p, C.c_float, p, i64, i64, p, p, p, p]
+            lib.rmsnorm_quant_run.restype = i
+            lib.kv_tables_run.argtypes = [i64, i64, i64, i64, i64, p, p, p, p, p, p, p, p, p, p, p]
+            lib.kv_tables_run.restype = i
+            lib.kv_append_run.argtypes = [p, i64, p, i64, p, i64, p, p]
+            lib.kv_append_run.restype = i
+            lib.qg_kv_attention_workspace_bytes.argtypes = [i64] * 9
+            lib.qg_kv_attention_workspace_bytes.restype = sz
+            lib.kv_attention_run.argtypes = [p, i64, i64, i64, p, i64, p, p, p, i64, p, i64,
+                                             C.c_float, i64, i64, p, sz, p, i64, i, p]
+            lib.kv_attention_run.restype = i
             _lib = lib
     return _lib
 
@@ -357,3 +384,219 @@ def qg_plain_read(buf, sink, grid: int, stream=None):
 
 def qg_batch_run(plan: Plan, stream=None):
     _check(raw().qg_batch_run(C.byref(plan.plan), _stream(stream)), "qg_batch_run")
+
+
+# ------------------------------------------------------------------ norm, cache and attention
+def _one_device(*tensors):
+    """The device of the tensors given (None: left out); ValueError where one
+    is a host tensor or lies on another device."""
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("expected a device tensor")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError("tensors on %s and %s" % (dev, t.device))
+    return dev
+
+
+def _call(dev, stream, where, fn, *args):
+    """fn(*args, stream) with `dev` current; stream: as given, or dev's current one."""
+    torch = _torch()
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _call(dev, stream, where, fn, *args)
+    _check(fn(*args, _stream(stream)), where)
+
+
+def _typed(t, dtype, shape, name):
+    """The address of a contiguous tensor of this type and shape (None: NULL)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s tensor of shape %s (got %s %s)"
+                         % (name, dtype, tuple(shape), t.dtype, tuple(t.shape)))
+    return t.data_ptr()
+
+
+def _rows(t, H, D, dtype, name):
+    """Address and row stride of a [M, H, D] tensor whose rows are dense."""
+    if t.dtype != dtype or t.dim() != 3 or tuple(t.shape[1:]) != (H, D):
+        raise ValueError("%s must be a %s tensor [M, %d, %d] (got %s %s)"
+                         % (name, dtype, H, D, t.dtype, tuple(t.shape)))
+    M, width = t.shape[0], H * D
+    if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D):
+        raise ValueError("%s: the heads and dimensions of a token must be dense" % name)
+    return t.data_ptr(), (t.stride(0) if M > 1 else width)
+
+
+def _float_type(t, name):
+    torch = _torch()
+    if t.dtype == torch.bfloat16:
+        return OUT_BF16
+    if t.dtype == torch.float32:
+        return OUT_F32
+    raise ValueError("%s must be bfloat16 or float32 (got %s)" % (name, t.dtype))
+
+
+def rmsnorm_quant_run(x, weight, eps: float, residual=None, residual_out=None, signs=None, y=None,
+                      Xq=None, x_scales=None, stream=None):
+    """Root-mean-square norm of x + residual; x [M, K] bf16 or fp32.  Outputs
+    are written where a tensor is given: residual_out (may be residual), y
+    (bf16 [M, K]), Xq and x_scales (int8 [M, K], fp32 [M]; one without the
+    other is allocated); with none of them given, Xq and x_scales are.
+    signs: rotate before quantizing.  Returns (residual_out, y, Xq, x_scales)."""
+    torch = _torch()
+    if x.dim() != 2:
+        raise ValueError("x must be [M, K]")
+    M, K = x.shape
+    xt = _float_type(x, "x")
+    if Xq is not None or x_scales is not None or y is None:
+        if Xq is None:
+            Xq = torch.empty((M, K), dtype=torch.int8, device=x.device)
+        if x_scales is None:
+            x_scales = torch.empty(M, dtype=torch.float32, device=x.device)
+    if M == 0:
+        return residual_out, y, Xq, x_scales
+    dev = _one_device(x, weight, residual, residual_out, signs, y, Xq, x_scales)
+    rt = xt if residual is None else _float_type(residual, "residual")
+    rdt = x.dtype if residual is None else residual.dtype
+    _call(dev, stream, "rmsnorm_quant_run", raw().rmsnorm_quant_run,
+          _typed(x, x.dtype, (M, K), "x"), xt, _typed(residual, rdt, (M, K), "residual"),
+          _typed(residual_out, rdt, (M, K), "residual_out"), rt,
+          _typed(weight, torch.bfloat16, (K,), "weight"), eps, _typed(signs, torch.int8, (K,), "signs"),
+          M, K, _typed(y, torch.bfloat16, (M, K), "y"), _typed(Xq, torch.int8, (M, K), "Xq"),
+          _typed(x_scales, torch.float32, (M,), "x_scales"))
+    return residual_out, y, Xq, x_scales
+
+
+class KVCache:
+    """One layer's paged cache: k and v [pages, Hkv, page, D] of torch.int8 or
+    torch.float8_e4m3fn, k_scales and v_scales fp32 [pages, Hkv].  The bytes
+    of a [page, D] block are in the order include/qgemv.h states."""
+
+    def __init__(self, k, v, k_scales, v_scales):
+        torch = _torch()
+        if k.dim() != 4:
+            raise ValueError("k must be [pages, Hkv, page, D]")
+        pages, Hkv, page, D = k.shape
+        fmt = {torch.int8: KV_INT8, torch.float8_e4m3fn: KV_E4M3}.get(k.dtype)
+        if fmt is None:
+            raise ValueError("codes must be int8 or float8_e4m3fn (got %s)" % k.dtype)
+        self.device = _one_device(k, v, k_scales, v_scales)
+        self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
+        self.pages, self.page, self.Hkv, self.D, self.fmt = pages, page, Hkv, D, fmt
+        self.desc = CacheDesc(_typed(k, k.dtype, k.shape, "k"), _typed(v, k.dtype, k.shape, "v"),
+                              _typed(k_scales, torch.float32, (pages, Hkv), "k_scales"),
+                              _typed(v_scales, torch.float32, (pages, Hkv), "v_scales"),
+                              pages, page, Hkv, D, fmt)
+        self._ref = C.addressof(self.desc)
+
+    @classmethod
+    def empty(cls, pages: int, page: int, Hkv: int, D: int, fmt: int = KV_INT8, device="cuda"):
+        """A cache of unwritten pages."""
+        torch = _torch()
+        if fmt not in (KV_INT8, KV_E4M3):
+            raise ValueError("unknown cache format %r" % (fmt,))
+        dt = torch.int8 if fmt == KV_INT8 else torch.float8_e4m3fn
+        codes = [torch.zeros((pages, Hkv, page, D), dtype=torch.uint8, device=device).view(dt)
+                 for _ in range(2)]
+        scales = [torch.zeros((pages, Hkv), dtype=torch.float32, device=device) for _ in range(2)]
+        return cls(*codes, *scales)
+
+
+def kv_tables_run(page: int, lens, add, table, free_pages, free_count, max_tokens: int, keep=None,
+                  q_start=None, slots=None, positions=None, status=None, stream=None):
+    """One step of block tables, lengths and the free list (all updated in
+    place); int32 tensors: lens, add, keep [R], table [R, max_blocks],
+    free_pages [pages], free_count [1].  Returns (q_start [R + 1], slots
+    [max_tokens], positions [max_tokens], status [1])."""
+    torch = _torch()
+    i32 = torch.int32
+    if lens.dim() != 1 or table.dim() != 2 or free_pages.dim() != 1:
+        raise ValueError("lens, table and free_pages must be [R], [R, max_blocks] and [pages]")
+    R, pages, nb = lens.shape[0], free_pages.shape[0], table.shape[1]
+
+    def out(t, n, name):
+        if t is None:
+            return torch.empty(n, dtype=i32, device=lens.device)
+        if t.dim() != 1 or t.shape[0] < n:
+            raise ValueError("%s must hold at least %d values" % (name, n))
+        return t
+
+    if R == 0:
+        raise ValueError("no requests")
+    q_start, status = out(q_start, R + 1, "q_start"), out(status, 1, "status")
+    slots, positions = out(slots, max_tokens, "slots"), out(positions, max_tokens, "positions")
+    dev = _one_device(lens, add, table, free_pages, free_count, keep, q_start, slots, positions, status)
+    _call(dev, stream, "kv_tables_run", raw().kv_tables_run, R, page, pages, nb, max_tokens,
+          _typed(lens, i32, (R,), "lens"), _typed(keep, i32, (R,), "keep"), _typed(add, i32, (R,), "add"),
+          _typed(table, i32, (R, nb), "table"), _typed(free_pages, i32, (pages,), "free_pages"),
+          _typed(free_count, i32, (1,), "free_count"), _typed(q_start, i32, q_start.shape, "q_start"),
+          _typed(slots, i32, slots.shape, "slots"), _typed(positions, i32, positions.shape, "positions"),
+          _typed(status, i32, status.shape, "status"))
+    return q_start, slots, positions, status
+
+
+def kv_append_run(cache: KVCache, K, V, slots, stream=None):
+    """Write K and V (bf16 [M, Hkv, D], rows at any multiple of 8 elements)
+    into the cache's slots (int32 [M])."""
+    torch = _torch()
+    M = K.shape[0]
+    if V.shape[0] != M:
+        raise ValueError("K and V have %d and %d tokens" % (M, V.shape[0]))
+    if M == 0:
+        return
+    kp, ks = _rows(K, cache.Hkv, cache.D, torch.bfloat16, "K")
+    vp, vs = _rows(V, cache.Hkv, cache.D, torch.bfloat16, "V")
+    dev = _one_device(cache.k, K, V, slots)
+    _call(dev, stream, "kv_append_run", raw().kv_append_run, cache._ref, M, kp, ks, vp, vs,
+          _typed(slots, torch.int32, (M,), "slots"))
+
+
+def kv_attention_workspace_bytes(R: int, M: int, Hq: int, Hkv: int, D: int, page: int, max_q: int,
+                                 max_len: int, window: int = 0) -> int:
+    return raw().qg_kv_attention_workspace_bytes(R, M, Hq, Hkv, D, page, max_q, max_len, window)
+
+
+def kv_attention_run(cache: KVCache, q, q_start, lens, table, max_q: int, max_len=None,
+                     tree_mask=None, window: int = 0, scale=None, workspace=None, out=None,
+                     out_dtype: int = OUT_BF16, stream=None):
+    """Attention of the new tokens q (bf16 [M, Hq, D]) over the cache; q_start
+    int32 [R + 1], lens int32 [R] (new tokens included), table int32 [R,
+    max_blocks]; max_q: the most new tokens a request has; max_len: the
+    longest request (the table's width by default); tree_mask int32 [M].
+    scale: 1 / sqrt(D) by default.  Returns out [M, Hq, D]."""
+    torch = _torch()
+    i32 = torch.int32
+    if q.dim() != 3 or table.dim() != 2:
+        raise ValueError("q must be [M, Hq, D] and table [R, max_blocks]")
+    M, Hq, D = q.shape
+    R, nb = table.shape
+    if max_len is None:
+        max_len = nb * cache.page
+    if out is None:
+        out = torch.empty((M, Hq, D), dtype=_out_torch_dtype(out_dtype), device=q.device)
+    else:
+        out_dtype = _float_type(out, "out")
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    if M == 0 or R == 0:
+        return out
+    qp, qs = _rows(q, Hq, cache.D, torch.bfloat16, "q")
+    op, os_ = _rows(out, Hq, cache.D, out.dtype, "out")
+    if workspace is None:
+        n = kv_attention_workspace_bytes(R, M, Hq, cache.Hkv, cache.D, cache.page, max_q, max_len, window)
+        workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+    nbytes = workspace.numel() * workspace.element_size()
+    dev = _one_device(cache.k, q, q_start, lens, table, tree_mask, workspace, out)
+    _call(dev, stream, "kv_attention_run", raw().kv_attention_run, cache._ref, R, M, Hq, qp, qs,
+          _typed(q_start, i32, (R + 1,), "q_start"), _typed(lens, i32, (R,), "lens"),
+          _typed(table, i32, (R, nb), "table"), nb, _typed(tree_mask, i32, (M,), "tree_mask"), window,
+          scale if scale is not None else cache.D ** -0.5, max_q, max_len,
+          _typed(workspace, workspace.dtype, workspace.shape, "workspace") if nbytes else None, nbytes,
+          op, os_, out_dtype)
+    return out

@@ -1,0 +1,73 @@
+// The paged 8-bit cache of keys and values: byte order of a block and the
+// argument structs shared by kv_append.hip, kv_attention.hip, kv_tables.hip
+// and the C ABI.
+//
+// A block is what one page (32, 64, 128 or 256 consecutive tokens of a
+// request) holds for one KV head: page * D codes, one byte each, with one
+// fp32 scale; value = scale * code.  Blocks are stored [pages][Hkv].  Inside
+// a block (token t of the page, dimension d) the bytes are ordered so that
+// a wave's 128-bit loads are contiguous kilobytes that are already operands
+// of the 16x16x32 MFMA:
+//   keys    [t/16][d/16][t%16][d%16]: the kilobyte of 16 tokens and 64
+//           dimensions gives lane (g = lane >> 4, r = lane & 15) the 16
+//           dimensions 16g.. of token r.
+//   values  [t/32][d/32][(t%16)/4][d%16][(d/16)%2][(t/16)%2][t%4]: the
+//           kilobyte of 32 tokens and 32 dimensions gives lane (g, r) the
+//           tokens 4g..4g+3 and 16+4g..16+4g+3 of dimensions r and r + 16,
+//           which are the tokens whose scores that lane holds after the
+//           product K Q^T, so probabilities never leave their registers.
+#pragma once
+
+#include "qg_internal.h"
+
+namespace qg {
+
+constexpr int KV_STEP = 32;          // tokens of one attention step
+constexpr int KV_CHUNK_MAX = 2048;   // tokens one workgroup takes at most (64 pages of 32)
+constexpr int KV_ROWS_MAX = 32;      // query tokens of one request
+
+struct KvAppendArgs {
+    uint8_t *k, *v;
+    float *k_scales, *v_scales;
+    const uint16_t *K, *V;
+    const int32_t *slots;
+    int64_t k_stride, v_stride;  // elements between tokens
+    int64_t slots_end;           // pages * page
+    int M, Hkv, D, page, chunk;
+};
+
+struct KvAttnArgs {
+    const uint8_t *k, *v;
+    const float *k_scales, *v_scales;
+    const uint16_t *q;
+    const int32_t *q_start, *lens, *table;
+    const uint32_t *tree;
+    void *out;
+    float *part;     // [chunks][M][Hq][D]: unnormalised sums of a chunk
+    float *part_ml;  // [chunks][M][Hq][2]: running maximum (base 2) and sum
+    int64_t q_stride, out_stride;  // elements between tokens
+    int64_t pages;
+    int R, M, Hq, Hkv, G, page, max_blocks, max_q, window, chunks, chunk;
+    float scale;     // softmax scale * log2(e)
+    bool out_f32;
+};
+
+struct KvTablesArgs {
+    int32_t *lens, *table, *free_pages, *free_count;
+    const int32_t *keep, *add;
+    int32_t *q_start, *slots, *positions, *status;
+    int64_t pages;
+    int R, page, max_blocks, max_tokens;
+};
+
+hipError_t launch_kv_append(const KvAppendArgs &a, bool e4m3, hipStream_t s);
+hipError_t launch_kv_attention(const KvAttnArgs &a, int D, bool e4m3, hipStream_t s);
+hipError_t launch_kv_tables(const KvTablesArgs &a, hipStream_t s);
+// chunk length and number of chunks of an attention call over at most `span`
+// tokens a request, for `rows` rows (query tokens * heads) to a KV head
+void kv_attention_split(int64_t R, int64_t Hkv, int64_t rows, int64_t page, int64_t span,
+                        bool windowed, int *chunk, int64_t *chunks);
+
+constexpr int KV_TABLES_R_MAX = 4096;
+
+}  // namespace qg

@@ -1,0 +1,328 @@
+"""GPU: attention over the paged 8-bit cache, against its definition in 64
+bits.
+
+Tolerance of one output o = sum p v / l, with A = sum p |v| / l:
+ * rounding of the output, half a step: 2^-8 |o| (bf16), 2^-24 |o| (fp32);
+ * p rounded to f16: 2^-11 A, and below f16's normal range half its smallest
+   step, 2^-25, for each of the n tokens, in units of the largest |v| and
+   the power of two above the largest value scale (2 at most);
+ * the scores: D products summed in fp32 (2^-23 each, whatever the order),
+   d = (D + 4) 2^-23 sum |q k| scale, twice that in p / l;
+ * the sums over n tokens in fp32: 2 n 2^-24 A; exp2 and the scales: 2^-20 A."""
+import numpy as np
+import pytest
+import torch
+
+import cache_ref as ref
+import quantized_weight_decode_dequant_amd as pkg
+from helpers import note, to_np
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+class Case:
+    def __init__(self, seed, lens, T, H=2, G=4, D=128, page=64, fmt=pkg.KV_INT8, tree=False, spare=3, qscale=1.0, pages=None):
+        g = np.random.default_rng(seed)
+        self.g, self.fmt, self.page, self.H, self.G, self.D = g, fmt, page, H, G, D
+        R = len(lens)
+        self.lens, self.T = np.array(lens), np.array(T)
+        nb = -(-self.lens // page)
+        self.cols = max(int(nb.max()), 1)
+        self.pages = int(nb.sum()) + spare if pages is None else pages
+        perm = g.permutation(self.pages)
+        self.table = np.full((R, self.cols), -1)
+        at = 0
+        for r in range(R):
+            self.table[r, : nb[r]] = perm[at: at + nb[r]]
+            at += nb[r]
+        self.q_start = np.concatenate([[0], np.cumsum(self.T)])
+        self.M = int(self.q_start[-1])
+        shape = (self.pages, H, page, D)
+        if fmt == pkg.KV_INT8:
+            self.k, self.v = (np.clip(np.rint(40 * g.standard_normal(shape)), -127, 127).astype(np.int8).view(np.uint8) for _ in range(2))
+            unit = 0.025
+        else:
+            self.k, self.v = (ref.e4m3_bits(np.clip(140 * g.standard_normal(shape), -448, 448)) for _ in range(2))
+            unit = 0.007
+        self.ks, self.vs = (((0.3 + g.random(shape[:2])) * unit).astype(np.float32) for _ in range(2))
+        self.q = to_np(torch.from_numpy(qscale * g.standard_normal((max(self.M, 1), H * G, D))).to(torch.bfloat16))[: self.M]
+        self.tree = None
+        if tree:
+            masks = []
+            for n in self.T:
+                seen = []
+                for j in range(n):
+                    p = int(g.integers(-1, j)) if j else -1
+                    seen.append((seen[p] if p >= 0 else 0) | (1 << j))
+                masks += seen
+            self.tree = np.array(masks, dtype=np.uint32)
+
+    def cache(self):
+        dt = torch.int8 if self.fmt == pkg.KV_INT8 else torch.float8_e4m3fn
+        dev = [torch.from_numpy(ref.to_blocks(c, i)).to(DEV).view(dt) for i, c in ((False, self.k), (True, self.v))]
+        return pkg.KVCache(*dev, torch.from_numpy(self.ks).to(DEV), torch.from_numpy(self.vs).to(DEV))
+
+    def args(self):
+        t = lambda a: torch.tensor(np.asarray(a), dtype=torch.int32, device=DEV)  # noqa: E731
+        d = dict(q=torch.from_numpy(self.q).to(torch.bfloat16).to(DEV), q_start=t(self.q_start), lens=t(self.lens),
+                 table=t(self.table), max_q=max(int(self.T.max()), 1))
+        if self.tree is not None:
+            d["tree_mask"] = torch.from_numpy(self.tree.view(np.int32)).to(DEV)
+        return d
+
+    def want(self, window=0, scale=None):
+        return ref.attention(self.k, self.v, self.ks.astype(np.float64), self.vs.astype(np.float64), self.fmt == pkg.KV_E4M3,
+                             self.q, self.q_start, self.lens, self.table, self.tree, window, scale)
+
+    def check(self, got, window=0, scale=None, f32=False):
+        o, A, S = self.want(window, scale)
+        n = int(self.lens.max())
+        vmax = float(self.vs.max()) * (127 if self.fmt == pkg.KV_INT8 else 448)
+        d = (self.D + 4) * 2.0 ** -23 * S[:, :, None]
+        tol = ((2.0 ** -24 if f32 else 2.0 ** -8) * np.abs(o) + (2.0 ** -11 + 2 * d + 2 * n * 2.0 ** -24 + 2.0 ** -20) * A
+               + n * 2.0 ** -25 * 2 * vmax)
+        got = to_np(got)
+        ok = ~np.isnan(o)
+        assert np.all(np.isfinite(got[ok]))
+        err = np.abs(got - o)[ok] / tol[ok].clip(1e-30)
+        zero = ok & (A == 0)
+        assert not got[zero].any()
+        assert err.size == 0 or err.max() <= 1, err.max()
+        return float(err.max()) if err.size else 0.0
+
+    def run(self, window=0, scale=None, out_dtype=None, **kw):
+        a = self.args()
+        a.update(kw)
+        for dt in (pkg.OUT_BF16, pkg.OUT_F32) if out_dtype is None else (out_dtype,):
+            got = pkg.kv_attention_run(self.cache(), window=window, scale=scale, out_dtype=dt, **a)
+            torch.cuda.synchronize()
+            self.check(got, window, scale, dt == pkg.OUT_F32)
+        return got
+
+
+FMTS = [pkg.KV_INT8, pkg.KV_E4M3]
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("page", [32, 64, 128, 256])
+def test_types_heads_pages(fmt, D, page):
+    note("attention fmt=%d D=%d page=%d" % (fmt, D, page))
+    Case(D + page, [1, page, page + 1, 700, 31, 33], [1] * 6, D=D, page=page, fmt=fmt).run()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("H,G", [(1, 1), (3, 1), (2, 3), (1, 7), (2, 16), (1, 17), (1, 71)])
+@pytest.mark.parametrize("T", [1, 2, 5, 16, 32])
+def test_groups_and_tiles(fmt, H, G, T):
+    note("attention H=%d G=%d T=%d" % (H, G, T))
+    Case(H * 100 + G + T, [T, 47, 300 + T], [T, min(T, 3), T], H=H, G=G, D=64, fmt=fmt).run()
+
+
+@pytest.mark.parametrize("n", [1, 2, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129, 255, 256, 257, 1000, 5003])
+def test_lengths(n):
+    note("attention length", n)
+    Case(n, [n], [1], H=1, G=4, D=64, page=32).run()
+    Case(n, [n], [min(n, 7)], H=1, G=4, D=64, page=64, fmt=pkg.KV_E4M3).run()
+
+
+@pytest.mark.parametrize("R,H", [(1, 1), (1, 8), (40, 2), (160, 8)])
+def test_splits(R, H):
+    """One long request and a ragged batch: many chunks and few."""
+    note("attention splits R=%d H=%d" % (R, H))
+    lens = [9001] + [int(x) for x in np.random.default_rng(R).integers(1, 3000 // R + 40, R - 1)]
+    Case(R, lens, [1] * R, H=H, G=4, D=64, page=32).run(out_dtype=pkg.OUT_F32)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("T", [1, 2, 8, 16, 31, 32])
+def test_trees(fmt, T):
+    note("attention tree T=%d" % T)
+    c = Case(T, [T, T + 1, 200 + T, 64 * 3], [T, min(T, 2), T, T], D=128, tree=True, fmt=fmt)
+    c.run()
+    c.tree[:] = 0                        # a draft token that does not see itself: context only, or nothing
+    c.run()
+    c.tree[:] = 0xFFFFFFFF               # bits behind the last new token mean nothing
+    c.run()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("window", [1, 2, 31, 32, 33, 512, 5000, 1 << 30])
+@pytest.mark.parametrize("T", [1, 6])
+def test_windows(fmt, window, T):
+    note("attention window=%d T=%d" % (window, T))
+    Case(window % 977, [T, 40, 1200, 4099], [T] * 4, H=2, G=2, D=64, page=32, fmt=fmt).run(window=window)
+
+
+def test_empty_requests_and_rows_left_alone():
+    """Requests without tokens, without query rows, longer than their rows
+    say; the rows of no request and the padding keep what they held."""
+    c = Case(3, [0, 5, 0, 100, 64, 2], [1, 0, 2, 3, 1, 4], D=64)
+    a = c.args()
+    M = c.M + 5
+    for dt in (torch.bfloat16, torch.float32):
+        wide = torch.full((M, c.H * c.G + 2, c.D), 7.0, dtype=dt, device=DEV)
+        out = wide[:, : c.H * c.G]
+        q = torch.cat([a["q"], torch.full((5, c.H * c.G, c.D), float("nan"), dtype=torch.bfloat16, device=DEV)])
+        got = pkg.kv_attention_run(c.cache(), **dict(a, q=q, out=out))
+        torch.cuda.synchronize()
+        c.check(got[: c.M], f32=dt == torch.float32)
+        assert bool((wide[c.M:] == 7).all()) and bool((wide[:, c.H * c.G:] == 7).all())
+
+
+def test_strided_q():
+    c = Case(8, [70, 300], [3, 1], D=128, H=2, G=3)
+    a = c.args()
+    joint = torch.full((c.M, (c.H * c.G + 2 * c.H) * c.D), float("nan"), dtype=torch.bfloat16, device=DEV)
+    q = joint[:, : c.H * c.G * c.D].view(c.M, c.H * c.G, c.D)
+    q.copy_(a["q"])
+    assert not q.is_contiguous()
+    c.check(pkg.kv_attention_run(c.cache(), **dict(a, q=q)))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_garbage_behind_the_last_token(fmt):
+    """Slots behind a request's last token, unused pages and the scales of
+    unused pages may hold anything, NaN codes and NaN scales among it."""
+    c = Case(5, [37, 65, 1], [1, 2, 1], D=64, page=64, fmt=fmt)
+    ref_out = c.run(out_dtype=pkg.OUT_BF16)
+    used = {int(p) for p in c.table.reshape(-1) if p >= 0}
+    for p in range(c.pages):
+        if p not in used:
+            c.k[p] = c.v[p] = 0x7F
+            c.ks[p] = c.vs[p] = np.nan
+    for r, n in enumerate(c.lens):
+        c.k[c.table[r, (n - 1) // 64], :, (n - 1) % 64 + 1:] = 0x7F
+        c.v[c.table[r, (n - 1) // 64], :, (n - 1) % 64 + 1:] = 0xFF
+    got = pkg.kv_attention_run(c.cache(), **c.args())
+    assert torch.equal(got, ref_out)
+
+
+def test_pages_that_are_not_there():
+    c = Case(6, [200, 130, 64], [1, 2, 1], D=64, page=32)
+    c.table[0, 2] = -1
+    c.table[1, 0] = c.pages
+    c.table[2, :2] = 2 ** 31 - 1
+    c.run()
+
+
+def test_zero_scales_and_wide_ones():
+    """Value blocks of zeros (scale 0), and neighbours whose scales differ by
+    2^40: the small ones still count where they are all that is seen."""
+    c = Case(7, [640, 64, 96], [1, 1, 1], D=64, page=32)
+    for i, p in enumerate(c.table[0]):
+        c.vs[p] = [0.0, 1e-3, 2.0 ** -40, 1e4, 0.25][i % 5]
+    c.vs[c.table[1, :2]] = 0.0
+    c.vs[c.table[2, :3]] = 2.0 ** -60
+    c.ks[c.table[1, 0]] = 0.0
+    c.run()
+    one = Case(7, [96], [1], D=64, page=32)
+    one.vs[:] = 2.0 ** -60
+    one.run()                            # its tolerance scales with its own values
+
+
+def test_scores_far_apart():
+    """Large queries: the softmax is one token; scores far below zero; a scale
+    of zero (the mean of the values)."""
+    Case(11, [300, 33], [2, 1], D=128, qscale=100.0).run()
+    Case(12, [300, 33], [2, 1], D=128, qscale=1e30).run(scale=1e-30)
+    Case(13, [700], [1], D=64).run(scale=0.0)
+    Case(14, [700], [1], D=64).run(scale=-0.2)
+
+
+def test_rising_scores():
+    """Keys ordered so that each step's scores pass the running maximum."""
+    c = Case(15, [2000], [1], H=1, G=2, D=64, page=64)
+    q = c.q[0, 0]
+    ids = c.table[0]
+    rows = np.concatenate([c.k[p, 0] for p in ids]).view(np.int8).astype(np.float64)[:2000]
+    order = np.argsort(rows @ q)
+    flat = np.zeros((len(ids) * 64, 64), np.uint8)
+    flat[:2000] = rows[order].astype(np.int8).view(np.uint8)
+    for i, p in enumerate(ids):
+        c.k[p, 0] = flat[i * 64:(i + 1) * 64]
+        c.ks[p] = 0.05
+    c.run()
+
+
+def test_query_rows_that_are_not_finite_stay_alone():
+    c = Case(16, [500, 90], [4, 2], D=64)
+    a = c.args()
+    cache = c.cache()
+    clean = pkg.kv_attention_run(cache, **a)
+    a["q"] = a["q"].clone()
+    a["q"][1, 3, 5] = float("nan")
+    a["q"][4, 0, 0] = float("inf")
+    got = pkg.kv_attention_run(cache, **a)
+    bad = torch.zeros(c.M, c.H * c.G, dtype=torch.bool, device=DEV)
+    bad[1, 3] = bad[4, 0] = True
+    assert torch.equal(got[~bad], clean[~bad]) and torch.isnan(got[bad]).all()
+
+
+def test_longer_than_max_len_is_seen():
+    c = Case(17, [3000, 40], [1, 1], D=64, page=32)
+    got = pkg.kv_attention_run(c.cache(), **c.args(), max_len=64)
+    torch.cuda.synchronize()
+    assert torch.isnan(got[0]).all() and torch.isfinite(got[1]).all()
+
+
+def test_more_rows_than_max_q_are_left_alone():
+    c = Case(18, [100], [6], D=64)
+    a = dict(c.args(), max_q=4)
+    out = torch.full((c.M, c.H * c.G, c.D), 3.0, dtype=torch.bfloat16, device=DEV)
+    pkg.kv_attention_run(c.cache(), **a, out=out)
+    assert bool((out[4:] == 3).all())
+
+
+def test_q_start_that_cannot_be():
+    """Offsets past the rows of q: those requests are not computed."""
+    c = Case(19, [100, 70], [2, 2], D=64)
+    a = c.args()
+    a["q_start"] = torch.tensor([0, 2, 99], dtype=torch.int32, device=DEV)
+    out = torch.full((c.M, c.H * c.G, c.D), 3.0, dtype=torch.bfloat16, device=DEV)
+    got = pkg.kv_attention_run(c.cache(), **dict(a, max_q=32), out=out)
+    torch.cuda.synchronize()
+    assert bool((got[2:] == 3).all()) and torch.isfinite(got[:2]).all()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_past_32_bits(fmt):
+    """A pool of more than 4 GiB a side, the request on its last pages."""
+    page, H, D = 128, 8, 256
+    pages = (1 << 32) // (page * H * D) + 40
+    note("attention pool of %.1f GiB" % (pages * page * H * D / 2 ** 30))
+    c = Case(20, [3 * page + 5], [2], H=H, G=2, D=D, page=page, fmt=fmt, spare=4)
+    dt = torch.int8 if fmt == pkg.KV_INT8 else torch.float8_e4m3fn
+    small = c.cache()
+    big = []
+    for x in (small.k, small.v):
+        b = torch.zeros(pages, H, page, D, dtype=torch.uint8, device=DEV)
+        b[-c.pages:] = x.view(torch.uint8)
+        big.append(b.view(dt))
+    sc = []
+    for x in (small.k_scales, small.v_scales):
+        s = torch.zeros(pages, H, device=DEV)
+        s[-c.pages:] = x
+        sc.append(s)
+    a = c.args()
+    a["table"] = torch.where(a["table"] >= 0, a["table"] + pages - c.pages, a["table"])
+    c.check(pkg.kv_attention_run(pkg.KVCache(*big, *sc), **a))
+
+
+def test_same_result_every_time_and_alone():
+    """Bit-equal in repeated runs, on another stream, beside another call, and
+    for a request alone in the batch with the same split."""
+    c = Case(21, [2500, 300], [5, 5], D=128)
+    a, cache = c.args(), c.cache()
+    first = pkg.kv_attention_run(cache, **a)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    outs = []
+    for _ in range(3):
+        for s in streams:
+            with torch.cuda.stream(s):
+                outs.append(pkg.kv_attention_run(cache, **a))
+    torch.cuda.synchronize()
+    assert all(torch.equal(first, o) for o in outs)
