@@ -570,9 +570,10 @@ int kv_tables_run(int64_t R, int64_t page, int64_t pages, int64_t max_blocks, in
 
 /*
  * kv_append_run -- write M tokens' keys and values into the cache in 8 bits.
- * For each (page, KV head) touched: s = max(s_old, amax / top) with amax over
- * the new tokens, top = 127 (int8) or 448 (E4M3), and s_old = the block's
- * scale, or 0 if the first of the new tokens is the page's first; the new
+ * For each (page, KV head) touched: s = max(s_old, amax * (1 / top)) with amax
+ * over the new tokens, 1 / top the fp32 nearest to 1/127 (int8) or 1/448
+ * (E4M3), and s_old = the block's scale, or 0 if the first of the new tokens
+ * is the page's first; the new
  * codes are x * (1 / s) rounded to nearest even; if s grew, the block's codes
  * become code * (s_old / s), rounded likewise.  Every quotient and product is
  * one fp32 operation.

@@ -106,6 +106,8 @@ class QGError(RuntimeError):
 def raw():
     """The loaded library with argument types set (loads on first use)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -387,57 +389,63 @@ def qg_batch_run(plan: Plan, stream=None):
 
 
 # ------------------------------------------------------------------ norm, cache and attention
-def _one_device(*tensors):
-    """The device of the tensors given (None: left out); ValueError where one
-    is a host tensor or lies on another device."""
-    dev = None
-    for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("expected a device tensor")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError("tensors on %s and %s" % (dev, t.device))
+# These calls are short on the GPU (a few microseconds), so their checks are
+# kept to a few attribute reads a tensor.
+def _device(t):
+    """The index of the device a tensor lies on."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("expected a device tensor")
     return dev
+
+
+def _arg(t, dtype, shape, dev, name):
+    """The address of a contiguous tensor of this type and shape on `dev`
+    (None: NULL)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s tensor of shape %s (got %s %s)"
+                         % (name, dtype, tuple(shape), t.dtype, tuple(t.shape)))
+    if t.get_device() != dev:
+        raise ValueError("%s must be a device tensor on device %d (got %s)" % (name, dev, t.device))
+    return t.data_ptr()
+
+
+def _rows(t, H, D, dtype, dev, name):
+    """Address and row stride of a [M, H, D] tensor whose rows are dense."""
+    shape = t.shape
+    if t.dtype is not dtype or len(shape) != 3 or shape[1] != H or shape[2] != D:
+        raise ValueError("%s must be a %s tensor [M, %d, %d] (got %s %s)"
+                         % (name, dtype, H, D, t.dtype, tuple(shape)))
+    if t.get_device() != dev:
+        raise ValueError("%s must be a device tensor on device %d (got %s)" % (name, dev, t.device))
+    row, head, dim = t.stride()
+    if dim != 1 or (H > 1 and head != D):
+        raise ValueError("%s: the heads and dimensions of a token must be dense" % name)
+    return t.data_ptr(), (row if shape[0] > 1 else H * D)
 
 
 def _call(dev, stream, where, fn, *args):
     """fn(*args, stream) with `dev` current; stream: as given, or dev's current one."""
     torch = _torch()
-    if dev.index != torch.cuda.current_device():
+    if torch.cuda.current_device() != dev:
         with torch.cuda.device(dev):
             return _call(dev, stream, where, fn, *args)
-    _check(fn(*args, _stream(stream)), where)
-
-
-def _typed(t, dtype, shape, name):
-    """The address of a contiguous tensor of this type and shape (None: NULL)."""
-    if t is None:
-        return None
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous %s tensor of shape %s (got %s %s)"
-                         % (name, dtype, tuple(shape), t.dtype, tuple(t.shape)))
-    return t.data_ptr()
-
-
-def _rows(t, H, D, dtype, name):
-    """Address and row stride of a [M, H, D] tensor whose rows are dense."""
-    if t.dtype != dtype or t.dim() != 3 or tuple(t.shape[1:]) != (H, D):
-        raise ValueError("%s must be a %s tensor [M, %d, %d] (got %s %s)"
-                         % (name, dtype, H, D, t.dtype, tuple(t.shape)))
-    M, width = t.shape[0], H * D
-    if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D):
-        raise ValueError("%s: the heads and dimensions of a token must be dense" % name)
-    return t.data_ptr(), (t.stride(0) if M > 1 else width)
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    status = fn(*args, stream)
+    if status != QG_OK:
+        raise QGError(status, where)
 
 
 def _float_type(t, name):
     torch = _torch()
-    if t.dtype == torch.bfloat16:
+    if t.dtype is torch.bfloat16:
         return OUT_BF16
-    if t.dtype == torch.float32:
+    if t.dtype is torch.float32:
         return OUT_F32
     raise ValueError("%s must be bfloat16 or float32 (got %s)" % (name, t.dtype))
 
@@ -461,15 +469,14 @@ def rmsnorm_quant_run(x, weight, eps: float, residual=None, residual_out=None, s
             x_scales = torch.empty(M, dtype=torch.float32, device=x.device)
     if M == 0:
         return residual_out, y, Xq, x_scales
-    dev = _one_device(x, weight, residual, residual_out, signs, y, Xq, x_scales)
-    rt = xt if residual is None else _float_type(residual, "residual")
-    rdt = x.dtype if residual is None else residual.dtype
+    dev, mk, i8 = _device(x), (M, K), torch.int8
+    rt, rdt = (xt, x.dtype) if residual is None else (_float_type(residual, "residual"), residual.dtype)
     _call(dev, stream, "rmsnorm_quant_run", raw().rmsnorm_quant_run,
-          _typed(x, x.dtype, (M, K), "x"), xt, _typed(residual, rdt, (M, K), "residual"),
-          _typed(residual_out, rdt, (M, K), "residual_out"), rt,
-          _typed(weight, torch.bfloat16, (K,), "weight"), eps, _typed(signs, torch.int8, (K,), "signs"),
-          M, K, _typed(y, torch.bfloat16, (M, K), "y"), _typed(Xq, torch.int8, (M, K), "Xq"),
-          _typed(x_scales, torch.float32, (M,), "x_scales"))
+          _arg(x, x.dtype, mk, dev, "x"), xt, _arg(residual, rdt, mk, dev, "residual"),
+          _arg(residual_out, rdt, mk, dev, "residual_out"), rt,
+          _arg(weight, torch.bfloat16, (K,), dev, "weight"), eps, _arg(signs, i8, (K,), dev, "signs"),
+          M, K, _arg(y, torch.bfloat16, mk, dev, "y"), _arg(Xq, i8, mk, dev, "Xq"),
+          _arg(x_scales, torch.float32, (M,), dev, "x_scales"))
     return residual_out, y, Xq, x_scales
 
 
@@ -486,13 +493,12 @@ class KVCache:
         fmt = {torch.int8: KV_INT8, torch.float8_e4m3fn: KV_E4M3}.get(k.dtype)
         if fmt is None:
             raise ValueError("codes must be int8 or float8_e4m3fn (got %s)" % k.dtype)
-        self.device = _one_device(k, v, k_scales, v_scales)
+        dev, sc = _device(k), (pages, Hkv)
         self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
-        self.pages, self.page, self.Hkv, self.D, self.fmt = pages, page, Hkv, D, fmt
-        self.desc = CacheDesc(_typed(k, k.dtype, k.shape, "k"), _typed(v, k.dtype, k.shape, "v"),
-                              _typed(k_scales, torch.float32, (pages, Hkv), "k_scales"),
-                              _typed(v_scales, torch.float32, (pages, Hkv), "v_scales"),
-                              pages, page, Hkv, D, fmt)
+        self.pages, self.page, self.Hkv, self.D, self.fmt, self.device = pages, page, Hkv, D, fmt, dev
+        self.desc = CacheDesc(_arg(k, k.dtype, k.shape, dev, "k"), _arg(v, k.dtype, k.shape, dev, "v"),
+                              _arg(k_scales, torch.float32, sc, dev, "k_scales"),
+                              _arg(v_scales, torch.float32, sc, dev, "v_scales"), pages, page, Hkv, D, fmt)
         self._ref = C.addressof(self.desc)
 
     @classmethod
@@ -531,13 +537,13 @@ def kv_tables_run(page: int, lens, add, table, free_pages, free_count, max_token
         raise ValueError("no requests")
     q_start, status = out(q_start, R + 1, "q_start"), out(status, 1, "status")
     slots, positions = out(slots, max_tokens, "slots"), out(positions, max_tokens, "positions")
-    dev = _one_device(lens, add, table, free_pages, free_count, keep, q_start, slots, positions, status)
+    dev, r = _device(lens), (R,)
     _call(dev, stream, "kv_tables_run", raw().kv_tables_run, R, page, pages, nb, max_tokens,
-          _typed(lens, i32, (R,), "lens"), _typed(keep, i32, (R,), "keep"), _typed(add, i32, (R,), "add"),
-          _typed(table, i32, (R, nb), "table"), _typed(free_pages, i32, (pages,), "free_pages"),
-          _typed(free_count, i32, (1,), "free_count"), _typed(q_start, i32, q_start.shape, "q_start"),
-          _typed(slots, i32, slots.shape, "slots"), _typed(positions, i32, positions.shape, "positions"),
-          _typed(status, i32, status.shape, "status"))
+          _arg(lens, i32, r, dev, "lens"), _arg(keep, i32, r, dev, "keep"), _arg(add, i32, r, dev, "add"),
+          _arg(table, i32, (R, nb), dev, "table"), _arg(free_pages, i32, (pages,), dev, "free_pages"),
+          _arg(free_count, i32, (1,), dev, "free_count"), _arg(q_start, i32, q_start.shape, dev, "q_start"),
+          _arg(slots, i32, slots.shape, dev, "slots"), _arg(positions, i32, positions.shape, dev, "positions"),
+          _arg(status, i32, status.shape, dev, "status"))
     return q_start, slots, positions, status
 
 
@@ -550,11 +556,11 @@ def kv_append_run(cache: KVCache, K, V, slots, stream=None):
         raise ValueError("K and V have %d and %d tokens" % (M, V.shape[0]))
     if M == 0:
         return
-    kp, ks = _rows(K, cache.Hkv, cache.D, torch.bfloat16, "K")
-    vp, vs = _rows(V, cache.Hkv, cache.D, torch.bfloat16, "V")
-    dev = _one_device(cache.k, K, V, slots)
+    dev, H, D, bf16 = cache.device, cache.Hkv, cache.D, torch.bfloat16
+    kp, ks = _rows(K, H, D, bf16, dev, "K")
+    vp, vs = _rows(V, H, D, bf16, dev, "V")
     _call(dev, stream, "kv_append_run", raw().kv_append_run, cache._ref, M, kp, ks, vp, vs,
-          _typed(slots, torch.int32, (M,), "slots"))
+          _arg(slots, torch.int32, (M,), dev, "slots"))
 
 
 def kv_attention_workspace_bytes(R: int, M: int, Hq: int, Hkv: int, D: int, page: int, max_q: int,
@@ -586,17 +592,19 @@ def kv_attention_run(cache: KVCache, q, q_start, lens, table, max_q: int, max_le
         raise ValueError("out must have q's shape")
     if M == 0 or R == 0:
         return out
-    qp, qs = _rows(q, Hq, cache.D, torch.bfloat16, "q")
-    op, os_ = _rows(out, Hq, cache.D, out.dtype, "out")
+    dev, D = cache.device, cache.D
+    qp, qs = _rows(q, Hq, D, torch.bfloat16, dev, "q")
+    op, os_ = _rows(out, Hq, D, out.dtype, dev, "out")
+    lib = raw()
     if workspace is None:
-        n = kv_attention_workspace_bytes(R, M, Hq, cache.Hkv, cache.D, cache.page, max_q, max_len, window)
-        workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
-    nbytes = workspace.numel() * workspace.element_size()
-    dev = _one_device(cache.k, q, q_start, lens, table, tree_mask, workspace, out)
-    _call(dev, stream, "kv_attention_run", raw().kv_attention_run, cache._ref, R, M, Hq, qp, qs,
-          _typed(q_start, i32, (R + 1,), "q_start"), _typed(lens, i32, (R,), "lens"),
-          _typed(table, i32, (R, nb), "table"), nb, _typed(tree_mask, i32, (M,), "tree_mask"), window,
-          scale if scale is not None else cache.D ** -0.5, max_q, max_len,
-          _typed(workspace, workspace.dtype, workspace.shape, "workspace") if nbytes else None, nbytes,
+        nbytes = lib.qg_kv_attention_workspace_bytes(R, M, Hq, cache.Hkv, D, cache.page, max_q, max_len, window)
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
+    else:
+        nbytes = workspace.numel() * workspace.element_size()
+    _call(dev, stream, "kv_attention_run", lib.kv_attention_run, cache._ref, R, M, Hq, qp, qs,
+          _arg(q_start, i32, (R + 1,), dev, "q_start"), _arg(lens, i32, (R,), dev, "lens"),
+          _arg(table, i32, (R, nb), dev, "table"), nb, _arg(tree_mask, i32, (M,), dev, "tree_mask"), window,
+          scale if scale is not None else D ** -0.5, max_q, max_len,
+          _arg(workspace, workspace.dtype, workspace.shape, dev, "workspace") if nbytes else None, nbytes,
           op, os_, out_dtype)
     return out

@@ -1,8 +1,8 @@
 // New keys and values written into the paged 8-bit cache.
 //
-// Per page and head: s = max(s_old, amax / top) with amax over the new
-// tokens' finite values, top = 127 (int8) or 448 (E4M3) and s_old = 0 where
-// the first of the new tokens opens the page; inv = 1 / s; code = round(x *
+// Per page and head: s = max(s_old, amax * (1 / top)) with amax over the new
+// tokens' finite values, 1 / top the fp32 nearest to 1/127 (int8) or 1/448
+// (E4M3) and s_old = 0 where the first of the new tokens opens the page; inv = 1 / s; code = round(x *
 // inv), clamped to +-top.  Where s grew, the page's codes are rounded again
 // from code * (s_old / s).  Each of these steps is one correctly rounded
 // fp32 operation (round to nearest even), so the codes do not depend on how
@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(AP_T) kv_append_kernel(KvAppendArgs a) {
     const uint16_t *X = value ? a.V : a.K;
     const int64_t stride = value ? a.v_stride : a.k_stride;
     const int D = a.D, page = a.page;
-    const float top = E4M3 ? 448.f : 127.f;
+    constexpr float inv_top = E4M3 ? 1.f / 448.f : 1.f / 127.f;
     const int m1 = min((int)(blockIdx.x + 1) * a.chunk, a.M);
     for (int m = blockIdx.x * a.chunk; m < m1; ++m) {
         const int slot = a.slots[m];
@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(AP_T) kv_append_kernel(KvAppendArgs a) {
         uint8_t *codes = (value ? a.v : a.k) + block * page * D;
         float *scale = (value ? a.v_scales : a.k_scales) + block;
         const float s_old = off ? *scale : 0.f;
-        const float s = fmaxf(s_old, amax / top);
+        const float s = fmaxf(s_old, amax * inv_top);
         const float inv = s > 0.f ? 1.f / s : 0.f;
         if (off && s > s_old) {
             const float ratio = s_old / s;

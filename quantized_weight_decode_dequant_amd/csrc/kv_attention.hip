@@ -15,7 +15,7 @@
 // is only raised when a score passes it by 8 (in powers of two: p <= 2^8 is
 // far inside f16), so most steps neither exchange across lanes nor rescale O.
 // The value scales enter p as vs / vref with vref a power of two at least as
-// large as every vs so far, wave-uniform.
+// large as every vs of the chunk.
 //
 // A workgroup takes one chunk of a request's tokens for one KV head and up to
 // 16 * NR * RS rows; its waves split the chunk's steps (TS of them) and the
@@ -29,33 +29,45 @@ namespace {
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
 
-constexpr int AT_WAVES = 4;
 constexpr float NEG_INF = -__builtin_inff();
+
+// An int8 code c enters the MFMA as the f16 whose bits are c + 128: a
+// denormal (which the MFMA keeps), worth (c + 128) 2^-24.  The products'
+// accumulators are corrected by -128 times the other operand's sum.
+template <bool E4M3>
+struct Code {
+    static constexpr float unit = E4M3 ? 1.f : 0x1p24f;
+    static constexpr float bias = E4M3 ? 0.f : 128.f;
+};
 
 // 8 codes (two words) as the f16 operand
 template <bool E4M3>
 __device__ __forceinline__ f16x8_t codes8(unsigned w0, unsigned w1) {
-    f16x2_t p[4];
+    u32x4_t o;
     if (E4M3) {
-        p[0] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w0, 1.f, false);
-        p[1] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w0, 1.f, true);
-        p[2] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w1, 1.f, false);
-        p[3] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w1, 1.f, true);
+        o[0] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w0, 1.f, false));
+        o[1] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w0, 1.f, true));
+        o[2] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w1, 1.f, false));
+        o[3] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w1, 1.f, true));
     } else {
-        // byte b ^ 0x80 under the f16 exponent of 1024: 1024 + 128 + code
         w0 ^= 0x80808080u;
         w1 ^= 0x80808080u;
-        const f16x2_t bias = {(_Float16)1152.f, (_Float16)1152.f};
-        p[0] = __builtin_bit_cast(f16x2_t, __builtin_amdgcn_perm(0x64646464u, w0, 0x04010400u)) - bias;
-        p[1] = __builtin_bit_cast(f16x2_t, __builtin_amdgcn_perm(0x64646464u, w0, 0x04030402u)) - bias;
-        p[2] = __builtin_bit_cast(f16x2_t, __builtin_amdgcn_perm(0x64646464u, w1, 0x04010400u)) - bias;
-        p[3] = __builtin_bit_cast(f16x2_t, __builtin_amdgcn_perm(0x64646464u, w1, 0x04030402u)) - bias;
+        o[0] = __builtin_amdgcn_perm(0u, w0, 0x0C010C00u);  // selector 0x0C: a zero byte
+        o[1] = __builtin_amdgcn_perm(0u, w0, 0x0C030C02u);
+        o[2] = __builtin_amdgcn_perm(0u, w1, 0x0C010C00u);
+        o[3] = __builtin_amdgcn_perm(0u, w1, 0x0C030C02u);
     }
-    return f16x8_t{p[0][0], p[0][1], p[1][0], p[1][1], p[2][0], p[2][1], p[3][0], p[3][1]};
+    return __builtin_bit_cast(f16x8_t, o);
 }
 
 __device__ __forceinline__ float readlane_f(float v, int l) {
     return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), l));
+}
+
+// four values rounded to bf16 (to nearest even)
+__device__ __forceinline__ u32x2_t bf16x4(f32x4_t v) {
+    return u32x2_t{__builtin_bit_cast(unsigned, bf16x2_t{(__bf16)v[0], (__bf16)v[1]}),
+                   __builtin_bit_cast(unsigned, bf16x2_t{(__bf16)v[2], (__bf16)v[3]})};
 }
 
 // the smallest power of two >= x (x > 0)
@@ -86,19 +98,37 @@ __device__ __forceinline__ Span span_of(const KvAttnArgs &a, int r) {
 
 }  // namespace
 
-template <bool E4M3, int D, int NR, int RS>
-__global__ void __launch_bounds__(AT_WAVES * 64) kv_attn_kernel(KvAttnArgs a) {
-    constexpr int TS = AT_WAVES / RS;   // waves that split the tokens
+// One wave's loads of N kilobytes, 128 bits a lane, through a buffer resource
+// over the page's block: `bytes` of 0 reads nothing and gives zeros, so the
+// loads are issued on every path and a wait for earlier ones leaves them in
+// flight.
+template <int N, bool NT>
+__device__ __forceinline__ void load_codes(u32x4_t (&to)[N], const uint8_t *block, unsigned bytes, unsigned at, int lane) {
+    const __amdgpu_buffer_rsrc_t r = make_rsrc(block, bytes);
+#pragma unroll
+    for (int u = 0; u < N; ++u)
+        to[u] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                                                r, 16 * lane + u % 4 * 1024, (int)at + u / 4 * 4096, NT ? 2 : 0));
+}
+
+template <bool E4M3, int D, int NR, int RS, int WAVES>
+__global__ void __launch_bounds__(WAVES * 64, 2) kv_attn_kernel(KvAttnArgs a) {
+    constexpr int TS = WAVES / RS;      // waves that split the tokens
     constexpr int KS = D / 32;          // MFMA steps of Q K^T
     constexpr int DT = D / 16;          // tiles of O
-    __shared__ float slots[TS > 1 ? 2 * RS : 1][TS > 1 ? NR * (DT * 4 + 2) : 1][64];
+    constexpr int SL = DT * 4 + 2;      // floats a lane and row tile joins
+    constexpr float UNIT = Code<E4M3>::unit, BIAS = Code<E4M3>::bias;
+    constexpr bool NT = RS == 1;        // read by one wave only: past the caches
+    __shared__ float slots[TS > 1 ? (TS / 2) * RS : 1][TS > 1 ? NR * SL : 1][64];
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g = lane >> 4, c = lane & 15;
     const int ts = wave / RS, rsi = wave % RS;
-    const int bx = blockIdx.x;
-    const int ci = bx % a.chunks, rh = bx / a.chunks;
+    // chunk index slowest: workgroups go to the XCDs in turn, and most late
+    // chunks are empty where lengths differ
+    const int nrh = a.R * a.Hkv;
+    const int ci = blockIdx.x / nrh, rh = blockIdx.x % nrh;
     const int r = rh / a.Hkv, h = rh % a.Hkv;
     const Span sp = span_of(a, r);
     const int rows = sp.T * a.G;
@@ -109,10 +139,48 @@ __global__ void __launch_bounds__(AT_WAVES * 64) kv_attn_kernel(KvAttnArgs a) {
     const int q0 = a.q_start[r];
     const int base = sp.len - sp.T;  // position of the first query token
 
+    // the chunk's pages and their scales, one a lane
+    const int t_lo = max(chunk * a.chunk, sp.first & ~(KV_STEP - 1));
+    const int t_hi = min((chunk + 1) * a.chunk, sp.len);
+    const int page0 = t_lo / a.page;
+    int my_page = -1;
+    float my_ks = 0.f, my_vs = 0.f;
+    if (page0 + lane < a.max_blocks && (page0 + lane) * a.page < t_hi) {
+        my_page = a.table[(size_t)r * a.max_blocks + page0 + lane];
+        if (my_page < 0 || my_page >= a.pages) my_page = -1;
+        if (my_page >= 0) {
+            my_ks = a.k_scales[(size_t)my_page * a.Hkv + h];
+            my_vs = a.v_scales[(size_t)my_page * a.Hkv + h];
+        }
+    }
+    // vref: a power of two at least as large as every value scale of the chunk
+    float vref = fmaxf(my_vs, 0.f);
+#pragma unroll
+    for (int d = 32; d; d >>= 1) vref = fmaxf(vref, __shfl_xor(vref, d));
+    vref = readlane_f(vref > 0.f ? pow2_above(vref) : 1.f, 0);
+    // the page's value scale over vref, as a power of two in the exponent, and
+    // its inverse (a page whose values are all 0: no scale)
+    const bool my_v = my_vs > 0.f;
+    const float my_lr = my_v ? __builtin_amdgcn_logf(my_vs / vref) : 0.f, my_rr = my_v ? vref / my_vs : 1.f;
+    const int shift = __builtin_ctz(a.page);
+    // the loads of the step at t (past the end, or of a page that is not
+    // there: none)
+    u32x4_t kw[D / 32], vw[D / 32];
+    const auto page_at = [&](int t) { return t < t_hi ? __builtin_amdgcn_readlane(my_page, (t >> shift) - page0) : -1; };
+    const auto load = [&](u32x4_t(&to)[D / 32], const uint8_t *codes, int t) {
+        const int page = page_at(t);
+        const size_t at = ((size_t)max(page, 0) * a.Hkv + h) * ((size_t)a.page * D);
+        load_codes<D / 32, NT>(to, uniform_ptr(codes + at), page < 0 ? 0u : (unsigned)a.page * D,
+                               (unsigned)(t & (a.page - 1)) * D, lane);
+    };
+    const int first = t_lo + ts * KV_STEP;
+    load(kw, a.k, first);
+    load(vw, a.v, first);
+
     // Q, as f16 in the K tiles' order of dimensions
     f16x8_t qf[NR][KS];
-    float cs[NR];    // softmax scale and q's power of two
-    int rowm[NR], rowh[NR], pos[NR];
+    float cs[NR], k0[NR];  // factor and start of the scores
+    int rowm[NR], rowh[NR], pos[NR], lo[NR];  // visible: lo < t <= pos
     unsigned tree[NR];
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
@@ -122,6 +190,7 @@ __global__ void __launch_bounds__(AT_WAVES * 64) kv_attn_kernel(KvAttnArgs a) {
         rowm[n] = valid ? q0 + j : -1;
         rowh[n] = h * a.G + (valid ? row % a.G : 0);
         pos[n] = base + j;
+        lo[n] = a.window > 0 ? pos[n] - a.window : -1;
         tree[n] = a.tree && valid ? a.tree[q0 + j] : 0u;
         const uint16_t *q = a.q + (size_t)(q0 + j) * a.q_stride + (size_t)rowh[n] * D;
         float v[KS][8];
@@ -139,136 +208,74 @@ __global__ void __launch_bounds__(AT_WAVES * 64) kv_attn_kernel(KvAttnArgs a) {
         }
         top = fmaxf(top, __shfl_xor(top, 16));
         top = fmaxf(top, __shfl_xor(top, 32));
-        // the row's largest magnitude to [2^13, 2^14)
+        // the row's largest magnitude to [2^13, 2^14), the scale's sign with it
         const int e2 = top > 0.f ? 13 - ((int)(__builtin_bit_cast(unsigned, top) >> 23) - 127) : 0;
+        float sum = 0.f;
 #pragma unroll
         for (int s = 0; s < KS; ++s)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) qf[n][s][e] = (_Float16)ldexpf(v[s][e], e2);
-        cs[n] = ldexpf(a.scale, -e2);
+            for (int e = 0; e < 8; ++e) {
+                const float x = ldexpf(v[s][e], e2);
+                const _Float16 hx = (_Float16)(a.scale < 0.f ? -x : x);
+                qf[n][s][e] = hx;
+                sum += (float)hx;
+            }
+        if (BIAS != 0.f) {
+            sum += __shfl_xor(sum, 16);
+            sum += __shfl_xor(sum, 32);
+        }
+        k0[n] = -(BIAS / UNIT) * sum;
+        cs[n] = ldexpf(fabsf(a.scale) * UNIT, -e2);
     }
 
-    f32x4_t o[NR][DT];
-    float m[NR], l[NR];
+    f32x4_t o[NR][DT];  // sums of p times values, in units of vref (/ UNIT, biased)
+    float m[NR], nm[NR], l[NR], ps[NR];
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
         m[n] = NEG_INF;
-        l[n] = 0.f;
+        nm[n] = l[n] = ps[n] = 0.f;
 #pragma unroll
         for (int d = 0; d < DT; ++d) o[n][d] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     }
-    float vref = 0.f;
+    const f16x8_t ones = {(_Float16)1.f, (_Float16)1.f, (_Float16)1.f, (_Float16)1.f,
+                          (_Float16)1.f, (_Float16)1.f, (_Float16)1.f, (_Float16)1.f};
 
-    const int t_lo = max(chunk * a.chunk, sp.first & ~(KV_STEP - 1));
-    const int t_hi = min((chunk + 1) * a.chunk, sp.len);
-    // the chunk's pages and their scales, one a lane
-    const int page0 = t_lo / a.page;
-    int my_page = -1;
-    float my_ks = 0.f, my_vs = 0.f;
-    if (page0 + lane < a.max_blocks && (page0 + lane) * a.page < t_hi) {
-        my_page = a.table[(size_t)r * a.max_blocks + page0 + lane];
-        if (my_page < 0 || my_page >= a.pages) my_page = -1;
-        if (my_page >= 0) {
-            my_ks = a.k_scales[(size_t)my_page * a.Hkv + h];
-            my_vs = a.v_scales[(size_t)my_page * a.Hkv + h];
-        }
-    }
-    for (int t0 = t_lo + ts * KV_STEP; t0 < t_hi; t0 += TS * KV_STEP) {
-        const int pi = t0 / a.page - page0;
-        const int page = __builtin_amdgcn_readlane(my_page, pi);
-        if (page < 0) continue;  // a page that is not there is not attended to
-        const float ks = readlane_f(my_ks, pi), vs = readlane_f(my_vs, pi);
-        const int in = t0 % a.page;
-        const size_t block = ((size_t)page * a.Hkv + h) * ((size_t)a.page * D) + (size_t)in * D;
-        const u32x4_t *kp = reinterpret_cast<const u32x4_t *>(a.k + block) + lane;
-        const u32x4_t *vp = reinterpret_cast<const u32x4_t *>(a.v + block) + lane;
-        u32x4_t kw[2][D / 64], vw[D / 32];
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int u = 0; u < D / 64; ++u) kw[i][u] = kp[(i * (D / 64) + u) * 64];
-#pragma unroll
-        for (int u = 0; u < D / 32; ++u) vw[u] = vp[u * 64];
-
+    // A step's keys are replaced by the next step's once they are used, then
+    // its values: one buffer each, with loads in flight all the time.
+    constexpr int STRIDE = TS * KV_STEP;
+    for (int t0 = first; t0 < t_hi; t0 += STRIDE) {
+        // a page that is not there is not attended to
+        const bool there = page_at(t0) >= 0;
+        const int pi = (t0 >> shift) - page0;
+        const float ks = readlane_f(my_ks, pi), lr = readlane_f(my_lr, pi), rr = readlane_f(my_rr, pi);
+        const bool no_v = !(readlane_f(my_vs, pi) > 0.f);
         // scores
         f32x4_t s[NR][2];
 #pragma unroll
-        for (int n = 0; n < NR; ++n) s[n][0] = s[n][1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        for (int n = 0; n < NR; ++n) s[n][0] = s[n][1] = f32x4_t{k0[n], k0[n], k0[n], k0[n]};
+        // (the barriers keep the compiler from converting every code first,
+        // which takes more registers than there are)
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int k = 0; k < KS; ++k) {
 #pragma unroll
-            for (int k = 0; k < KS; ++k) {
-                const u32x4_t w = kw[i][k >> 1];
+            for (int i = 0; i < 2; ++i) {
+                const u32x4_t w = kw[i * (D / 64) + (k >> 1)];
                 const f16x8_t kf = codes8<E4M3>(w[2 * (k & 1)], w[2 * (k & 1) + 1]);
 #pragma unroll
                 for (int n = 0; n < NR; ++n)
                     s[n][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[n][k], s[n][i], 0, 0, 0);
             }
-        // the value scale: O is in units of vref
-        float ratio = 0.f;
-        if (vs > 0.f) {
-            if (vs > vref) {
-                const float up = pow2_above(vs), f = vref / up;
-                vref = up;
-#pragma unroll
-                for (int n = 0; n < NR; ++n)
-#pragma unroll
-                    for (int d = 0; d < DT; ++d) o[n][d] *= f;
-            }
-            ratio = vs / vref;
+            if (k & 1) __builtin_amdgcn_sched_barrier(0);
         }
-        const bool mask = t0 + KV_STEP - 1 > base || t0 < sp.len - a.window * (a.window > 0);
-        f16x8_t pf[NR];
-#pragma unroll
-        for (int n = 0; n < NR; ++n) {
-            const float f = ks * cs[n];
-            float x[8];
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x[4 * i + e] = s[n][i][e] * f;
-            if (mask) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int t = t0 + 16 * (e >> 2) + 4 * g + (e & 3);
-                    bool see = t < sp.len;
-                    if (a.tree)
-                        see = see && (t < base || ((tree[n] >> ((t - base) & 31)) & 1u));
-                    else
-                        see = see && t <= pos[n] && (a.window <= 0 || t > pos[n] - a.window);
-                    x[e] = see ? x[e] : NEG_INF;
-                }
-            }
-            float top = x[0];
-#pragma unroll
-            for (int e = 1; e < 8; ++e) top = fmaxf(top, x[e]);
-            if (__any(top > m[n] + 8.f)) {
-                top = fmaxf(top, __shfl_xor(top, 16));
-                top = fmaxf(top, __shfl_xor(top, 32));
-                // only the rows concerned: a row does not depend on its neighbours
-                const float mn = top > m[n] + 8.f ? top : m[n];
-                const float down = mn == NEG_INF ? 1.f : __builtin_amdgcn_exp2f(m[n] - mn);
-                m[n] = mn;
-                l[n] *= down;
-#pragma unroll
-                for (int d = 0; d < DT; ++d) o[n][d] *= down;
-            }
-            const float ref = m[n] == NEG_INF ? 0.f : m[n];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float p = __builtin_amdgcn_exp2f(x[e] - ref);
-                l[n] += p;
-                pf[n][e] = (_Float16)(p * ratio);
-            }
-        }
-        // codes of slots behind the last token may be anything (an E4M3 NaN)
-        if (t0 + KV_STEP > sp.len) {
+        load(kw, a.k, t0 + STRIDE);
+        // codes of slots behind the last token may be anything (an E4M3 NaN),
+        // and those of a page without a value scale are worth nothing
+        if (t0 + KV_STEP > sp.len || no_v) {
             unsigned keep[2] = {0u, 0u};
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (t0 + 16 * i + 4 * g + e < sp.len) keep[i] |= 0xFFu << (8 * e);
+                for (int e = 0; e < 4; ++e) keep[i] |= (t0 + 16 * i + 4 * g + e < sp.len) & !no_v ? 0xFFu << (8 * e) : 0u;
 #pragma unroll
             for (int u = 0; u < D / 32; ++u) {
                 vw[u][0] &= keep[0];
@@ -277,8 +284,66 @@ __global__ void __launch_bounds__(AT_WAVES * 64) kv_attn_kernel(KvAttnArgs a) {
                 vw[u][3] &= keep[1];
             }
         }
+        const bool mask = !there || t0 + KV_STEP - 1 > base || t0 < sp.len - a.window * (a.window > 0);
+        f16x8_t pf[NR];
 #pragma unroll
-        for (int u = 0; u < D / 32; ++u)
+        for (int n = 0; n < NR; ++n) {
+            const float f = ks * cs[n];
+            float x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = s[n][e >> 2][e & 3] * f;
+            if (mask) {
+                const int t1 = t0 + 4 * g;  // the lane's first token
+                if (a.tree) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int t = t1 + 16 * (e >> 2) + (e & 3);
+                        const bool see = there & (t < sp.len) & ((t < base) | (((tree[n] >> ((t - base) & 31)) & 1u) != 0u));
+                        x[e] = see ? x[e] : NEG_INF;
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int t = t1 + 16 * (e >> 2) + (e & 3);
+                        x[e] = there & (t <= pos[n]) & (t > lo[n]) ? x[e] : NEG_INF;
+                    }
+                }
+            }
+            float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+            if (__any(top > m[n] + 8.f)) {
+                top = fmaxf(top, __shfl_xor(top, 16));
+                top = fmaxf(top, __shfl_xor(top, 32));
+                // only the rows concerned: a row does not depend on its neighbours
+                const float mn = top > m[n] + 8.f ? top : m[n];
+                const float down = mn == NEG_INF ? 1.f : __builtin_amdgcn_exp2f(m[n] - mn);
+                m[n] = mn;
+                nm[n] = mn == NEG_INF ? 0.f : -mn;
+                l[n] *= down;
+                ps[n] *= down;
+#pragma unroll
+                for (int d = 0; d < DT; ++d) o[n][d] *= down;
+            }
+            const float nr = nm[n] + lr;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) pf[n][e] = (_Float16)__builtin_amdgcn_exp2f(x[e] + nr);
+            // the sum of the step's p, as rounded, in every lane of the row
+            const f32x4_t t = __builtin_amdgcn_mfma_f32_16x16x32_f16(ones, pf[n], f32x4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+            ps[n] += t[0];
+            if (rr <= 8.f) {
+                l[n] = fmaf(t[0], rr, l[n]);
+            } else {
+                // values far smaller than the chunk's largest: p vs / vref may
+                // have left f16's range, so p is summed by itself
+                float sum = 0.f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sum += __builtin_amdgcn_exp2f(x[e] + nm[n]);
+                sum += __shfl_xor(sum, 16);
+                l[n] += sum + __shfl_xor(sum, 32);
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int u = 0; u < D / 32; ++u) {
 #pragma unroll
             for (int d = 0; d < 2; ++d) {
                 const f16x8_t vf = codes8<E4M3>(vw[u][2 * d], vw[u][2 * d + 1]);
@@ -286,14 +351,18 @@ __global__ void __launch_bounds__(AT_WAVES * 64) kv_attn_kernel(KvAttnArgs a) {
                 for (int n = 0; n < NR; ++n)
                     o[n][2 * u + d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, pf[n], o[n][2 * u + d], 0, 0, 0);
             }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        load(vw, a.v, t0 + STRIDE);
     }
-    // in true units, each wave its own maximum; the sum over the lanes' tokens
+    // in true units
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
-        l[n] += __shfl_xor(l[n], 16);
-        l[n] += __shfl_xor(l[n], 32);
+        const float back = -BIAS * ps[n];
 #pragma unroll
-        for (int d = 0; d < DT; ++d) o[n][d] *= vref;
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[n][d][e] = fmaf(o[n][d][e], UNIT, back) * vref;
     }
     // join the waves that split the tokens, half of them at a time
     if constexpr (TS > 1) {
@@ -307,9 +376,9 @@ __global__ void __launch_bounds__(AT_WAVES * 64) kv_attn_kernel(KvAttnArgs a) {
 #pragma unroll
                     for (int d = 0; d < DT; ++d)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) to[n * (DT * 4 + 2) + 4 * d + e][lane] = o[n][d][e];
-                    to[n * (DT * 4 + 2) + DT * 4][lane] = m[n];
-                    to[n * (DT * 4 + 2) + DT * 4 + 1][lane] = l[n];
+                        for (int e = 0; e < 4; ++e) to[n * SL + 4 * d + e][lane] = o[n][d][e];
+                    to[n * SL + DT * 4][lane] = m[n];
+                    to[n * SL + DT * 4 + 1][lane] = l[n];
                 }
             }
             __syncthreads();
@@ -317,8 +386,8 @@ __global__ void __launch_bounds__(AT_WAVES * 64) kv_attn_kernel(KvAttnArgs a) {
                 float(*from)[64] = slots[ts * RS + rsi];
 #pragma unroll
                 for (int n = 0; n < NR; ++n) {
-                    const float m2 = from[n * (DT * 4 + 2) + DT * 4][lane];
-                    const float l2 = from[n * (DT * 4 + 2) + DT * 4 + 1][lane];
+                    const float m2 = from[n * SL + DT * 4][lane];
+                    const float l2 = from[n * SL + DT * 4 + 1][lane];
                     const float mn = fmaxf(m[n], m2);
                     const float f1 = mn == NEG_INF ? 0.f : __builtin_amdgcn_exp2f(m[n] - mn);
                     const float f2 = mn == NEG_INF ? 0.f : __builtin_amdgcn_exp2f(m2 - mn);
@@ -328,7 +397,7 @@ __global__ void __launch_bounds__(AT_WAVES * 64) kv_attn_kernel(KvAttnArgs a) {
                     for (int d = 0; d < DT; ++d)
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            o[n][d][e] = o[n][d][e] * f1 + from[n * (DT * 4 + 2) + 4 * d + e][lane] * f2;
+                            o[n][d][e] = o[n][d][e] * f1 + from[n * SL + 4 * d + e][lane] * f2;
                 }
             }
         }
@@ -346,9 +415,7 @@ __global__ void __launch_bounds__(AT_WAVES * 64) kv_attn_kernel(KvAttnArgs a) {
                 if (a.out_f32)
                     *reinterpret_cast<f32x4_t *>((float *)a.out + at + 16 * d) = v;
                 else
-                    *reinterpret_cast<u32x2_t *>((uint16_t *)a.out + at + 16 * d) =
-                        u32x2_t{(unsigned)f32_to_bf16(v[0]) | ((unsigned)f32_to_bf16(v[1]) << 16),
-                                (unsigned)f32_to_bf16(v[2]) | ((unsigned)f32_to_bf16(v[3]) << 16)};
+                    *reinterpret_cast<u32x2_t *>((uint16_t *)a.out + at + 16 * d) = bf16x4(v);
             }
         } else {
             const size_t at = ((size_t)ci * a.M + rowm[n]) * a.Hq + rowh[n];
@@ -360,11 +427,17 @@ __global__ void __launch_bounds__(AT_WAVES * 64) kv_attn_kernel(KvAttnArgs a) {
     }
 }
 
-// Joins the chunks of one (query token, head): one wave, D / 64 dimensions a lane.
+// Joins the chunks of one (query token, head).  D / 4 threads take 4
+// dimensions each of one chunk; the workgroup's groups of them take the
+// chunks in turn, four loads in flight a thread, and join in LDS.
+constexpr int JOIN_T = 256;
+
 template <int D>
-__global__ void __launch_bounds__(64) kv_attn_join_kernel(KvAttnArgs a) {
-    constexpr int E = D / 64;
-    const int lane = threadIdx.x;
+__global__ void __launch_bounds__(JOIN_T) kv_attn_join_kernel(KvAttnArgs a) {
+    constexpr int TD = D / 4, NG = JOIN_T / TD, AHEAD = 4;
+    __shared__ f32x4_t so[NG][TD];
+    __shared__ float sl[NG], smx[JOIN_T / 64];
+    const int tid = threadIdx.x, gi = tid / TD, d4 = tid % TD;
     const int r = blockIdx.x / a.max_q, j = blockIdx.x % a.max_q, hq = blockIdx.y;
     const Span sp = span_of(a, r);
     if (j >= sp.T) return;
@@ -372,28 +445,49 @@ __global__ void __launch_bounds__(64) kv_attn_join_kernel(KvAttnArgs a) {
     const int n = max(min(sp.c1 - sp.c0, a.chunks), 1);
     const size_t at = (size_t)row * a.Hq + hq, step = (size_t)a.M * a.Hq;
     float mx = NEG_INF;
-    for (int c = lane; c < n; c += 64) mx = fmaxf(mx, a.part_ml[2 * (at + c * step)]);
+    for (int c = tid; c < n; c += JOIN_T) mx = fmaxf(mx, a.part_ml[2 * (at + c * step)]);
 #pragma unroll
     for (int d = 32; d; d >>= 1) mx = fmaxf(mx, __shfl_xor(mx, d));
-    float o[E], l = 0.f;
+    if ((tid & 63) == 0) smx[tid >> 6] = mx;
+    __syncthreads();
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = 0.f;
-    for (int c = 0; c < n; ++c) {
-        // (a row of NaN scores has no maximum, but a NaN sum)
-        const float f = mx == NEG_INF ? 0.f : __builtin_amdgcn_exp2f(a.part_ml[2 * (at + c * step)] - mx);
-        l += f * a.part_ml[2 * (at + c * step) + 1];
+    for (int w = 0; w < JOIN_T / 64; ++w) mx = fmaxf(mx, smx[w]);
+    f32x4_t o = {0.f, 0.f, 0.f, 0.f};
+    float l = 0.f;
+    for (int c0 = gi; c0 < n; c0 += NG * AHEAD) {
+        f32x4_t v[AHEAD];
+        f32x2_t ml[AHEAD];
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] += f * a.part[(at + c * step) * D + e * 64 + lane];
+        for (int i = 0; i < AHEAD; ++i) {
+            const int c = min(c0 + i * NG, n - 1);
+            v[i] = reinterpret_cast<const f32x4_t *>(a.part + (at + c * step) * D)[d4];
+            ml[i] = reinterpret_cast<const f32x2_t *>(a.part_ml)[at + c * step];
+        }
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            if (c0 + i * NG >= n) break;
+            // (a row of NaN scores has no maximum, but a NaN sum)
+            const float f = mx == NEG_INF ? 0.f : __builtin_amdgcn_exp2f(ml[i][0] - mx);
+            l = fmaf(f, ml[i][1], l);
+            o += v[i] * f;
+        }
+    }
+    so[gi][d4] = o;
+    if (d4 == 0) sl[gi] = l;
+    __syncthreads();
+    if (gi != 0) return;
+#pragma unroll
+    for (int k = 1; k < NG; ++k) {
+        o += so[k][d4];
+        l += sl[k];
     }
     const float f = sp.too_long ? __builtin_nanf("") : l == 0.f ? 0.f : 1.f / l;
-    const size_t to = (size_t)row * a.out_stride + (size_t)hq * D + lane;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        if (a.out_f32)
-            ((float *)a.out)[to + 64 * e] = o[e] * f;
-        else
-            ((uint16_t *)a.out)[to + 64 * e] = f32_to_bf16(o[e] * f);
-    }
+    const size_t to = (size_t)row * a.out_stride + (size_t)hq * D + 4 * d4;
+    o *= f;
+    if (a.out_f32)
+        *reinterpret_cast<f32x4_t *>((float *)a.out + to) = o;
+    else
+        *reinterpret_cast<u32x2_t *>((uint16_t *)a.out + to) = bf16x4(o);
 }
 
 void kv_attention_split(int64_t R, int64_t Hkv, int64_t rows, int64_t page, int64_t span,
@@ -413,24 +507,27 @@ void kv_attention_split(int64_t R, int64_t Hkv, int64_t rows, int64_t page, int6
 
 namespace {
 
-template <bool E4M3, int D, int NR, int RS>
+template <bool E4M3, int D, int NR, int RS, int WAVES>
 void run(const KvAttnArgs &a, hipStream_t s) {
     const int rows = a.max_q * a.G;
     const dim3 grid((unsigned)(a.R * a.Hkv * a.chunks), (unsigned)((rows + 16 * NR * RS - 1) / (16 * NR * RS)));
-    hipLaunchKernelGGL((kv_attn_kernel<E4M3, D, NR, RS>), grid, dim3(AT_WAVES * 64), 0, s, a);
+    hipLaunchKernelGGL((kv_attn_kernel<E4M3, D, NR, RS, WAVES>), grid, dim3(WAVES * 64), 0, s, a);
     if (a.chunks > 1)
-        hipLaunchKernelGGL((kv_attn_join_kernel<D>), dim3((unsigned)(a.R * a.max_q), (unsigned)a.Hq), dim3(64), 0, s, a);
+        hipLaunchKernelGGL((kv_attn_join_kernel<D>), dim3((unsigned)(a.R * a.max_q), (unsigned)a.Hq), dim3(JOIN_T), 0, s, a);
 }
 
 template <bool E4M3, int D>
 void pick(const KvAttnArgs &a, hipStream_t s) {
     const int rows = a.max_q * a.G;
+    constexpr int NR = D == 256 ? 1 : 2;  // two row tiles of 256 dimensions do not fit the registers
     if (rows <= 16)
-        run<E4M3, D, 1, 1>(a, s);
+        run<E4M3, D, 1, 1, 4>(a, s);
     else if (rows <= 32)
-        run<E4M3, D, 1, 2>(a, s);
+        run<E4M3, D, NR, 2 / NR, 4>(a, s);
+    else if (rows <= 64 || NR == 1)
+        run<E4M3, D, NR, 4 / NR, 4>(a, s);
     else
-        run<E4M3, D, 1, 4>(a, s);
+        run<E4M3, D, NR, 4, 4>(a, s);
 }
 
 }  // namespace

@@ -115,7 +115,7 @@ def append(codes, scales, x, slots, value, e4m3):
             a = np.where(np.isfinite(a), a, 0.0)
             amax = a.max() if a.max() >= 2.0 ** -100 else 0.0
             old = scales[p, h] if o else 0.0
-            new = max(old, float(f32(amax / top)))
+            new = max(old, float(f32(amax * float(f32(1.0 / top)))))
             inv = float(f32(1.0 / new)) if new > 0 else 0.0
             if o and new > old:
                 rows[p, h] = enc(f32(dec(rows[p, h]) * float(f32(old / new))))
