@@ -595,8 +595,8 @@ int kv_append_run(const qg_kv_cache *cache, int64_t M, const void *K, int64_t k_
                   const void *V, int64_t v_stride, const int32_t *slots, void *stream);
 
 /*
- * Bytes of workspace kv_attention_run needs (0 where a request's tokens are
- * not split).  Pure host function; 0 for arguments the call would refuse.
+ * Bytes of workspace kv_attention_run needs (0 for contexts so short that
+ * the work on a request's tokens is not cut).  Pure host function; 0 for arguments the call would refuse.
  */
 size_t qg_kv_attention_workspace_bytes(int64_t R, int64_t M, int64_t Hq, int64_t Hkv, int64_t D,
                                        int64_t page, int64_t max_q, int64_t max_len,
@@ -615,7 +615,7 @@ size_t qg_kv_attention_workspace_bytes(int64_t R, int64_t M, int64_t Hq, int64_t
  * Query head i reads KV head i / (Hq / Hkv).
  *
  *  cache        read only.
- *  R, M         requests, 0..65535, and rows of q and out, 0..2^30.
+ *  R, M         requests, 0..4096, and rows of q and out, 0..2^30.
  *  Hq           query heads, a multiple of Hkv, at most 8192.
  *  q            device bf16 [M][Hq][D], 16-B; rows q_stride elements apart (a
  *               multiple of 8, at least Hq * D).
@@ -628,8 +628,9 @@ size_t qg_kv_attention_workspace_bytes(int64_t R, int64_t M, int64_t Hq, int64_t
  *  scale        of the scores, finite; usually 1 / sqrt(D).
  *  max_q        1..32: no request has more new tokens.  Rows past it are not
  *               computed.
- *  max_len      1..max_blocks * page: no request is longer.  A longer one may
- *               get rows of NaN.
+ *  max_len      1..max_blocks * page: no request is longer; a longer one gets
+ *               rows of NaN.  (The product of requests, heads, row groups and
+ *               max_len / 32 has to stay below 2^31: QG_ESHAPE.)
  *  workspace    device buffer, 16-B, of qg_kv_attention_workspace_bytes; NULL
  *               if that is 0.  Scratch: calls that may overlap, or graphs
  *               that may run at once, need one each.

@@ -40,25 +40,17 @@ int check_cache(const qg_kv_cache *c) {
 
 bool row_stride(int64_t stride, int64_t width) { return stride >= width && stride % 8 == 0 && stride < STRIDE_MAX; }
 
-struct Split {
-    int chunk;
-    int64_t chunks;
-    size_t bytes;
-};
-
-// shape rules and split of an attention call (false: refused)
-bool attention_split(int64_t R, int64_t M, int64_t Hq, int64_t Hkv, int64_t D, int64_t page,
-                     int64_t max_q, int64_t max_len, int64_t window, Split *s) {
-    if (R < 0 || R > 65535 || M < 0 || M > ROWS_MAX || Hkv < 1 || Hkv > 1024 || Hq < 1 || Hq > 8192 ||
+// shape rules and plan of an attention call (false: refused)
+bool attention_plan(int64_t R, int64_t M, int64_t Hq, int64_t Hkv, int64_t D, int64_t page,
+                    int64_t max_q, int64_t max_len, int64_t window, KvAttnPlan *p, size_t *bytes) {
+    if (R < 0 || R > KV_R_MAX || M < 0 || M > ROWS_MAX || Hkv < 1 || Hkv > 1024 || Hq < 1 || Hq > 8192 ||
         Hq % Hkv || !head_size(D) || !page_size(page) || max_q < 1 || max_q > KV_ROWS_MAX ||
         max_len < 1 || max_len > LEN_MAX || window < 0 || window > LEN_MAX)
         return false;
-    const int64_t seen = window > 0 ? window + max_q - 1 : max_len;
-    kv_attention_split(R, Hkv, max_q * (Hq / Hkv), page, seen < max_len ? seen : max_len,
-                       window > 0, &s->chunk, &s->chunks);
-    if (s->chunks * M > (int64_t(1) << 33)) return false;  // the workspace's size stays in range
-    s->bytes = s->chunks > 1 ? (size_t)s->chunks * (size_t)M * (size_t)Hq * (size_t)(D + 2) * 4 : 0;
-    return R * Hkv * s->chunks < INT32_END && R * max_q < INT32_END;
+    const int64_t seen = window > 0 && window + max_q - 1 < max_len ? window + max_q - 1 : max_len;
+    if (!kv_attention_plan(R, Hkv, Hq / Hkv, D, max_q, seen, p)) return false;
+    *bytes = R == 0 || M == 0 ? 0 : (size_t)p->head_bytes + (size_t)p->part_slots * (size_t)p->part_rows * (size_t)(D + 2) * 4;
+    return true;
 }
 
 }  // namespace
@@ -109,7 +101,7 @@ int kv_tables_run(int64_t R, int64_t page, int64_t pages, int64_t max_blocks, in
                   int32_t *free_pages, int32_t *free_count, int32_t *q_start, int32_t *slots,
                   int32_t *positions, int32_t *status, void *stream) {
     try {
-        if (R < 0 || R > KV_TABLES_R_MAX || !page_size(page) || pages < 1 || pages >= INT32_END / page ||
+        if (R < 0 || R > KV_R_MAX || !page_size(page) || pages < 1 || pages >= INT32_END / page ||
             max_blocks < 1 || max_blocks > LEN_MAX / page || max_tokens < 0 || max_tokens > ROWS_MAX)
             return QG_ESHAPE;
         if (!lens || !add || !table || !free_pages || !free_count || !q_start || !status ||
@@ -178,8 +170,9 @@ int kv_append_run(const qg_kv_cache *cache, int64_t M, const void *K, int64_t k_
 size_t qg_kv_attention_workspace_bytes(int64_t R, int64_t M, int64_t Hq, int64_t Hkv, int64_t D,
                                        int64_t page, int64_t max_q, int64_t max_len,
                                        int64_t window) {
-    Split s;
-    return attention_split(R, M, Hq, Hkv, D, page, max_q, max_len, window, &s) ? s.bytes : 0;
+    KvAttnPlan p;
+    size_t bytes = 0;
+    return attention_plan(R, M, Hq, Hkv, D, page, max_q, max_len, window, &p, &bytes) ? bytes : 0;
 }
 
 int kv_attention_run(const qg_kv_cache *cache, int64_t R, int64_t M, int64_t Hq, const void *q,
@@ -194,15 +187,16 @@ int kv_attention_run(const qg_kv_cache *cache, int64_t R, int64_t M, int64_t Hq,
         if (out_dtype == QG_OUT_I32_GROUPS || (tree_mask && window != 0)) return QG_EUNSUPPORTED;
         const int st = check_cache(cache);
         if (st != QG_OK) return st;
-        Split s;
+        KvAttnPlan p;
+        size_t need = 0;
         if (max_blocks < 1 || max_blocks > LEN_MAX / cache->page ||
             max_len > max_blocks * cache->page ||
-            !attention_split(R, M, Hq, cache->Hkv, cache->D, cache->page, max_q, max_len, window, &s) ||
+            !attention_plan(R, M, Hq, cache->Hkv, cache->D, cache->page, max_q, max_len, window, &p, &need) ||
             !row_stride(q_stride, Hq * cache->D) || !row_stride(out_stride, Hq * cache->D))
             return QG_ESHAPE;
         if (!std::isfinite(scale)) return QG_EINVAL;
-        if (!q || !q_start || !lens || !table || !out || (s.bytes && !workspace)) return QG_EINVAL;
-        if (s.bytes && workspace_bytes < s.bytes) return QG_ESIZE;
+        if (!q || !q_start || !lens || !table || !out || (need && !workspace)) return QG_EINVAL;
+        if (need && workspace_bytes < need) return QG_ESIZE;
         if (!aligned(q, 16) || !aligned(q_start, 4) || !aligned(lens, 4) || !aligned(table, 4) ||
             !aligned(tree_mask, 4) || !aligned(workspace, 16) || !aligned(out, 16))
             return QG_EALIGN;
@@ -218,8 +212,9 @@ int kv_attention_run(const qg_kv_cache *cache, int64_t R, int64_t M, int64_t Hq,
         a.table = table;
         a.tree = tree_mask;
         a.out = out;
-        a.part = reinterpret_cast<float *>(workspace);
-        a.part_ml = a.part + (size_t)s.chunks * (size_t)M * (size_t)Hq * (size_t)cache->D;
+        a.head = reinterpret_cast<int32_t *>(workspace);
+        a.part = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(workspace) + p.head_bytes);
+        a.part_ml = a.part + (size_t)p.part_slots * (size_t)p.part_rows * (size_t)cache->D;
         a.q_stride = q_stride;
         a.out_stride = out_stride;
         a.pages = cache->pages;
@@ -232,8 +227,13 @@ int kv_attention_run(const qg_kv_cache *cache, int64_t R, int64_t M, int64_t Hq,
         a.max_blocks = (int)max_blocks;
         a.max_q = (int)max_q;
         a.window = (int)window;
-        a.chunks = (int)s.chunks;
-        a.chunk = s.chunk;
+        a.max_len = (int)max_len;
+        a.groups = p.groups;
+        a.slots = p.slots;
+        a.min_run = p.min_run;
+        a.part_rows = p.part_rows;
+        a.whole = p.whole;
+        a.aligned = p.aligned;
         a.scale = scale * 1.44269504088896340736f;  // scores in powers of two
         a.out_f32 = out_dtype == QG_OUT_F32;
         return hip_status(launch_kv_attention(a, cache->D, cache->fmt == QG_KV_E4M3,

@@ -17,9 +17,14 @@
 // The value scales enter p as vs / vref with vref a power of two at least as
 // large as every vs of the chunk.
 //
-// A workgroup takes one chunk of a request's tokens for one KV head and up to
-// 16 * NR * RS rows; its waves split the chunk's steps (TS of them) and the
-// rows (RS) and join in LDS.  Several chunks are joined by a second kernel.
+// The work is a line of (request, head, group of 16 NR RS rows, step).  It is
+// cut into one equal run for each of the workgroups that fit the GPU at once,
+// so that requests of any lengths load it evenly; a run's part of one
+// (request, head, row group) is a segment.  Where there are few of these
+// (batch-one decode), a cut falls on each one's start too, so that no
+// workgroup has two segments.  A workgroup's waves split the segment's steps
+// (TS of them) and the rows (RS) and join in LDS; a second kernel joins the
+// segments.  Short contexts are not cut.
 #include "kv_cache.h"
 
 namespace qg {
@@ -76,25 +81,60 @@ __device__ __forceinline__ float pow2_above(float x) {
     return __builtin_bit_cast(float, (u + 0x7FFFFFu) & 0x7F800000u);
 }
 
-// tokens [first, end) that some row of the request may see, and the chunks
-// that hold them
-struct Span {
-    int len, T, first, c0, c1;
-    bool too_long;  // longer than the call was told of: its rows become NaN
+// What a request asks for: its T query tokens see the steps (of 32 tokens)
+// from `start` on.
+struct Req {
+    int q0, T, len, start, units, groups;  // groups of RW rows
+    bool too_long;                         // longer than the call was told of: its rows become NaN
+    __device__ __forceinline__ int work(int Hkv) const { return units * groups * Hkv; }
 };
 
-__device__ __forceinline__ Span span_of(const KvAttnArgs &a, int r) {
-    Span s;
-    const int q0 = a.q_start[r];
-    s.T = min(max(a.q_start[r + 1] - q0, 0), a.max_q);
-    if (q0 < 0 || q0 + s.T > a.M) s.T = 0;
+// The kernel's arguments where the hardware left them, anew at each call: the
+// compiler reads them again there instead of holding all of them in SGPRs,
+// which are too few for that.
+typedef const __attribute__((address_space(4))) KvAttnArgs Args;
+__device__ __forceinline__ Args &args() {
+    Args *p = (Args *)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(p));
+    return *p;
+}
+
+template <int RW>
+__device__ __forceinline__ Req req_of(Args &a, int r) {
+    Req s;
+    s.q0 = a.q_start[r];
+    s.T = min(max(a.q_start[r + 1] - s.q0, 0), a.max_q);
+    if (s.q0 < 0 || s.q0 + s.T > a.M) s.T = 0;
     s.len = min(max(a.lens[r], 0), a.max_blocks * a.page);
-    s.first = a.window > 0 ? max(s.len - s.T - a.window + 1, 0) : 0;
-    s.c0 = s.first / a.chunk;
-    s.c1 = (s.len + a.chunk - 1) / a.chunk;
-    s.too_long = s.c1 - s.c0 > a.chunks;
+    s.too_long = s.len > a.max_len;
+    s.start = a.window > 0 ? max(s.len - s.T - a.window + 1, 0) & ~(KV_STEP - 1) : 0;
+    s.units = s.T == 0 ? 0 : s.too_long ? 1 : max((s.len - s.start + KV_STEP - 1) / KV_STEP, 1);
+    s.groups = (s.T * a.G + RW - 1) / RW;
     return s;
 }
+
+// Sum over the requests before `end` of their work, by the whole wave.
+template <int RW>
+__device__ __forceinline__ int work_before(Args &a, int end, int lane) {
+    if (end == 1) return __builtin_amdgcn_readfirstlane(req_of<RW>(a, 0).work(a.Hkv));
+    int sum = 0;
+    for (int r = lane; r < end; r += 64) sum += req_of<RW>(a, r).work(a.Hkv);
+#pragma unroll
+    for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d);
+    return __builtin_amdgcn_readfirstlane(sum);
+}
+
+// A workgroup's run, given all the work: equal runs, or, where a cut falls on
+// every start (`aligned`), so long that the rounded-up parts fit too.
+__device__ __forceinline__ int run_length(Args &a, int total) {
+    const unsigned n = a.aligned ? a.slots - a.R * a.Hkv * a.groups : a.slots;
+    const int u = (int)(((unsigned)total + n - 1) / n);
+    return (max(u, a.min_run) + a.min_run - 1) / a.min_run * a.min_run;
+}
+
+// The start of the workspace: the run's length and where each request's work
+// starts on the line, for the second kernel.
+constexpr int64_t PART_HEAD = 4 * (KV_R_MAX + 4);
 
 }  // namespace
 
@@ -108,74 +148,156 @@ __device__ __forceinline__ void load_codes(u32x4_t (&to)[N], const uint8_t *bloc
 #pragma unroll
     for (int u = 0; u < N; ++u)
         to[u] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
-                                                r, 16 * lane + u % 4 * 1024, (int)at + u / 4 * 4096, NT ? 2 : 0));
+                                                r, 16 * lane, (int)at + u * 1024, NT ? 2 : 0));
 }
 
 template <bool E4M3, int D, int NR, int RS, int WAVES>
-__global__ void __launch_bounds__(WAVES * 64, 2) kv_attn_kernel(KvAttnArgs a) {
+__global__ void __launch_bounds__(WAVES * 64, NR == 1 && D <= 128 && WAVES == 4 ? 3 : 2) kv_attn_kernel(KvAttnArgs) {
     constexpr int TS = WAVES / RS;      // waves that split the tokens
     constexpr int KS = D / 32;          // MFMA steps of Q K^T
     constexpr int DT = D / 16;          // tiles of O
     constexpr int SL = DT * 4 + 2;      // floats a lane and row tile joins
     constexpr float UNIT = Code<E4M3>::unit, BIAS = Code<E4M3>::bias;
-    constexpr bool NT = RS == 1;        // read by one wave only: past the caches
-    __shared__ float slots[TS > 1 ? (TS / 2) * RS : 1][TS > 1 ? NR * SL : 1][64];
+    constexpr int KB = D / 32;          // kilobytes of keys, and of values, of a step
+    // Several waves that take different rows of the same tokens share a
+    // step's codes through LDS; a wave alone reads them into its registers,
+    // past the caches.
+    constexpr bool SHARED = RS > 1;
+    constexpr int PART = 2 * KB / RS;   // kilobytes each of them brings
+    constexpr int STAGE = SHARED ? 2 * TS * 2 * KB * 64 : 0;
+    constexpr int JOIN = TS > 1 ? (TS / 2) * RS * NR * SL * 16 : 0;
+    __shared__ u32x4_t lds[STAGE > JOIN ? STAGE : JOIN > 0 ? JOIN : 1];
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g = lane >> 4, c = lane & 15;
     const int ts = wave / RS, rsi = wave % RS;
-    // chunk index slowest: workgroups go to the XCDs in turn, and most late
-    // chunks are empty where lengths differ
-    const int nrh = a.R * a.Hkv;
-    const int ci = blockIdx.x / nrh, rh = blockIdx.x % nrh;
-    const int r = rh / a.Hkv, h = rh % a.Hkv;
-    const Span sp = span_of(a, r);
-    const int rows = sp.T * a.G;
-    const int row0 = blockIdx.y * (16 * NR * RS);
-    if (row0 >= rows) return;
-    const int chunk = sp.c0 + ci;
-    if (chunk >= sp.c1 && !(ci == 0 && sp.c0 >= sp.c1)) return;  // chunk 0 of an empty request writes zeros
-    const int q0 = a.q_start[r];
-    const int base = sp.len - sp.T;  // position of the first query token
+    constexpr int RW = 16 * NR * RS;
+    const int shift = __builtin_ctz(args().page);
+    const int per = args().Hkv * args().groups;  // (head, row group) pairs of a request
 
-    // the chunk's pages and their scales, one a lane
-    const int t_lo = max(chunk * a.chunk, sp.first & ~(KV_STEP - 1));
-    const int t_hi = min((chunk + 1) * a.chunk, sp.len);
-    const int page0 = t_lo / a.page;
-    int my_page = -1;
-    float my_ks = 0.f, my_vs = 0.f;
-    if (page0 + lane < a.max_blocks && (page0 + lane) * a.page < t_hi) {
-        my_page = a.table[(size_t)r * a.max_blocks + page0 + lane];
-        if (my_page < 0 || my_page >= a.pages) my_page = -1;
-        if (my_page >= 0) {
-            my_ks = a.k_scales[(size_t)my_page * a.Hkv + h];
-            my_vs = a.v_scales[(size_t)my_page * a.Hkv + h];
+    // this workgroup's run [x, end) of the line, and the request it starts in
+    int r, x, end, before;
+    const bool whole = args().whole;
+    if (whole) {
+        r = blockIdx.x / per;
+        x = end = before = 0;
+    } else {
+        Args &a = args();
+        int len = 0, unit = 1;  // steps are counted in `unit`s
+        len = run_length(a, work_before<RW>(a, a.R, lane));
+        if (a.aligned) {
+            unit = len;
+            len = 1;
         }
-    }
-    // vref: a power of two at least as large as every value scale of the chunk
-    float vref = fmaxf(my_vs, 0.f);
+        x = blockIdx.x * len;
+        end = x + len;
+        before = 0;
+        r = -1;
+        // the request that x falls into; the first workgroup goes through all
+        // of them and leaves their starts for the second kernel
+        const bool leave = blockIdx.x == 0 && wave == 0;
+        if (leave && lane == 0) a.head[0] = a.aligned ? unit : len;
+        int sum = 0;
+        if (a.R == 1) {
+            const Req q = req_of<RW>(a, 0);
+            if (x < (q.units + unit - 1) / unit * q.groups * a.Hkv) r = 0;
+            if (leave && lane == 0) a.head[1] = 0;
+        } else
+            for (int r0 = 0; r0 < a.R && (r < 0 || leave); r0 += 64) {
+            int w = 0;
+            if (r0 + lane < a.R) {
+                const Req q = req_of<RW>(a, r0 + lane);
+                w = (q.units + unit - 1) / unit * q.groups * a.Hkv;
+            }
+            int upto = w;
 #pragma unroll
-    for (int d = 32; d; d >>= 1) vref = fmaxf(vref, __shfl_xor(vref, d));
-    vref = readlane_f(vref > 0.f ? pow2_above(vref) : 1.f, 0);
-    // the page's value scale over vref, as a power of two in the exponent, and
-    // its inverse (a page whose values are all 0: no scale)
-    const bool my_v = my_vs > 0.f;
-    const float my_lr = my_v ? __builtin_amdgcn_logf(my_vs / vref) : 0.f, my_rr = my_v ? vref / my_vs : 1.f;
-    const int shift = __builtin_ctz(a.page);
-    // the loads of the step at t (past the end, or of a page that is not
-    // there: none)
-    u32x4_t kw[D / 32], vw[D / 32];
+            for (int d = 1; d < 64; d <<= 1) {
+                const int u = __shfl_up(upto, d);
+                if (lane >= d) upto += u;
+            }
+            if (leave && r0 + lane < a.R) a.head[1 + r0 + lane] = sum + upto - w;
+            const unsigned long long past = __ballot(sum + upto > x);
+            if (r < 0 && past) {
+                const int i = __builtin_ctzll(past);
+                r = r0 + i;
+                before = sum + __builtin_amdgcn_readlane(upto - w, i);
+            }
+            sum += __builtin_amdgcn_readlane(upto, 63);
+        }
+        if (r < 0) return;
+        if (a.aligned) end = -unit;  // one segment
+    }
+    for (;;) {  // segments
+    Args &a = args();
+    const Req rq = req_of<RW>(a, r);
+    const int rows = rq.T * a.G;
+    int h, rgi, u0, u1;
+    if (whole) {
+        const int pair = blockIdx.x % per;
+        h = pair / a.groups;
+        rgi = pair % a.groups;
+        u0 = 0;
+        u1 = rq.units;
+        if (rgi * RW >= rows) return;
+    } else {
+        // (aligned: end = -(length of a segment), x counts segments)
+        const int parts = end < 0 ? (rq.units - end - 1) / -end : rq.units;
+        const int pair = (x - before) / parts, u = (x - before) % parts;
+        h = pair / rq.groups;
+        rgi = pair % rq.groups;
+        u0 = end < 0 ? u * -end : u;
+        u1 = min(rq.units, end < 0 ? u0 - end : u0 + end - x);
+    }
+    const bool all = u0 == 0 && u1 == rq.units;  // not cut
+    const int row0 = rgi * RW, base = rq.len - rq.T;  // base: position of the first query token
+    const int t_begin = rq.start + u0 * KV_STEP, t_end = rq.too_long ? 0 : min(rq.start + u1 * KV_STEP, rq.len);
+
+    // up to 64 pages from the step at t_lo on, and their scales, one a lane
+    int t_lo = t_begin, t_hi = t_begin, page0 = 0, my_page = -1;
+    float my_ks = 0.f, my_vs = 0.f, my_lr = 0.f, my_rr = 1.f, vref = 0.f;
+    const auto pages = [&](int t) {
+        t_lo = t;
+        page0 = t >> shift;
+        t_hi = min(t_end, (page0 + 64) << shift);
+        my_page = -1;
+        my_ks = my_vs = 0.f;
+        if ((page0 + lane) << shift < t_hi) {
+            my_page = a.table[(size_t)r * a.max_blocks + page0 + lane];
+            if (my_page < 0 || my_page >= a.pages) my_page = -1;
+            if (my_page >= 0) {
+                my_ks = a.k_scales[(size_t)my_page * a.Hkv + h];
+                my_vs = a.v_scales[(size_t)my_page * a.Hkv + h];
+            }
+        }
+    };
+    pages(t_begin);
+    // N kilobytes of the step at t from `skip` on (past the end, or of a page
+    // that is not there: none)
     const auto page_at = [&](int t) { return t < t_hi ? __builtin_amdgcn_readlane(my_page, (t >> shift) - page0) : -1; };
-    const auto load = [&](u32x4_t(&to)[D / 32], const uint8_t *codes, int t) {
+    const auto load = [&](auto &to, const uint8_t *codes, int t, unsigned skip) {
         const int page = page_at(t);
         const size_t at = ((size_t)max(page, 0) * a.Hkv + h) * ((size_t)a.page * D);
-        load_codes<D / 32, NT>(to, uniform_ptr(codes + at), page < 0 ? 0u : (unsigned)a.page * D,
-                               (unsigned)(t & (a.page - 1)) * D, lane);
+        load_codes<sizeof(to) / 16, !SHARED>(to, uniform_ptr(codes + at), page < 0 ? 0u : (unsigned)a.page * D,
+                                             (unsigned)(t & (a.page - 1)) * D + skip, lane);
     };
-    const int first = t_lo + ts * KV_STEP;
-    load(kw, a.k, first);
-    load(vw, a.v, first);
+    constexpr int STRIDE = TS * KV_STEP;
+    u32x4_t kw[SHARED ? 1 : KB], vw[SHARED ? 1 : KB];    // a wave alone: one step
+    u32x4_t st0[SHARED ? PART : 1], st1[SHARED ? PART : 1];  // sharing: its part of two steps
+    const bool st_v = rsi * 2 >= RS;
+    const uint8_t *st_codes = st_v ? a.v : a.k;
+    const unsigned st_skip = 1024u * PART * (st_v ? rsi - RS / 2 : rsi);
+    const auto first_loads = [&]() {
+        const int first = t_lo + ts * KV_STEP;
+        if constexpr (SHARED) {
+            load(st0, st_codes, first, st_skip);
+            load(st1, st_codes, first + STRIDE, st_skip);
+        } else {
+            load(kw, a.k, first, 0);
+            load(vw, a.v, first, 0);
+        }
+    };
+    first_loads();
 
     // Q, as f16 in the K tiles' order of dimensions
     f16x8_t qf[NR][KS];
@@ -187,12 +309,12 @@ __global__ void __launch_bounds__(WAVES * 64, 2) kv_attn_kernel(KvAttnArgs a) {
         const int row = row0 + 16 * (rsi * NR + n) + c;
         const bool valid = row < rows;
         const int j = valid ? row / a.G : 0;
-        rowm[n] = valid ? q0 + j : -1;
+        rowm[n] = valid ? rq.q0 + j : -1;
         rowh[n] = h * a.G + (valid ? row % a.G : 0);
         pos[n] = base + j;
         lo[n] = a.window > 0 ? pos[n] - a.window : -1;
-        tree[n] = a.tree && valid ? a.tree[q0 + j] : 0u;
-        const uint16_t *q = a.q + (size_t)(q0 + j) * a.q_stride + (size_t)rowh[n] * D;
+        tree[n] = a.tree && valid ? a.tree[rq.q0 + j] : 0u;
+        const uint16_t *q = a.q + (size_t)(rq.q0 + j) * a.q_stride + (size_t)rowh[n] * D;
         float v[KS][8];
         float top = 0.f;
 #pragma unroll
@@ -240,10 +362,10 @@ __global__ void __launch_bounds__(WAVES * 64, 2) kv_attn_kernel(KvAttnArgs a) {
     const f16x8_t ones = {(_Float16)1.f, (_Float16)1.f, (_Float16)1.f, (_Float16)1.f,
                           (_Float16)1.f, (_Float16)1.f, (_Float16)1.f, (_Float16)1.f};
 
-    // A step's keys are replaced by the next step's once they are used, then
-    // its values: one buffer each, with loads in flight all the time.
-    constexpr int STRIDE = TS * KV_STEP;
-    for (int t0 = first; t0 < t_hi; t0 += STRIDE) {
+    // One step.  A wave alone replaces its keys by the next step's once they
+    // are used, then its values: one buffer each, with loads in flight all the
+    // time.  `buf`: where the shared codes lie.
+    const auto compute = [&](int t0, const u32x4_t *buf) {
         // a page that is not there is not attended to
         const bool there = page_at(t0) >= 0;
         const int pi = (t0 >> shift) - page0;
@@ -259,7 +381,8 @@ __global__ void __launch_bounds__(WAVES * 64, 2) kv_attn_kernel(KvAttnArgs a) {
         for (int k = 0; k < KS; ++k) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const u32x4_t w = kw[i * (D / 64) + (k >> 1)];
+                const int kb = i * (D / 64) + (k >> 1);
+                const u32x4_t w = SHARED ? buf[kb * 64 + lane] : kw[SHARED ? 0 : kb];
                 const f16x8_t kf = codes8<E4M3>(w[2 * (k & 1)], w[2 * (k & 1) + 1]);
 #pragma unroll
                 for (int n = 0; n < NR; ++n)
@@ -267,24 +390,20 @@ __global__ void __launch_bounds__(WAVES * 64, 2) kv_attn_kernel(KvAttnArgs a) {
             }
             if (k & 1) __builtin_amdgcn_sched_barrier(0);
         }
-        load(kw, a.k, t0 + STRIDE);
+        if constexpr (!SHARED) load(kw, a.k, t0 + STRIDE, 0);
         // codes of slots behind the last token may be anything (an E4M3 NaN),
         // and those of a page without a value scale are worth nothing
-        if (t0 + KV_STEP > sp.len || no_v) {
-            unsigned keep[2] = {0u, 0u};
+        const bool cut = t0 + KV_STEP > rq.len || no_v;
+        unsigned keep[2] = {~0u, ~0u};
+        if (cut) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < 2; ++i) {
+                keep[i] = 0u;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) keep[i] |= (t0 + 16 * i + 4 * g + e < sp.len) & !no_v ? 0xFFu << (8 * e) : 0u;
-#pragma unroll
-            for (int u = 0; u < D / 32; ++u) {
-                vw[u][0] &= keep[0];
-                vw[u][1] &= keep[1];
-                vw[u][2] &= keep[0];
-                vw[u][3] &= keep[1];
+                for (int e = 0; e < 4; ++e) keep[i] |= (t0 + 16 * i + 4 * g + e < rq.len) & !no_v ? 0xFFu << (8 * e) : 0u;
             }
         }
-        const bool mask = !there || t0 + KV_STEP - 1 > base || t0 < sp.len - a.window * (a.window > 0);
+        const bool mask = !there || t0 + KV_STEP - 1 > base || t0 < rq.len - a.window * (a.window > 0);
         f16x8_t pf[NR];
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
@@ -298,7 +417,7 @@ __global__ void __launch_bounds__(WAVES * 64, 2) kv_attn_kernel(KvAttnArgs a) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const int t = t1 + 16 * (e >> 2) + (e & 3);
-                        const bool see = there & (t < sp.len) & ((t < base) | (((tree[n] >> ((t - base) & 31)) & 1u) != 0u));
+                        const bool see = there & (t < rq.len) & ((t < base) | (((tree[n] >> ((t - base) & 31)) & 1u) != 0u));
                         x[e] = see ? x[e] : NEG_INF;
                     }
                 } else {
@@ -343,17 +462,69 @@ __global__ void __launch_bounds__(WAVES * 64, 2) kv_attn_kernel(KvAttnArgs a) {
         }
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int u = 0; u < D / 32; ++u) {
+        for (int u = 0; u < KB; ++u) {
+            u32x4_t w = SHARED ? buf[(KB + u) * 64 + lane] : vw[SHARED ? 0 : u];
+            w[0] &= keep[0];
+            w[1] &= keep[1];
+            w[2] &= keep[0];
+            w[3] &= keep[1];
 #pragma unroll
             for (int d = 0; d < 2; ++d) {
-                const f16x8_t vf = codes8<E4M3>(vw[u][2 * d], vw[u][2 * d + 1]);
+                const f16x8_t vf = codes8<E4M3>(w[2 * d], w[2 * d + 1]);
 #pragma unroll
                 for (int n = 0; n < NR; ++n)
                     o[n][2 * u + d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, pf[n], o[n][2 * u + d], 0, 0, 0);
             }
             __builtin_amdgcn_sched_barrier(0);
         }
-        load(vw, a.v, t0 + STRIDE);
+        if constexpr (!SHARED) load(vw, a.v, t0 + STRIDE, 0);
+    };
+    if constexpr (TS > 1 || SHARED) __syncthreads();  // LDS is free of the last segment
+    while (t_lo < t_end) {  // windows of 64 pages
+        // vref: a power of two at least as large as every value scale so far;
+        // a page's scale over it, as a power of two in the exponent, and its
+        // inverse (a page whose values are all 0 has no scale)
+        float up = fmaxf(my_vs, 0.f);
+#pragma unroll
+        for (int d = 32; d; d >>= 1) up = fmaxf(up, __shfl_xor(up, d));
+        up = readlane_f(up, 0);
+        if (t_lo == t_begin || up > vref) {
+            up = up > 0.f ? pow2_above(up) : 1.f;
+            const float f = vref / up;
+            vref = up;
+#pragma unroll
+            for (int n = 0; n < NR; ++n) {
+                ps[n] *= f;
+#pragma unroll
+                for (int d = 0; d < DT; ++d) o[n][d] *= f;
+            }
+        }
+        my_lr = my_vs > 0.f ? __builtin_amdgcn_logf(my_vs / vref) : 0.f;
+        my_rr = my_vs > 0.f ? vref / my_vs : 1.f;
+        if constexpr (SHARED) {
+            // two steps' parts in registers, two in LDS: a part is written to
+            // LDS while the next one's loads run, and one barrier a step tells
+            // that all parts are there (and that the step before the last is
+            // used up)
+            u32x4_t *mine = lds + (ts * 2 * KB + (st_v ? KB : 0)) * 64 + (st_skip / 16) + lane;
+            const auto stage = [&](u32x4_t(&st)[PART], int t, int b) {
+                u32x4_t *to = mine + b * (TS * 2 * KB * 64);
+#pragma unroll
+                for (int u = 0; u < PART; ++u) to[u * 64] = st[u];
+                load(st, st_codes, t + 2 * STRIDE, st_skip);
+                __syncthreads();
+                if (t < t_hi) compute(t, lds + (b * TS + ts) * 2 * KB * 64);
+            };
+            for (int t0 = t_lo; t0 < t_hi; t0 += 2 * STRIDE) {
+                stage(st0, t0 + ts * KV_STEP, 0);
+                stage(st1, t0 + STRIDE + ts * KV_STEP, 1);
+            }
+        } else {
+            for (int t0 = t_lo + ts * KV_STEP; t0 < t_hi; t0 += STRIDE) compute(t0, nullptr);
+        }
+        if (t_hi >= t_end) break;
+        pages(t_hi);
+        first_loads();
     }
     // in true units
 #pragma unroll
@@ -370,7 +541,7 @@ __global__ void __launch_bounds__(WAVES * 64, 2) kv_attn_kernel(KvAttnArgs a) {
         for (int half = TS / 2; half; half >>= 1) {
             __syncthreads();
             if (ts >= half && ts < 2 * half) {
-                float(*to)[64] = slots[(ts - half) * RS + rsi];
+                float(*to)[64] = reinterpret_cast<float(*)[64]>(lds) + ((ts - half) * RS + rsi) * (NR * SL);
 #pragma unroll
                 for (int n = 0; n < NR; ++n) {
 #pragma unroll
@@ -383,7 +554,7 @@ __global__ void __launch_bounds__(WAVES * 64, 2) kv_attn_kernel(KvAttnArgs a) {
             }
             __syncthreads();
             if (ts < half) {
-                float(*from)[64] = slots[ts * RS + rsi];
+                float(*from)[64] = reinterpret_cast<float(*)[64]>(lds) + (ts * RS + rsi) * (NR * SL);
 #pragma unroll
                 for (int n = 0; n < NR; ++n) {
                     const float m2 = from[n * SL + DT * 4][lane];
@@ -402,56 +573,85 @@ __global__ void __launch_bounds__(WAVES * 64, 2) kv_attn_kernel(KvAttnArgs a) {
             }
         }
     }
-    if (ts != 0) return;
+    if (ts == 0) {
+        Args &a = args();
 #pragma unroll
-    for (int n = 0; n < NR; ++n) {
-        if (rowm[n] < 0) continue;
-        if (a.chunks == 1) {
-            const float f = sp.too_long ? __builtin_nanf("") : l[n] == 0.f ? 0.f : 1.f / l[n];
-            const size_t at = (size_t)rowm[n] * a.out_stride + (size_t)rowh[n] * D + 4 * g;
+        for (int n = 0; n < NR; ++n) {
+            if (rowm[n] < 0) continue;
+            if (all) {
+                const float f = rq.too_long ? __builtin_nanf("") : l[n] == 0.f ? 0.f : 1.f / l[n];
+                const size_t at = (size_t)rowm[n] * a.out_stride + (size_t)rowh[n] * D + 4 * g;
 #pragma unroll
-            for (int d = 0; d < DT; ++d) {
-                const f32x4_t v = o[n][d] * f;
-                if (a.out_f32)
-                    *reinterpret_cast<f32x4_t *>((float *)a.out + at + 16 * d) = v;
-                else
-                    *reinterpret_cast<u32x2_t *>((uint16_t *)a.out + at + 16 * d) = bf16x4(v);
+                for (int d = 0; d < DT; ++d) {
+                    const f32x4_t v = o[n][d] * f;
+                    if (a.out_f32)
+                        *reinterpret_cast<f32x4_t *>((float *)a.out + at + 16 * d) = v;
+                    else
+                        *reinterpret_cast<u32x2_t *>((uint16_t *)a.out + at + 16 * d) = bf16x4(v);
+                }
+            } else {
+                // its place: segments and pairs both only go up along the line
+                const size_t at = (size_t)(blockIdx.x + (end < 0 ? 0 : r * per + h * rq.groups + rgi)) * a.part_rows + 16 * (rsi * NR + n) + c;
+#pragma unroll
+                for (int d = 0; d < DT; ++d)
+                    *reinterpret_cast<f32x4_t *>(a.part + at * D + 16 * d + 4 * g) = o[n][d];
+                if (g == 0) *reinterpret_cast<f32x2_t *>(a.part_ml + 2 * at) = f32x2_t{m[n], l[n]};
             }
-        } else {
-            const size_t at = ((size_t)ci * a.M + rowm[n]) * a.Hq + rowh[n];
-#pragma unroll
-            for (int d = 0; d < DT; ++d)
-                *reinterpret_cast<f32x4_t *>(a.part + at * D + 16 * d + 4 * g) = o[n][d];
-            if (g == 0) *reinterpret_cast<f32x2_t *>(a.part_ml + 2 * at) = f32x2_t{m[n], l[n]};
         }
+    }
+    if (whole) return;
+    x += u1 - u0;
+    if (x >= end) return;  // (aligned: end < 0)
+    if (x - before >= rq.work(a.Hkv)) {  // on to the next request that has work
+        before = x;
+        do ++r;
+        while (r < a.R && req_of<RW>(a, r).units == 0);
+        if (r >= a.R) return;
+    }
     }
 }
 
-// Joins the chunks of one (query token, head).  D / 4 threads take 4
-// dimensions each of one chunk; the workgroup's groups of them take the
-// chunks in turn, four loads in flight a thread, and join in LDS.
-constexpr int JOIN_T = 256;
-
-template <int D>
-__global__ void __launch_bounds__(JOIN_T) kv_attn_join_kernel(KvAttnArgs a) {
-    constexpr int TD = D / 4, NG = JOIN_T / TD, AHEAD = 4;
-    __shared__ f32x4_t so[NG][TD];
-    __shared__ float sl[NG], smx[JOIN_T / 64];
-    const int tid = threadIdx.x, gi = tid / TD, d4 = tid % TD;
-    const int r = blockIdx.x / a.max_q, j = blockIdx.x % a.max_q, hq = blockIdx.y;
-    const Span sp = span_of(a, r);
-    if (j >= sp.T) return;
-    const int row = a.q_start[r] + j;
-    const int n = max(min(sp.c1 - sp.c0, a.chunks), 1);
-    const size_t at = (size_t)row * a.Hq + hq, step = (size_t)a.M * a.Hq;
+// Joins the segments of a (query token, head), where there are several: W
+// waves for each.  D / 4 lanes take 4 dimensions each of one segment; the
+// waves' groups of them take the segments in turn, eight loads in flight a
+// lane, and join across lanes and in LDS.  Many rows take one wave each, few
+// rows eight.
+template <int D, int RW, int W>
+__global__ void __launch_bounds__(512) kv_attn_join_kernel(KvAttnArgs) {
+    constexpr int TD = D / 4, NG = W * 64 / TD, AHEAD = 8, ROWS = 8 / W;
+    __shared__ f32x4_t so[W > 1 ? W : 1][TD];
+    __shared__ float sl[W], smx[W];
+    Args &a = args();
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wi = wave % W, tid = wi * 64 + lane, gi = tid / TD, d4 = tid % TD;
+    const int which = blockIdx.x * ROWS + wave / W;  // (request, token, head)
+    const int r = which / (a.max_q * a.Hq), j = which / a.Hq % a.max_q, hq = which % a.Hq;
+    if (r >= a.R) return;
+    const Req rq = req_of<RW>(a, r);
+    if (j >= rq.T) return;
+    const int row = j * a.G + hq % a.G, pair = (hq / a.G) * rq.groups + row / RW;
+    const int len = a.head[0], before = a.head[1 + r];
+    int w0, n;
+    if (a.aligned) {
+        n = (rq.units + len - 1) / len;
+        w0 = before + pair * n;
+    } else {
+        const int x = before + pair * rq.units;
+        w0 = x / len;
+        n = (x + rq.units - 1) / len - w0 + 1;
+    }
+    if (n == 1) return;  // not cut: written already
+    const size_t at = (size_t)(w0 + (a.aligned ? 0 : r * a.Hkv * a.groups + pair)) * a.part_rows + row % RW, step = a.part_rows;
     float mx = NEG_INF;
-    for (int c = tid; c < n; c += JOIN_T) mx = fmaxf(mx, a.part_ml[2 * (at + c * step)]);
+    for (int c = tid; c < n; c += W * 64) mx = fmaxf(mx, a.part_ml[2 * (at + c * step)]);
 #pragma unroll
     for (int d = 32; d; d >>= 1) mx = fmaxf(mx, __shfl_xor(mx, d));
-    if ((tid & 63) == 0) smx[tid >> 6] = mx;
-    __syncthreads();
+    if constexpr (W > 1) {
+        if (lane == 0) smx[wi] = mx;
+        __syncthreads();
 #pragma unroll
-    for (int w = 0; w < JOIN_T / 64; ++w) mx = fmaxf(mx, smx[w]);
+        for (int w = 0; w < W; ++w) mx = fmaxf(mx, smx[w]);
+    }
     f32x4_t o = {0.f, 0.f, 0.f, 0.f};
     float l = 0.f;
     for (int c0 = gi; c0 < n; c0 += NG * AHEAD) {
@@ -460,29 +660,40 @@ __global__ void __launch_bounds__(JOIN_T) kv_attn_join_kernel(KvAttnArgs a) {
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
             const int c = min(c0 + i * NG, n - 1);
-            v[i] = reinterpret_cast<const f32x4_t *>(a.part + (at + c * step) * D)[d4];
-            ml[i] = reinterpret_cast<const f32x2_t *>(a.part_ml)[at + c * step];
+            v[i] = *reinterpret_cast<const f32x4_t *>(a.part + (at + c * step) * D + 4 * d4);
+            ml[i] = *reinterpret_cast<const f32x2_t *>(a.part_ml + 2 * (at + c * step));
         }
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
-            if (c0 + i * NG >= n) break;
             // (a row of NaN scores has no maximum, but a NaN sum)
             const float f = mx == NEG_INF ? 0.f : __builtin_amdgcn_exp2f(ml[i][0] - mx);
-            l = fmaf(f, ml[i][1], l);
-            o += v[i] * f;
+            if (c0 + i * NG < n) {
+                l = fmaf(f, ml[i][1], l);
+                o += v[i] * f;
+            }
         }
     }
-    so[gi][d4] = o;
-    if (d4 == 0) sl[gi] = l;
-    __syncthreads();
-    if (gi != 0) return;
+    // the wave's groups of lanes, then the waves
 #pragma unroll
-    for (int k = 1; k < NG; ++k) {
-        o += so[k][d4];
-        l += sl[k];
+    for (int d = TD; d < 64; d <<= 1) {
+        l += __shfl_xor(l, d);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] += __shfl_xor(o[e], d);
     }
-    const float f = sp.too_long ? __builtin_nanf("") : l == 0.f ? 0.f : 1.f / l;
-    const size_t to = (size_t)row * a.out_stride + (size_t)hq * D + 4 * d4;
+    if constexpr (W > 1) {
+        if (lane < TD) so[wi][lane] = o;
+        if (lane == 0) sl[wi] = l;
+        __syncthreads();
+        if (wi != 0) return;
+#pragma unroll
+        for (int k = 1; k < W; ++k) {
+            o += so[k][lane % TD];
+            l += sl[k];
+        }
+    }
+    if (lane >= TD) return;
+    const float f = l == 0.f ? 0.f : 1.f / l;
+    const size_t to = (size_t)(rq.q0 + j) * a.out_stride + (size_t)hq * D + 4 * d4;
     o *= f;
     if (a.out_f32)
         *reinterpret_cast<f32x4_t *>((float *)a.out + to) = o;
@@ -490,47 +701,77 @@ __global__ void __launch_bounds__(JOIN_T) kv_attn_join_kernel(KvAttnArgs a) {
         *reinterpret_cast<u32x2_t *>((uint16_t *)a.out + to) = bf16x4(o);
 }
 
-void kv_attention_split(int64_t R, int64_t Hkv, int64_t rows, int64_t page, int64_t span,
-                        bool windowed, int *chunk, int64_t *chunks) {
-    const int64_t groups = (R > 0 ? R : 1) * Hkv * ((rows + 127) / 128);
-    // about four workgroups to a CU
-    const int64_t want = (1024 + groups - 1) / groups;
-    int64_t c = (span + want - 1) / want;
-    if (c < 128) c = 128;
-    if (c > KV_CHUNK_MAX) c = KV_CHUNK_MAX;
-    const int64_t unit = page > 128 ? page : 128;
-    c = (c + unit - 1) / unit * unit;
-    *chunk = (int)c;
-    // a window need not start where a chunk does
-    *chunks = (span + c - 1) / c + (windowed ? 1 : 0);
-}
-
 namespace {
 
-template <bool E4M3, int D, int NR, int RS, int WAVES>
+// The variant for a call's rows (query tokens * heads to a KV head): row tiles
+// a wave holds, waves that take different rows.
+struct Shape {
+    int NR, RS;
+};
+
+constexpr Shape shape_of(int D, int64_t rows) {
+    if (rows <= 16) return {1, 1};
+    if (D == 256) return {1, rows <= 32 ? 2 : 4};  // two row tiles of 256 dimensions do not fit the registers
+    return {2, rows <= 32 ? 1 : rows <= 64 ? 2 : 4};
+}
+
+constexpr int WAVES = 4;
+// Contexts up to here are not cut: a second launch would cost more than the
+// steps that the waves of a workgroup then take in turn.  With 16 rows or
+// fewer to a KV head 8 waves take them (1021 tokens, one request: 12.4 us
+// uncut, 13.7 with 4 waves, 13.0 cut; 2048: 16.7 and 13.2 cut).
+constexpr int WHOLE_WAVES = 8, WHOLE_MAX_8 = 1024, WHOLE_MAX_4 = 512;
+
+template <bool E4M3, int D, int NR, int RS>
 void run(const KvAttnArgs &a, hipStream_t s) {
-    const int rows = a.max_q * a.G;
-    const dim3 grid((unsigned)(a.R * a.Hkv * a.chunks), (unsigned)((rows + 16 * NR * RS - 1) / (16 * NR * RS)));
-    hipLaunchKernelGGL((kv_attn_kernel<E4M3, D, NR, RS, WAVES>), grid, dim3(WAVES * 64), 0, s, a);
-    if (a.chunks > 1)
-        hipLaunchKernelGGL((kv_attn_join_kernel<D>), dim3((unsigned)(a.R * a.max_q), (unsigned)a.Hq), dim3(JOIN_T), 0, s, a);
+    const unsigned grid = a.whole ? (unsigned)(a.R * a.Hkv * a.groups) : (unsigned)a.slots;
+    if constexpr (RS == 1 && NR == 1 && D <= 128)
+        if (a.whole) {
+            hipLaunchKernelGGL((kv_attn_kernel<E4M3, D, NR, RS, WHOLE_WAVES>), dim3(grid), dim3(WHOLE_WAVES * 64), 0, s, a);
+            return;
+        }
+    hipLaunchKernelGGL((kv_attn_kernel<E4M3, D, NR, RS, WAVES>), dim3(grid), dim3(WAVES * 64), 0, s, a);
+    if (a.whole) return;
+    const int64_t joins = (int64_t)a.R * a.max_q * a.Hq;
+    if (joins >= 1024)
+        hipLaunchKernelGGL((kv_attn_join_kernel<D, 16 * NR * RS, 1>), dim3((unsigned)((joins + 7) / 8)), dim3(512), 0, s, a);
+    else
+        hipLaunchKernelGGL((kv_attn_join_kernel<D, 16 * NR * RS, 8>), dim3((unsigned)joins), dim3(512), 0, s, a);
 }
 
 template <bool E4M3, int D>
 void pick(const KvAttnArgs &a, hipStream_t s) {
-    const int rows = a.max_q * a.G;
-    constexpr int NR = D == 256 ? 1 : 2;  // two row tiles of 256 dimensions do not fit the registers
-    if (rows <= 16)
-        run<E4M3, D, 1, 1, 4>(a, s);
-    else if (rows <= 32)
-        run<E4M3, D, NR, 2 / NR, 4>(a, s);
-    else if (rows <= 64 || NR == 1)
-        run<E4M3, D, NR, 4 / NR, 4>(a, s);
+    const Shape v = shape_of(D, a.max_q * a.G);
+    if constexpr (D == 256)
+        v.RS == 1 ? run<E4M3, D, 1, 1>(a, s) : v.RS == 2 ? run<E4M3, D, 1, 2>(a, s) : run<E4M3, D, 1, 4>(a, s);
+    else if (v.NR == 1)
+        run<E4M3, D, 1, 1>(a, s);
     else
-        run<E4M3, D, NR, 4, 4>(a, s);
+        v.RS == 1 ? run<E4M3, D, 2, 1>(a, s) : v.RS == 2 ? run<E4M3, D, 2, 2>(a, s) : run<E4M3, D, 2, 4>(a, s);
 }
 
 }  // namespace
+
+bool kv_attention_plan(int64_t R, int64_t Hkv, int64_t G, int64_t D, int64_t max_q, int64_t seen, KvAttnPlan *p) {
+    const int64_t rows = max_q * G;
+    const Shape v = shape_of((int)D, rows);
+    const int64_t RW = 16 * v.NR * v.RS, groups = (rows + RW - 1) / RW, units = (seen + KV_STEP - 1) / KV_STEP + 1;
+    p->groups = (int)groups;
+    p->whole = seen <= (v.NR == 1 && v.RS == 1 && D <= 128 ? WHOLE_MAX_8 : WHOLE_MAX_4);
+    // workgroups that run at once: 3 to a CU of the variants of up to 168
+    // registers, else 2
+    p->slots = 256 * (v.NR == 1 && D <= 128 ? 3 : 2);
+    p->min_run = WAVES / v.RS;  // a step for each of the waves that split them
+    p->part_rows = (int)(rows < RW ? rows : RW);
+    // few (request, head, row group)s: a cut on each one's start.  Many: twice
+    // as many runs as fit at once (330693 tokens in 48 requests of 8 heads:
+    // 128 us, with one round of them 142, with four 128)
+    p->aligned = 4 * R * Hkv * groups <= p->slots;
+    if (!p->aligned) p->slots *= 2;
+    p->part_slots = p->whole ? 0 : p->slots + (p->aligned ? 0 : R * Hkv * groups);
+    p->head_bytes = p->whole ? 0 : PART_HEAD;
+    return R * Hkv * groups * units < (int64_t(1) << 31) - 4096;
+}
 
 hipError_t launch_kv_attention(const KvAttnArgs &a, int D, bool e4m3, hipStream_t s) {
     if (e4m3)

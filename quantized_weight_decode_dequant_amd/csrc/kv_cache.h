@@ -23,7 +23,6 @@
 namespace qg {
 
 constexpr int KV_STEP = 32;          // tokens of one attention step
-constexpr int KV_CHUNK_MAX = 2048;   // tokens one workgroup takes at most (64 pages of 32)
 constexpr int KV_ROWS_MAX = 32;      // query tokens of one request
 
 struct KvAppendArgs {
@@ -43,11 +42,14 @@ struct KvAttnArgs {
     const int32_t *q_start, *lens, *table;
     const uint32_t *tree;
     void *out;
-    float *part;     // [chunks][M][Hq][D]: unnormalised sums of a chunk
-    float *part_ml;  // [chunks][M][Hq][2]: running maximum (base 2) and sum
+    float *part;     // [part_slots][part_rows][D]: a segment's unnormalised sums
+    float *part_ml;  // [part_slots][part_rows][2]: its running maximum (base 2) and sum
     int64_t q_stride, out_stride;  // elements between tokens
     int64_t pages;
-    int R, M, Hq, Hkv, G, page, max_blocks, max_q, window, chunks, chunk;
+    int R, M, Hq, Hkv, G, page, max_blocks, max_q, max_len, window;
+    int groups, slots, min_run, part_rows;  // of KvAttnPlan
+    int32_t *head;       // run length, then where each request's work starts
+    bool whole, aligned;
     float scale;     // softmax scale * log2(e)
     bool out_f32;
 };
@@ -63,11 +65,19 @@ struct KvTablesArgs {
 hipError_t launch_kv_append(const KvAppendArgs &a, bool e4m3, hipStream_t s);
 hipError_t launch_kv_attention(const KvAttnArgs &a, int D, bool e4m3, hipStream_t s);
 hipError_t launch_kv_tables(const KvTablesArgs &a, hipStream_t s);
-// chunk length and number of chunks of an attention call over at most `span`
-// tokens a request, for `rows` rows (query tokens * heads) to a KV head
-void kv_attention_split(int64_t R, int64_t Hkv, int64_t rows, int64_t page, int64_t span,
-                        bool windowed, int *chunk, int64_t *chunks);
+// How an attention call is cut; false where its work does not fit 31 bits.
+struct KvAttnPlan {
+    int groups;          // row groups of a request of max_q tokens
+    int slots;           // workgroups that share the work
+    int min_run;         // steps one of them takes at least
+    int part_rows;       // rows of a segment
+    int64_t part_slots;  // places for segments
+    int64_t head_bytes;  // in front of them
+    bool aligned;        // a cut falls on the start of every (request, head, row group)
+    bool whole;          // nothing is cut: a workgroup for each (request, head, row group)
+};
+bool kv_attention_plan(int64_t R, int64_t Hkv, int64_t G, int64_t D, int64_t max_q, int64_t seen, KvAttnPlan *p);
 
-constexpr int KV_TABLES_R_MAX = 4096;
+constexpr int KV_R_MAX = 4096;       // requests of a call
 
 }  // namespace qg

@@ -126,10 +126,10 @@ def test_attention():
 def test_workspace_size():
     f = pkg.kv_attention_workspace_bytes
     assert f(1, 1, 8, 2, 128, 64, 1, 64) == 0                    # one chunk: nothing to join
-    small, large = f(1, 1, 8, 2, 128, 64, 1, 1 << 14), f(1, 1, 8, 2, 128, 64, 1, 1 << 20)
-    assert 0 < small <= large and small % (8 * 130 * 4) == 0
+    few, many = f(1, 1, 8, 2, 128, 64, 1, 1 << 14), f(48, 48, 8, 2, 128, 64, 1, 1 << 14)
+    assert 0 < few <= many < 1 << 26
     assert f(1, 1, 7, 2, 128, 64, 1, 1 << 14) == 0 and f(1, 1, 8, 2, 100, 64, 1, 1 << 14) == 0
-    assert f(1, 1 << 30, 8192, 1, 256, 32, 32, 1 << 30) == 0     # refused: past any memory
+    assert f(4096, 1 << 30, 8192, 1, 256, 32, 32, 1 << 30) == 0  # refused: the work does not fit 31 bits
 
 
 def test_binding_refuses_host_tensors_and_wrong_types():
