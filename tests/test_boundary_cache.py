@@ -97,12 +97,12 @@ def test_append():
 
 def test_attention():
     lib = pkg.raw()
-    ws = pkg.kv_attention_workspace_bytes(3, 5, 8, 2, 128, 64, 4, 640)
+    ws = pkg.kv_attention_workspace_bytes(3, 5, 8, 2, 128, 64, 4, 2560)
     assert ws > 0
 
     def call(c=None, **kw):
-        a = dict(R=3, M=5, Hq=8, q=A, qs=1024, q_start=A, lens=A, table=A, nb=10, tree=None, window=0, scale=0.1, max_q=4,
-                 max_len=640, ws=A, wsb=ws, out=A, os=1024, od=0)
+        a = dict(R=3, M=5, Hq=8, q=A, qs=1024, q_start=A, lens=A, table=A, nb=40, tree=None, window=0, scale=0.1, max_q=4,
+                 max_len=2560, ws=A, wsb=ws, out=A, os=1024, od=0)
         a.update(kw)
         desc = cache(**(c or {}))
         return lib.kv_attention_run(C.addressof(desc), a["R"], a["M"], a["Hq"], a["q"], a["qs"], a["q_start"], a["lens"], a["table"],
@@ -115,7 +115,7 @@ def test_attention():
         (dict(M=-1), L.QG_ESHAPE), (dict(M=(1 << 30) + 1), L.QG_ESHAPE), (dict(Hq=7), L.QG_ESHAPE), (dict(Hq=0), L.QG_ESHAPE),
         (dict(Hq=8194, qs=1 << 21, os=1 << 21), L.QG_ESHAPE), (dict(qs=1016), L.QG_ESHAPE), (dict(qs=1028), L.QG_ESHAPE),
         (dict(os=512), L.QG_ESHAPE), (dict(os=1 << 31), L.QG_ESHAPE), (dict(nb=0), L.QG_ESHAPE), (dict(nb=(1 << 30) // 64 + 1), L.QG_ESHAPE),
-        (dict(max_q=0), L.QG_ESHAPE), (dict(max_q=33), L.QG_ESHAPE), (dict(max_len=0), L.QG_ESHAPE), (dict(max_len=641), L.QG_ESHAPE),
+        (dict(max_q=0), L.QG_ESHAPE), (dict(max_q=33), L.QG_ESHAPE), (dict(max_len=0), L.QG_ESHAPE), (dict(max_len=2561), L.QG_ESHAPE),
         (dict(window=-1), L.QG_ESHAPE), (dict(window=(1 << 30) + 1), L.QG_ESHAPE), (dict(tree=A, window=5), L.QG_EUNSUPPORTED),
         (dict(od=2), L.QG_EUNSUPPORTED), (dict(od=3), L.QG_EINVAL), (dict(scale=NAN), L.QG_EINVAL), (dict(scale=INF), L.QG_EINVAL),
         (dict(wsb=ws - 1), L.QG_ESIZE), (dict(ws=None), L.QG_EINVAL), (dict(ws=A + 8), L.QG_EALIGN), (dict(tree=A + 2), L.QG_EALIGN),
