@@ -59,7 +59,7 @@ struct KvTablesArgs {
     const int32_t *keep, *add;
     int32_t *q_start, *slots, *positions, *status;
     int64_t pages;
-    int R, page, max_blocks, max_tokens;
+    int R, page, page_bits, max_blocks, max_tokens;
 };
 
 hipError_t launch_kv_append(const KvAppendArgs &a, bool e4m3, hipStream_t s);
