@@ -232,6 +232,7 @@ int kv_attention_run(const qg_kv_cache *cache, int64_t R, int64_t M, int64_t Hq,
         a.slots = p.slots;
         a.min_run = p.min_run;
         a.part_rows = p.part_rows;
+        a.part_slots = (int)p.part_slots;
         a.whole = p.whole;
         a.aligned = p.aligned;
         a.scale = scale * 1.44269504088896340736f;  // scores in powers of two

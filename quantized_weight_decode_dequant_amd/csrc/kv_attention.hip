@@ -25,6 +25,8 @@
 // workgroup has two segments.  A workgroup's waves split the segment's steps
 // (TS of them) and the rows (RS) and join in LDS; a second kernel joins the
 // segments.  Short contexts are not cut.
+#include <type_traits>
+
 #include "kv_cache.h"
 
 namespace qg {
@@ -302,19 +304,18 @@ __global__ void __launch_bounds__(WAVES * 64, NR == 1 && D <= 128 && WAVES == 4 
     // Q, as f16 in the K tiles' order of dimensions
     f16x8_t qf[NR][KS];
     float cs[NR], k0[NR];  // factor and start of the scores
-    int rowm[NR], rowh[NR], pos[NR], lo[NR];  // visible: lo < t <= pos
+    int pos[NR], lo[NR];   // visible: lo < t <= pos
     unsigned tree[NR];
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
         const int row = row0 + 16 * (rsi * NR + n) + c;
         const bool valid = row < rows;
         const int j = valid ? row / a.G : 0;
-        rowm[n] = valid ? rq.q0 + j : -1;
-        rowh[n] = h * a.G + (valid ? row % a.G : 0);
+        const int hq = h * a.G + (valid ? row - j * a.G : 0);
         pos[n] = base + j;
         lo[n] = a.window > 0 ? pos[n] - a.window : -1;
         tree[n] = a.tree && valid ? a.tree[rq.q0 + j] : 0u;
-        const uint16_t *q = a.q + (size_t)(rq.q0 + j) * a.q_stride + (size_t)rowh[n] * D;
+        const uint16_t *q = a.q + (size_t)(rq.q0 + j) * a.q_stride + (size_t)hq * D;
         float v[KS][8];
         float top = 0.f;
 #pragma unroll
@@ -362,10 +363,11 @@ __global__ void __launch_bounds__(WAVES * 64, NR == 1 && D <= 128 && WAVES == 4 
     const f16x8_t ones = {(_Float16)1.f, (_Float16)1.f, (_Float16)1.f, (_Float16)1.f,
                           (_Float16)1.f, (_Float16)1.f, (_Float16)1.f, (_Float16)1.f};
 
-    // One step.  A wave alone replaces its keys by the next step's once they
-    // are used, then its values: one buffer each, with loads in flight all the
+    // One step; MASK: some row may not see some of its tokens.  A wave alone
+    // replaces its keys by the next step's once they are used, then its values: one buffer each, with loads in flight all the
     // time.  `buf`: where the shared codes lie.
-    const auto compute = [&](int t0, const u32x4_t *buf) {
+    const auto compute = [&](auto masked, int t0, const u32x4_t *buf) {
+        constexpr bool MASK = decltype(masked)::value;
         // a page that is not there is not attended to
         const bool there = page_at(t0) >= 0;
         const int pi = (t0 >> shift) - page0;
@@ -393,9 +395,8 @@ __global__ void __launch_bounds__(WAVES * 64, NR == 1 && D <= 128 && WAVES == 4 
         if constexpr (!SHARED) load(kw, a.k, t0 + STRIDE, 0);
         // codes of slots behind the last token may be anything (an E4M3 NaN),
         // and those of a page without a value scale are worth nothing
-        const bool cut = t0 + KV_STEP > rq.len || no_v;
         unsigned keep[2] = {~0u, ~0u};
-        if (cut) {
+        if (no_v || (MASK && t0 + KV_STEP > rq.len)) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 keep[i] = 0u;
@@ -403,28 +404,28 @@ __global__ void __launch_bounds__(WAVES * 64, NR == 1 && D <= 128 && WAVES == 4 
                 for (int e = 0; e < 4; ++e) keep[i] |= (t0 + 16 * i + 4 * g + e < rq.len) & !no_v ? 0xFFu << (8 * e) : 0u;
             }
         }
-        const bool mask = !there || t0 + KV_STEP - 1 > base || t0 < rq.len - a.window * (a.window > 0);
+        const float off = there ? 0.f : NEG_INF;
         f16x8_t pf[NR];
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
             const float f = ks * cs[n];
             float x[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = s[n][e >> 2][e & 3] * f;
-            if (mask) {
+            for (int e = 0; e < 8; ++e) x[e] = fmaf(s[n][e >> 2][e & 3], f, off);
+            if constexpr (MASK) {
                 const int t1 = t0 + 4 * g;  // the lane's first token
                 if (a.tree) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const int t = t1 + 16 * (e >> 2) + (e & 3);
-                        const bool see = there & (t < rq.len) & ((t < base) | (((tree[n] >> ((t - base) & 31)) & 1u) != 0u));
+                        const bool see = (t < rq.len) & ((t < base) | (((tree[n] >> ((t - base) & 31)) & 1u) != 0u));
                         x[e] = see ? x[e] : NEG_INF;
                     }
                 } else {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const int t = t1 + 16 * (e >> 2) + (e & 3);
-                        x[e] = there & (t <= pos[n]) & (t > lo[n]) ? x[e] : NEG_INF;
+                        x[e] = (t <= pos[n]) & (t > lo[n]) ? x[e] : NEG_INF;
                     }
                 }
             }
@@ -481,6 +482,8 @@ __global__ void __launch_bounds__(WAVES * 64, NR == 1 && D <= 128 && WAVES == 4 
     };
     if constexpr (TS > 1 || SHARED) __syncthreads();  // LDS is free of the last segment
     while (t_lo < t_end) {  // windows of 64 pages
+        // every row sees all of the steps before this one's start
+        const int t_clear = a.window > 0 ? t_lo : min(t_hi, (base + 1) & ~(KV_STEP - 1));
         // vref: a power of two at least as large as every value scale so far;
         // a page's scale over it, as a power of two in the exponent, and its
         // inverse (a page whose values are all 0 has no scale)
@@ -507,20 +510,27 @@ __global__ void __launch_bounds__(WAVES * 64, NR == 1 && D <= 128 && WAVES == 4 
             // that all parts are there (and that the step before the last is
             // used up)
             u32x4_t *mine = lds + (ts * 2 * KB + (st_v ? KB : 0)) * 64 + (st_skip / 16) + lane;
-            const auto stage = [&](u32x4_t(&st)[PART], int t, int b) {
+            const auto stage = [&](auto masked, u32x4_t(&st)[PART], int t, int b) {
                 u32x4_t *to = mine + b * (TS * 2 * KB * 64);
 #pragma unroll
                 for (int u = 0; u < PART; ++u) to[u * 64] = st[u];
                 load(st, st_codes, t + 2 * STRIDE, st_skip);
                 __syncthreads();
-                if (t < t_hi) compute(t, lds + (b * TS + ts) * 2 * KB * 64);
+                if (t < t_hi) compute(masked, t, lds + (b * TS + ts) * 2 * KB * 64);
             };
-            for (int t0 = t_lo; t0 < t_hi; t0 += 2 * STRIDE) {
-                stage(st0, t0 + ts * KV_STEP, 0);
-                stage(st1, t0 + STRIDE + ts * KV_STEP, 1);
+            int t0 = t_lo;
+            for (; t0 + 2 * STRIDE <= t_clear; t0 += 2 * STRIDE) {
+                stage(std::false_type(), st0, t0 + ts * KV_STEP, 0);
+                stage(std::false_type(), st1, t0 + STRIDE + ts * KV_STEP, 1);
+            }
+            for (; t0 < t_hi; t0 += 2 * STRIDE) {
+                stage(std::true_type(), st0, t0 + ts * KV_STEP, 0);
+                stage(std::true_type(), st1, t0 + STRIDE + ts * KV_STEP, 1);
             }
         } else {
-            for (int t0 = t_lo + ts * KV_STEP; t0 < t_hi; t0 += STRIDE) compute(t0, nullptr);
+            int t0 = t_lo + ts * KV_STEP;
+            for (; t0 < t_clear; t0 += STRIDE) compute(std::false_type(), t0, nullptr);
+            for (; t0 < t_hi; t0 += STRIDE) compute(std::true_type(), t0, nullptr);
         }
         if (t_hi >= t_end) break;
         pages(t_hi);
@@ -577,10 +587,12 @@ __global__ void __launch_bounds__(WAVES * 64, NR == 1 && D <= 128 && WAVES == 4 
         Args &a = args();
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
-            if (rowm[n] < 0) continue;
+            const int row = row0 + 16 * (rsi * NR + n) + c;
+            if (row >= rows) continue;
             if (all) {
                 const float f = rq.too_long ? __builtin_nanf("") : l[n] == 0.f ? 0.f : 1.f / l[n];
-                const size_t at = (size_t)rowm[n] * a.out_stride + (size_t)rowh[n] * D + 4 * g;
+                const int j = row / a.G;
+                const size_t at = (size_t)(rq.q0 + j) * a.out_stride + (size_t)(h * a.G + row - j * a.G) * D + 4 * g;
 #pragma unroll
                 for (int d = 0; d < DT; ++d) {
                     const f32x4_t v = o[n][d] * f;
@@ -630,7 +642,7 @@ __global__ void __launch_bounds__(512) kv_attn_join_kernel(KvAttnArgs) {
     const Req rq = req_of<RW>(a, r);
     if (j >= rq.T) return;
     const int row = j * a.G + hq % a.G, pair = (hq / a.G) * rq.groups + row / RW;
-    const int len = a.head[0], before = a.head[1 + r];
+    const int len = max(a.head[0], 1), before = a.head[1 + r];
     int w0, n;
     if (a.aligned) {
         n = (rq.units + len - 1) / len;
@@ -641,7 +653,10 @@ __global__ void __launch_bounds__(512) kv_attn_join_kernel(KvAttnArgs) {
         n = (x + rq.units - 1) / len - w0 + 1;
     }
     if (n == 1) return;  // not cut: written already
-    const size_t at = (size_t)(w0 + (a.aligned ? 0 : r * a.Hkv * a.groups + pair)) * a.part_rows + row % RW, step = a.part_rows;
+    const int slot = w0 + (a.aligned ? 0 : r * a.Hkv * a.groups + pair);
+    // (never so, unless another call wrote to the workspace in between)
+    if (slot < 0 || n < 1 || n > a.part_slots || slot > a.part_slots - n) return;
+    const size_t at = (size_t)slot * a.part_rows + row % RW, step = a.part_rows;
     float mx = NEG_INF;
     for (int c = tid; c < n; c += W * 64) mx = fmaxf(mx, a.part_ml[2 * (at + c * step)]);
 #pragma unroll

@@ -47,7 +47,7 @@ struct KvAttnArgs {
     int64_t q_stride, out_stride;  // elements between tokens
     int64_t pages;
     int R, M, Hq, Hkv, G, page, max_blocks, max_q, max_len, window;
-    int groups, slots, min_run, part_rows;  // of KvAttnPlan
+    int groups, slots, min_run, part_rows, part_slots;  // of KvAttnPlan
     int32_t *head;       // run length, then where each request's work starts
     bool whole, aligned;
     float scale;     // softmax scale * log2(e)
