@@ -482,8 +482,9 @@ __global__ void __launch_bounds__(WAVES * 64, NR == 1 && D <= 128 && WAVES == 4 
     };
     if constexpr (TS > 1 || SHARED) __syncthreads();  // LDS is free of the last segment
     while (t_lo < t_end) {  // windows of 64 pages
-        // every row sees all of the steps before this one's start
-        const int t_clear = a.window > 0 ? t_lo : min(t_hi, (base + 1) & ~(KV_STEP - 1));
+        // every row sees all of the steps before this one (the first new token
+        // only where there is no tree)
+        const int t_clear = a.window > 0 ? t_lo : min(t_hi, (base + (a.tree ? 0 : 1)) & ~(KV_STEP - 1));
         // vref: a power of two at least as large as every value scale so far;
         // a page's scale over it, as a power of two in the exponent, and its
         // inverse (a page whose values are all 0 has no scale)
