@@ -518,7 +518,7 @@ typedef enum { QG_KV_INT8 = 0, QG_KV_E4M3 = 1 } qg_kv_format;
 
 typedef struct qg_kv_cache {
     void *k, *v;                  /* device codes [pages][Hkv][page * D], 16-B */
-    float *k_scales, *v_scales;   /* device fp32 [pages][Hkv] */
+    float *k_scales, *v_scales;   /* device fp32 [pages][Hkv], not negative */
     int64_t pages;                /* >= 1, pages * page < 2^31 */
     int32_t page;                 /* 32, 64, 128 or 256 */
     int32_t Hkv;                  /* 1..1024 */
@@ -584,8 +584,9 @@ int kv_tables_run(int64_t R, int64_t page, int64_t pages, int64_t max_blocks, in
  *               elements (a multiple of 8, at least Hkv * D), so a joint
  *               projection's output can be given as it is.  Read only.
  *  slots        device int32 [M] (kv_tables_run's).  Tokens of one page must
- *               be neighbours with slots that rise by 1; a slot outside
- *               [0, pages * page) is skipped.
+ *               be neighbours with slots that rise by 1, each slot given
+ *               once (otherwise those pages' contents are unspecified); a
+ *               slot outside [0, pages * page) is skipped.
  * amax is over finite values; infinities are stored as the largest code, NaN
  * as 0.  A block whose amax is below 2^-100 is stored as zeros.  Two calls
  * that write the same page must not overlap in time.

@@ -786,7 +786,7 @@ bool kv_attention_plan(int64_t R, int64_t Hkv, int64_t G, int64_t D, int64_t max
     if (!p->aligned) p->slots *= 2;
     p->part_slots = p->whole ? 0 : p->slots + (p->aligned ? 0 : R * Hkv * groups);
     p->head_bytes = p->whole ? 0 : PART_HEAD;
-    return R * Hkv * groups * units < (int64_t(1) << 31) - 4096;
+    return R * Hkv * groups * units < (int64_t(1) << 31) - 65536;
 }
 
 hipError_t launch_kv_attention(const KvAttnArgs &a, int D, bool e4m3, hipStream_t s) {

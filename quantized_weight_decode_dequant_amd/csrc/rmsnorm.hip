@@ -146,7 +146,6 @@ __global__ void __launch_bounds__(U == 2 || U == 4 ? 256 : 1024) rmsnorm_kernel(
             if (Q && ROT) amax = fmax(amax, fabs(z[i][e]));
             if (Q && !ROT) zmax = fmaxf(zmax, fabsf(r[i][e] * (e & 1 ? bf16_hi(wt[i][e >> 1]) : bf16_lo(wt[i][e >> 1]))));
         }
-    if (Q && !ROT) amax = (double)zmax;
 #pragma unroll
     for (int d = 32; d; d >>= 1) {
         ss += __shfl_xor(ss, d);
@@ -164,6 +163,18 @@ __global__ void __launch_bounds__(U == 2 || U == 4 ? 256 : 1024) rmsnorm_kernel(
         ss += wss[w];
         if (Q) amax = fmax(amax, wmax[w]);
     }
+    // products this small have lost bits in fp32, or all of them: fp64 decides
+    // every element
+    const bool tiny = Q && !ROT && amax < 0x1p-60;
+    bool nonzero = true;  // (a row of zeros needs none of that)
+    if (tiny) {
+        unsigned any = 0u;
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) any |= __builtin_bit_cast(unsigned, r[i][e]) << 1;
+        nonzero = __syncthreads_or(any != 0u);
+    }
     // z in fp64 from its inputs (not rotated)
     const auto exact = [&](int k) {
         const double v = load1<XF32>(x, k);
@@ -172,8 +183,8 @@ __global__ void __launch_bounds__(U == 2 || U == 4 ? 256 : 1024) rmsnorm_kernel(
     const float rs = 1.f / sqrtf(ss / (float)a.K + a.eps);
     // a row with a NaN or an infinity has no scale: codes 0, scale NaN
     const bool fin = ss < __builtin_inff();
-    if (Q && !ROT && fin && amax > 0.0) {
-        const float near = (float)amax * (1.f - 0x1p-21f);
+    if (Q && !ROT && fin && nonzero) {
+        const float near = tiny ? 0.f : (float)amax * (1.f - 0x1p-21f);
         unsigned mine = 0u;  // the thread's elements that may be the largest
 #pragma unroll
         for (int i = 0; i < U; ++i)
@@ -183,6 +194,7 @@ __global__ void __launch_bounds__(U == 2 || U == 4 ? 256 : 1024) rmsnorm_kernel(
 #pragma unroll 1
         for (; mine; mine &= mine - 1) {
             const int k = __builtin_ctz(mine);
+            if (tid + (k >> 3) * nt >= units) break;
             atomicMax(&top_bits, __builtin_bit_cast(unsigned long long, fabs(exact(8 * (tid + (k >> 3) * nt) + (k & 7)))));
         }
         __syncthreads();
@@ -214,13 +226,13 @@ __global__ void __launch_bounds__(U == 2 || U == 4 ? 256 : 1024) rmsnorm_kernel(
                     q[e] = (int)(fin ? c : 0.0);
                 } else {
                     const float p = r[i][e] * w[e] * f32, c = rintf(p);
-                    border |= fabsf(p - c) > fmaf(fabsf(p), -2.5e-7f, 0.5f) ? 1u << e : 0u;
-                    q[e] = (int)(fin ? c : 0.f);
+                    border |= tiny || fabsf(p - c) > fmaf(fabsf(p), -2.5e-7f, 0.5f) ? 1u << e : 0u;
+                    q[e] = (int)(fin && !tiny ? c : 0.f);
                 }
             }
             u32x2_t o = {(q[0] & 0xFFu) | (q[1] & 0xFFu) << 8 | (q[2] & 0xFFu) << 16 | (unsigned)q[3] << 24,
                          (q[4] & 0xFFu) | (q[5] & 0xFFu) << 8 | (q[6] & 0xFFu) << 16 | (unsigned)q[7] << 24};
-            if (!fin) border = 0u;
+            if (!fin || !(amax > 0.0)) border = 0u;
 #pragma unroll 1
             for (; border; border &= border - 1) {
                 const int e = __builtin_ctz(border), sh = 8 * (e & 3);

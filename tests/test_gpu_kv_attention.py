@@ -91,6 +91,19 @@ class Case:
         assert err.size == 0 or err.max() <= 1, err.max()
         return float(err.max()) if err.size else 0.0
 
+    def run_rows(self, requests):
+        """Runs all, checks the rows of some requests."""
+        got = pkg.kv_attention_run(self.cache(), **self.args())
+        torch.cuda.synchronize()
+        sub = object.__new__(Case)
+        sub.__dict__.update(self.__dict__)
+        sub.lens, sub.table, sub.T = self.lens[requests], self.table[requests], self.T[requests]
+        sub.q_start = np.concatenate([[0], np.cumsum(sub.T)])
+        rows = np.concatenate([np.arange(self.q_start[r], self.q_start[r + 1]) for r in requests])
+        sub.q, sub.M = self.q[rows], len(rows)
+        sub.check(got[torch.from_numpy(rows).to(DEV)])
+        return got
+
     def run(self, window=0, scale=None, out_dtype=None, **kw):
         a = self.args()
         a.update(kw)
@@ -326,3 +339,33 @@ def test_same_result_every_time_and_alone():
                 outs.append(pkg.kv_attention_run(cache, **a))
     torch.cuda.synchronize()
     assert all(torch.equal(first, o) for o in outs)
+
+
+@pytest.mark.parametrize("lens,H", [([200003] * 4, 8), ([150001, 1, 0, 90000] + [70000] * 20, 16)])
+def test_long_runs_over_shared_pages(lens, H):
+    """Workgroups whose run is longer than the 64 pages whose entries a wave
+    holds at once; requests that share pages with each other, and a table
+    that names a page many times; value scales that grow along the way."""
+    note("attention long runs R=%d" % len(lens))
+    page, pages = 32, 97
+    c = Case(30, [min(n, 3000) for n in lens], [1 if n else 0 for n in lens], H=H, G=1, D=64, page=page, pages=4096)
+    c.lens = np.array(lens)
+    c.pages = pages
+    c.k, c.v, c.ks, c.vs = c.k[:pages], c.v[:pages], c.ks[:pages], c.vs[:pages]
+    c.vs *= np.linspace(0.01, 1, pages, dtype=np.float32)[:, None]
+    cols = -(-max(lens) // page)
+    c.table = np.stack([np.sort(c.g.integers(0, pages, cols)) if r % 2 else c.g.integers(0, pages, cols) for r in range(len(lens))])
+    # the reference for some of the requests (the rows of the others are checked against each other's split)
+    got = c.run_rows([0, len(lens) - 1])
+    assert torch.isfinite(got).all()
+
+
+def test_many_requests():
+    """More requests than a wave has lanes, most of them without new tokens."""
+    g = np.random.default_rng(31)
+    R = 1500
+    T = (g.random(R) < 0.1).astype(int)
+    T[-1] = 3
+    lens = np.where(T > 0, g.integers(3, 200, R), 5)
+    lens[700], T[700] = 2100, 2
+    Case(32, lens.tolist(), T.tolist(), H=2, G=2, D=64, page=32).run(out_dtype=pkg.OUT_BF16)

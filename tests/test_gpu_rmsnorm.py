@@ -87,6 +87,27 @@ def test_ties_zero_rows_and_one_value():
     assert not Xq[1].any() and float(sc[1]) == 0.0
 
 
+@pytest.mark.parametrize("K", [64, 4128])
+def test_tiny_values(K):
+    """Rows whose products underflow in fp32, or lose bits there, beside
+    ordinary ones; weights that are 0."""
+    g = np.random.default_rng(K)
+    x = g.standard_normal((7, K)) * np.array([1e-20, 1e-30, 1e-36, 3e-38, 1e-38, 0.0, 1.0])[:, None]
+    w = torch.from_numpy(g.standard_normal(K) * np.where(np.arange(K) % 3 == 0, 1e-9, 1.0)).to(torch.bfloat16)
+    w[::5] = 0.0
+    x = torch.from_numpy(x).to(torch.bfloat16)
+    for M in (7, 600):
+        xx = x.repeat((M + 6) // 7, 1)[:M]
+        Xq, sc = pkg.rmsnorm_quant_run(xx.to(DEV), w.to(DEV), 1e-30)[2:]
+        torch.cuda.synchronize()
+        _, _, q64, s64 = ref.norm(to_np(xx), to_np(w), np.float64(np.float32(1e-30)))
+        assert np.array_equal(Xq.cpu().numpy(), q64), np.argwhere(Xq.cpu().numpy() != q64)[:4]
+        big = s64 > 1e-30  # (the sum of squares of smaller rows underflows in fp32: eps decides)
+        assert np.all(np.abs(to_np(sc) - s64)[big] <= FP32_PART * s64[big])
+    Xq, sc = pkg.rmsnorm_quant_run((x * 0 + 1e-30).to(DEV), (w * 0 + 1e-20).to(DEV), 1e-6)[2:]
+    assert bool((Xq == 127).all())  # every product is 0 in fp32
+
+
 def test_rows_that_are_not_finite_stay_alone():
     x, res, w, _ = inputs(3, 4, 256, torch.bfloat16, torch.bfloat16)
     x[1, 17] = float("nan")
