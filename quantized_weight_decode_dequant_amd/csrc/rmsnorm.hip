@@ -223,16 +223,20 @@ __global__ void __launch_bounds__(U == 2 || U == 4 ? 256 : 1024) rmsnorm_kernel(
                     const double p = z[i][e] * f;
                     double c = rint(p);
                     if (fabs(p - c) > 0.5 - 1e-9) c = rint(z[i][e] * 127.0 / amax);
-                    q[e] = (int)(fin ? c : 0.0);
+                    q[e] = (int)c;
                 } else {
                     const float p = r[i][e] * w[e] * f32, c = rintf(p);
-                    border |= tiny || fabsf(p - c) > fmaf(fabsf(p), -2.5e-7f, 0.5f) ? 1u << e : 0u;
-                    q[e] = (int)(fin && !tiny ? c : 0.f);
+                    border |= fabsf(p - c) > fmaf(fabsf(p), -2.5e-7f, 0.5f) ? 1u << e : 0u;
+                    q[e] = (int)c;
                 }
             }
             u32x2_t o = {(q[0] & 0xFFu) | (q[1] & 0xFFu) << 8 | (q[2] & 0xFFu) << 16 | (unsigned)q[3] << 24,
                          (q[4] & 0xFFu) | (q[5] & 0xFFu) << 8 | (q[6] & 0xFFu) << 16 | (unsigned)q[7] << 24};
-            if (!fin || !(amax > 0.0)) border = 0u;
+            if (tiny) border = 0xFFu;
+            if (!fin || !(amax > 0.0)) {
+                o = u32x2_t{0u, 0u};
+                border = 0u;
+            }
 #pragma unroll 1
             for (; border; border &= border - 1) {
                 const int e = __builtin_ctz(border), sh = 8 * (e & 3);
