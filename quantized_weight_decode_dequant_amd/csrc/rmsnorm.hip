@@ -16,9 +16,11 @@
 // sum of squares are fp32.
 //
 // One workgroup per row; a thread holds U units of 8 consecutive elements, the
-// four lanes of a quad one block of 32.  Bound by latency for a few rows (one
-// unit a thread: as many loads at once as there are), by memory for many
-// (workgroups of up to 256 threads, so that many rows are in flight on a CU).
+// four lanes of a quad one block of 32.  Bound by latency for a few rows (2.4
+// us for 1 x 4096 in bf16, 6.8 for 32 x 12288 in fp32, rotated), by memory for
+// many (5003 x 7168, residual, bf16 and codes: 67 us, 4.8 TB/s; in bf16 alone
+// 54 us, 5.3 TB/s).  With every element in fp64 that took 85 us, with a border
+// of 1e-4 codes 104: an element computed again waits for memory.
 #include "rmsnorm.h"
 
 namespace qg {
@@ -92,7 +94,7 @@ __device__ __forceinline__ double load1(const void *row, int k) {
 
 // RES: 0 none, 1 bf16, 2 fp32
 template <int U, bool XF32, int RES, bool Q, bool ROT>
-__global__ void __launch_bounds__(U == 2 || U == 4 ? 256 : 1024) rmsnorm_kernel(RmsArgs a) {
+__global__ void __launch_bounds__(U == 4 ? 256 : 1024) rmsnorm_kernel(RmsArgs a) {
     __shared__ float wss[16];
     __shared__ double wmax[16];
     __shared__ unsigned long long top_bits;
@@ -273,9 +275,12 @@ namespace {
 template <int U, bool XF32, int RES>
 void run(const RmsArgs &a, int threads, hipStream_t s) {
     const dim3 g((unsigned)a.M), b(threads);
-    if (!a.Xq)
-        hipLaunchKernelGGL((rmsnorm_kernel<U, XF32, RES, false, false>), g, b, 0, s, a);
-    else if (!a.signs)
+    if constexpr (U != 4)
+        if (!a.Xq) {
+            hipLaunchKernelGGL((rmsnorm_kernel<U, XF32, RES, false, false>), g, b, 0, s, a);
+            return;
+        }
+    if (!a.signs)
         hipLaunchKernelGGL((rmsnorm_kernel<U, XF32, RES, true, false>), g, b, 0, s, a);
     else
         hipLaunchKernelGGL((rmsnorm_kernel<U, XF32, RES, true, true>), g, b, 0, s, a);
@@ -292,15 +297,17 @@ void pick(const RmsArgs &a, bool xf32, int res, int threads, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_rmsnorm(const RmsArgs &a, bool x_f32, int res, hipStream_t s) {
-    // few rows: one unit a thread where 1024 threads take the row; many: up to
-    // four, in workgroups of 64 to 256 threads where the row allows
+    // One unit a thread while 1024 threads take the row.  Not where codes are
+    // asked of many rows of 9 waves or more: the codes wait for two reductions
+    // of the whole workgroup, and too few of these are on a CU to hide that
+    // (4 units against 1: 67.6 us against 74.0 for 5003 x 7168, but 63.9
+    // against 58.2 for 8192 x 4096, 5.7 against 5.2 for 32 x 7168 and, in bf16
+    // alone, 59.1 against 54.4 for 5003 x 7168).
     const int units = a.K / 8;
-    const int u = units > 1024 ? 3 : a.M < 512 ? 1 : units >= 512 ? 4 : units >= 256 ? 2 : 1;
+    const int u = units > 1024 ? 3 : a.Xq && a.M >= 512 && units > 512 ? 4 : 1;
     const int threads = (((units + u - 1) / u) + 63) / 64 * 64;
     if (u == 1)
         pick<1>(a, x_f32, res, threads, s);
-    else if (u == 2)
-        pick<2>(a, x_f32, res, threads, s);
     else if (u == 3)
         pick<3>(a, x_f32, res, threads, s);
     else

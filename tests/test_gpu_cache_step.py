@@ -161,7 +161,7 @@ def test_captured_steps_equal_eager_ones(nb):
         for s in states[1:]:
             assert all(torch.equal(a, b) for a, b in zip(states[0], s)), rep
         assert int(loops[0].status) == 0
-        lens = np.array(loops[0].lens.cpu())
+        lens = loops[0].lens.cpu().numpy().copy()
         _ = torch.randn(1000, device=DEV).sum().item()  # unrelated eager work in between
 
 

@@ -71,6 +71,15 @@ def test_sizes(M, K, rot):
     check(x, res, w, signs if rot else None, 1, 1, alias=True)
 
 
+@pytest.mark.parametrize("M,K", [(512, 4128), (511, 4128), (601, 8192), (513, 8224)])
+@pytest.mark.parametrize("rot", [0, 1])
+def test_many_long_rows(M, K, rot):
+    """Rows whose threads hold four units, and the sizes beside them."""
+    note("rmsnorm M=%d K=%d rot=%d" % (M, K, rot))
+    x, res, w, signs = inputs(M * 100003 + K, M, K, torch.bfloat16, torch.bfloat16)
+    check(x, res, w, signs if rot else None, 1, 1, alias=True)
+
+
 def test_ties_zero_rows_and_one_value():
     """Codes that land on .5 (ties to even), a row of zeros, a row with one
     value, a row of equal values."""
