@@ -10,9 +10,10 @@
 //
 // One workgroup per (run of slots that lie in one page, head, K or V): the
 // largest magnitude first, then, with the values read again from the caches,
-// the codes (holding them in registers takes three times as many: 25.2 us
-// against 26.8 for 11460 tokens of prompts, but 7.4 against 6.0 for 64 single
-// tokens).  Keys: a thread codes 16 dimensions of a token, one 16-byte piece
+// the codes (held in registers, before the packed conversions: 25.2 us against
+// 26.8 for 11460 tokens of prompts, but 7.4 against 6.0 for 64 single tokens).
+// Latency bounds a few tokens (slot, run, values, scale in turn: 5.3 us for 64
+// single ones, 8 heads of 128), the two passes many (11460: 21 us, 3.4 TB/s).  Keys: a thread codes 16 dimensions of a token, one 16-byte piece
 // of the block, with the tokens along the lanes, so that a wave writes whole
 // kilobytes.  Values, which the block holds by token within a dimension: a
 // thread codes 2 x 2 dimensions of 8 tokens, two whole 16-byte pieces; where
