@@ -535,7 +535,8 @@ typedef struct qg_kv_cache {
  * next step's keep dropping the rejected drafts, a prompt add = its length, a
  * finished request keep = 0, add = 0.
  *
- *  R            requests, 0..4096.
+ *  R            requests, 0..4096; of 0, the outputs are written all the same
+ *               (lens, add and table may be NULL).
  *  page, pages  as in qg_kv_cache.
  *  max_blocks   columns of the table, >= 1; max_blocks * page <= 2^30.
  *  max_tokens   entries of slots and positions, >= 0.

@@ -533,8 +533,6 @@ def kv_tables_run(page: int, lens, add, table, free_pages, free_count, max_token
             raise ValueError("%s must hold at least %d values" % (name, n))
         return t
 
-    if R == 0:
-        raise ValueError("no requests")
     q_start, status = out(q_start, R + 1, "q_start"), out(status, 1, "status")
     slots, positions = out(slots, max_tokens, "slots"), out(positions, max_tokens, "positions")
     dev, r = _device(lens), (R,)

@@ -104,7 +104,7 @@ int kv_tables_run(int64_t R, int64_t page, int64_t pages, int64_t max_blocks, in
         if (R < 0 || R > KV_R_MAX || !page_size(page) || pages < 1 || pages >= INT32_END / page ||
             max_blocks < 1 || max_blocks > LEN_MAX / page || max_tokens < 0 || max_tokens > ROWS_MAX)
             return QG_ESHAPE;
-        if (!lens || !add || !table || !free_pages || !free_count || !q_start || !status ||
+        if ((R > 0 && (!lens || !add || !table)) || !free_pages || !free_count || !q_start || !status ||
             (max_tokens > 0 && (!slots || !positions)))
             return QG_EINVAL;
         for (const void *p : {(const void *)lens, (const void *)keep, (const void *)add,
@@ -112,7 +112,6 @@ int kv_tables_run(int64_t R, int64_t page, int64_t pages, int64_t max_blocks, in
                               (const void *)free_count, (const void *)q_start,
                               (const void *)slots, (const void *)positions, (const void *)status})
             if (!aligned(p, 4)) return QG_EALIGN;
-        if (R == 0) return QG_OK;
         KvTablesArgs a;
         a.lens = lens;
         a.table = table;

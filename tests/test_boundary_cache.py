@@ -57,7 +57,7 @@ def test_tables():
         return lib.kv_tables_run(*[{**base, **kw}[n] for n in names], None)
 
     expect(call, [
-        (dict(R=0), L.QG_OK), (dict(R=-1), L.QG_ESHAPE), (dict(R=4097), L.QG_ESHAPE), (dict(page=16), L.QG_ESHAPE),
+        (dict(R=0, q=None), L.QG_EINVAL), (dict(R=-1), L.QG_ESHAPE), (dict(R=4097), L.QG_ESHAPE), (dict(page=16), L.QG_ESHAPE),
         (dict(page=48), L.QG_ESHAPE), (dict(page=512), L.QG_ESHAPE), (dict(page=0), L.QG_ESHAPE), (dict(pages=0), L.QG_ESHAPE),
         (dict(pages=(1 << 31) // 64), L.QG_ESHAPE), (dict(nb=0), L.QG_ESHAPE), (dict(nb=(1 << 30) // 64 + 1), L.QG_ESHAPE),
         (dict(mt=-1), L.QG_ESHAPE), (dict(mt=(1 << 30) + 1), L.QG_ESHAPE),

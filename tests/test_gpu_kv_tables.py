@@ -57,6 +57,18 @@ def test_random_steps(page, R):
     assert refused < 12
 
 
+@pytest.mark.parametrize("max_tokens", [0, 5, 5000])
+def test_no_requests(max_tokens):
+    """Nothing to do, but the outputs that later calls read are written."""
+    t = lambda *a: torch.tensor(a, dtype=torch.int32, device=DEV)  # noqa: E731
+    none, free, count = torch.empty(0, dtype=torch.int32, device=DEV), t(2, 0, 1), t(3)
+    q_start, slots, pos, status = t(7), t(7).repeat(max_tokens), t(7).repeat(max_tokens), t(7)
+    pkg.kv_tables_run(32, none, none, torch.empty(0, 4, dtype=torch.int32, device=DEV), free, count, max_tokens,
+                      q_start=q_start, slots=slots, positions=pos, status=status)
+    assert int(q_start) == 0 and int(status) == 0 and bool((slots == -1).all()) and not bool(pos.any())
+    assert free.tolist() == [2, 0, 1] and int(count) == 3
+
+
 def test_release_restores_the_list():
     b = Both(32, 5, 40, 300, seed=3)
     b.step([70, 0, 33, 1, 600])
