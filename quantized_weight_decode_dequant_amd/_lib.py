@@ -441,6 +441,18 @@ def _call(dev, stream, where, fn, *args):
         raise QGError(status, where)
 
 
+def _empty(shape, dtype, device, stream):
+    """torch.empty for a call on `stream`: from that stream's memory, which
+    work on no other stream may still be using."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _float_type(t, name):
     torch = _torch()
     if t.dtype is torch.bfloat16:
@@ -464,9 +476,9 @@ def rmsnorm_quant_run(x, weight, eps: float, residual=None, residual_out=None, s
     xt = _float_type(x, "x")
     if Xq is not None or x_scales is not None or y is None:
         if Xq is None:
-            Xq = torch.empty((M, K), dtype=torch.int8, device=x.device)
+            Xq = _empty((M, K), torch.int8, x.device, stream)
         if x_scales is None:
-            x_scales = torch.empty(M, dtype=torch.float32, device=x.device)
+            x_scales = _empty(M, torch.float32, x.device, stream)
     if M == 0:
         return residual_out, y, Xq, x_scales
     dev, mk, i8 = _device(x), (M, K), torch.int8
@@ -528,7 +540,7 @@ def kv_tables_run(page: int, lens, add, table, free_pages, free_count, max_token
 
     def out(t, n, name):
         if t is None:
-            return torch.empty(n, dtype=i32, device=lens.device)
+            return _empty(n, i32, lens.device, stream)
         if t.dim() != 1 or t.shape[0] < n:
             raise ValueError("%s must hold at least %d values" % (name, n))
         return t
@@ -583,7 +595,7 @@ def kv_attention_run(cache: KVCache, q, q_start, lens, table, max_q: int, max_le
     if max_len is None:
         max_len = nb * cache.page
     if out is None:
-        out = torch.empty((M, Hq, D), dtype=_out_torch_dtype(out_dtype), device=q.device)
+        out = _empty((M, Hq, D), _out_torch_dtype(out_dtype), q.device, stream)
     else:
         out_dtype = _float_type(out, "out")
     if out.shape != q.shape:
@@ -596,7 +608,7 @@ def kv_attention_run(cache: KVCache, q, q_start, lens, table, max_q: int, max_le
     lib = raw()
     if workspace is None:
         nbytes = lib.qg_kv_attention_workspace_bytes(R, M, Hq, cache.Hkv, D, cache.page, max_q, max_len, window)
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
+        workspace = _empty(nbytes, torch.uint8, q.device, stream) if nbytes else None
     else:
         nbytes = workspace.numel() * workspace.element_size()
     _call(dev, stream, "kv_attention_run", lib.kv_attention_run, cache._ref, R, M, Hq, qp, qs,

@@ -369,3 +369,26 @@ def test_many_requests():
     lens = np.where(T > 0, g.integers(3, 200, R), 5)
     lens[700], T[700] = 2100, 2
     Case(32, lens.tolist(), T.tolist(), H=2, G=2, D=64, page=32).run(out_dtype=pkg.OUT_BF16)
+
+
+@pytest.mark.parametrize("as_int", [False, True])
+def test_given_stream_takes_its_own_memory(as_int):
+    """Output and workspace of a call on a given stream are not memory that
+    the current stream freed but has work left to do on."""
+    c = Case(33, [5000], [5])
+    a, cache = c.args(), c.cache()
+    first = pkg.kv_attention_run(cache, **a)
+    side = torch.cuda.Stream()
+    mats = [torch.ones(4096, 4096, device=DEV) for _ in range(2)]
+    ws = pkg.kv_attention_workspace_bytes(1, c.M, 8, 2, 128, c.page, 5, c.cols * c.page)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        left = [torch.empty(n, dtype=torch.uint8, device=DEV) for n in (ws, first.numel() * 2)]
+        for _ in range(20):
+            mats[1] = torch.mm(mats[0], mats[0])
+        for t in left:
+            t.fill_(255)
+        del left, t
+        got = pkg.kv_attention_run(cache, stream=side.cuda_stream if as_int else side, **a)
+        torch.cuda.synchronize()
+        assert torch.equal(got, first)
