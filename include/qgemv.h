@@ -482,7 +482,7 @@ int qg_plain_read(const void *buf, size_t bytes, uint32_t *sink, int grid, void 
  *  eps          > 0, finite.
  *  signs        device int8 [K], 16-B, each +1 or -1, or NULL (no rotation);
  *               NULL when Xq is.
- *  M, K         M >= 0; K a multiple of 32, 32..24576.
+ *  M, K         M 0..2^22 - 1; K a multiple of 32, 32..24576.
  *  y            device bf16 [M][K], 16-B, or NULL.
  *  Xq, x_scales device int8 [M][K], 16-B, and fp32 [M], or both NULL; one of
  *               y and Xq is required.
@@ -580,7 +580,7 @@ int kv_tables_run(int64_t R, int64_t page, int64_t pages, int64_t max_blocks, in
  * one fp32 operation.
  *
  *  cache        written.
- *  M            tokens, 0..2^30.
+ *  M            tokens, 0..2^28.
  *  K, V         device bf16 [M][Hkv][D], 16-B; token m at K + m * k_stride
  *               elements (a multiple of 8, at least Hkv * D), so a joint
  *               projection's output can be given as it is.  Read only.
@@ -629,7 +629,7 @@ size_t qg_kv_attention_workspace_bytes(int64_t R, int64_t M, int64_t Hq, int64_t
  *  window       0 (none), or 1..2^30; with tree_mask: 0 only.
  *  scale        of the scores, finite; usually 1 / sqrt(D).
  *  max_q        1..32: no request has more new tokens.  Rows past it are not
- *               computed.
+ *               computed.  R * max_q * Hq < 2^26 (QG_ESHAPE).
  *  max_len      1..max_blocks * page: no request is longer; a longer one gets
  *               rows of NaN.  (The product of requests, heads, row groups and
  *               max_len / 32 has to stay below 2^31: QG_ESHAPE.)

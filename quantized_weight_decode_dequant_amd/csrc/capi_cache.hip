@@ -15,6 +15,11 @@ using namespace qg;
 
 constexpr int64_t INT32_END = int64_t(1) << 31;
 constexpr int64_t ROWS_MAX = int64_t(1) << 30;
+// A launch has fewer than 2^32 threads: the norm takes up to 1024 a row, the
+// append 8 a token, the attention's join 64 a row and head.
+constexpr int64_t NORM_ROWS_MAX = (int64_t(1) << 22) - 1;
+constexpr int64_t APPEND_TOKENS_MAX = int64_t(1) << 28;
+constexpr int64_t JOINS_END = int64_t(1) << 26;
 constexpr int64_t LEN_MAX = int64_t(1) << 30;
 constexpr int64_t STRIDE_MAX = int64_t(1) << 31;
 
@@ -45,7 +50,7 @@ bool attention_plan(int64_t R, int64_t M, int64_t Hq, int64_t Hkv, int64_t D, in
                     int64_t max_q, int64_t max_len, int64_t window, KvAttnPlan *p, size_t *bytes) {
     if (R < 0 || R > KV_R_MAX || M < 0 || M > ROWS_MAX || Hkv < 1 || Hkv > 1024 || Hq < 1 || Hq > 8192 ||
         Hq % Hkv || !head_size(D) || !page_size(page) || max_q < 1 || max_q > KV_ROWS_MAX ||
-        max_len < 1 || max_len > LEN_MAX || window < 0 || window > LEN_MAX)
+        max_len < 1 || max_len > LEN_MAX || window < 0 || window > LEN_MAX || R * max_q * Hq >= JOINS_END)
         return false;
     const int64_t seen = window > 0 && window + max_q - 1 < max_len ? window + max_q - 1 : max_len;
     if (!kv_attention_plan(R, Hkv, Hq / Hkv, D, max_q, seen, p)) return false;
@@ -65,7 +70,7 @@ int rmsnorm_quant_run(const void *x, int x_dtype, const void *residual, void *re
             if (t == QG_OUT_I32_GROUPS) return QG_EUNSUPPORTED;
             if (t != QG_OUT_BF16 && t != QG_OUT_F32) return QG_EINVAL;
         }
-        if (M < 0 || M > ROWS_MAX || K < 32 || K > RMS_K_MAX || K % 32) return QG_ESHAPE;
+        if (M < 0 || M > NORM_ROWS_MAX || K < 32 || K > RMS_K_MAX || K % 32) return QG_ESHAPE;
         if (!x || !weight || (!y && !Xq) || (Xq != nullptr) != (x_scales != nullptr) ||
             (signs && !Xq) || (residual_out && !residual))
             return QG_EINVAL;
@@ -140,7 +145,7 @@ int kv_append_run(const qg_kv_cache *cache, int64_t M, const void *K, int64_t k_
         const int st = check_cache(cache);
         if (st != QG_OK) return st;
         const int64_t width = (int64_t)cache->Hkv * cache->D;
-        if (M < 0 || M > ROWS_MAX || !row_stride(k_stride, width) || !row_stride(v_stride, width))
+        if (M < 0 || M > APPEND_TOKENS_MAX || !row_stride(k_stride, width) || !row_stride(v_stride, width))
             return QG_ESHAPE;
         if (!K || !V || !slots) return QG_EINVAL;
         if (!aligned(K, 16) || !aligned(V, 16) || !aligned(slots, 4)) return QG_EALIGN;

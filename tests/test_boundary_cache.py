@@ -38,7 +38,7 @@ def test_rmsnorm():
                                      a["K"], a["y"], a["Xq"], a["sc"], None)
 
     expect(call, [
-        (dict(M=0), L.QG_OK), (dict(M=-1), L.QG_ESHAPE), (dict(M=(1 << 30) + 1), L.QG_ESHAPE),
+        (dict(M=0), L.QG_OK), (dict(M=-1), L.QG_ESHAPE), (dict(M=(1 << 30) + 1), L.QG_ESHAPE), (dict(M=1 << 22), L.QG_ESHAPE),
         (dict(K=0), L.QG_ESHAPE), (dict(K=48), L.QG_ESHAPE), (dict(K=24576 + 32), L.QG_ESHAPE), (dict(K=-32), L.QG_ESHAPE),
         (dict(x=None), L.QG_EINVAL), (dict(w=None), L.QG_EINVAL), (dict(y=None, Xq=None, sc=None, signs=None), L.QG_EINVAL),
         (dict(Xq=None), L.QG_EINVAL), (dict(sc=None), L.QG_EINVAL), (dict(res=None), L.QG_EINVAL),
@@ -115,6 +115,7 @@ def test_attention():
         (dict(M=-1), L.QG_ESHAPE), (dict(M=(1 << 30) + 1), L.QG_ESHAPE), (dict(Hq=7), L.QG_ESHAPE), (dict(Hq=0), L.QG_ESHAPE),
         (dict(Hq=8194, qs=1 << 21, os=1 << 21), L.QG_ESHAPE), (dict(qs=1016), L.QG_ESHAPE), (dict(qs=1028), L.QG_ESHAPE),
         (dict(os=512), L.QG_ESHAPE), (dict(os=1 << 31), L.QG_ESHAPE), (dict(nb=0), L.QG_ESHAPE), (dict(nb=(1 << 30) // 64 + 1), L.QG_ESHAPE),
+        (dict(R=4096, Hq=512, qs=1 << 16, os=1 << 16, max_q=32, max_len=64, wsb=1 << 40), L.QG_ESHAPE),  # more joins than a launch holds
         (dict(max_q=0), L.QG_ESHAPE), (dict(max_q=33), L.QG_ESHAPE), (dict(max_len=0), L.QG_ESHAPE), (dict(max_len=2561), L.QG_ESHAPE),
         (dict(window=-1), L.QG_ESHAPE), (dict(window=(1 << 30) + 1), L.QG_ESHAPE), (dict(tree=A, window=5), L.QG_EUNSUPPORTED),
         (dict(od=2), L.QG_EUNSUPPORTED), (dict(od=3), L.QG_EINVAL), (dict(scale=NAN), L.QG_EINVAL), (dict(scale=INF), L.QG_EINVAL),
