@@ -506,7 +506,8 @@ int rmsnorm_quant_run(const void *x, int x_dtype, const void *residual, void *re
  * at place p % page, i.e. in slot table[r][p / page] * page + p % page.  Each
  * (page, KV head) block holds page * D one-byte codes with one fp32 scale:
  *  - QG_KV_INT8: int8 codes in [-127, 127], value = scale * code;
- *  - QG_KV_E4M3: OCP E4M3 codes, value = scale * code.
+ *  - QG_KV_E4M3: OCP E4M3 codes, value = scale * code (kv_append_run writes
+ *    no NaN; places behind a request's last token may hold anything).
  * Byte order of a block (token t of the page, dimension d), chosen for
  * 128-bit loads that are matrix-core operands:
  *  - keys   [t/16][d/16][t%16][d%16]
@@ -628,8 +629,8 @@ size_t qg_kv_attention_workspace_bytes(int64_t R, int64_t M, int64_t Hq, int64_t
  *  tree_mask    device uint32 [M] or NULL: bit i = the request's new token i.
  *  window       0 (none), or 1..2^30; with tree_mask: 0 only.
  *  scale        of the scores, finite; usually 1 / sqrt(D).
- *  max_q        1..32: no request has more new tokens.  Rows past it are not
- *               computed.  R * max_q * Hq < 2^26 (QG_ESHAPE).
+ *  max_q        1..32: no request has more new tokens; of one that has, the
+ *               first max_q rows become NaN and the others are left.  R * max_q * Hq < 2^26 (QG_ESHAPE).
  *  max_len      1..max_blocks * page: no request is longer; a longer one gets
  *               rows of NaN.  (The product of requests, heads, row groups and
  *               max_len / 32 has to stay below 2^31: QG_ESHAPE.)

@@ -93,7 +93,7 @@ __device__ __forceinline__ float pow2_above(float x) {
 // from `start` on.
 struct Req {
     int q0, T, len, start, units, groups;  // groups of RW rows
-    bool too_long;                         // longer than the call was told of: its rows become NaN
+    bool too_long;                         // more tokens, or new ones, than the call was told of: its rows become NaN
     __device__ __forceinline__ int work(int Hkv) const { return units * groups * Hkv; }
 };
 
@@ -111,10 +111,11 @@ template <int RW>
 __device__ __forceinline__ Req req_of(Args &a, int r) {
     Req s;
     s.q0 = a.q_start[r];
-    s.T = min(max(a.q_start[r + 1] - s.q0, 0), a.max_q);
-    if (s.q0 < 0 || s.q0 + s.T > a.M) s.T = 0;
+    const int T = max((int)((unsigned)a.q_start[r + 1] - (unsigned)s.q0), 0);
+    s.T = min(T, a.max_q);
+    if (s.q0 < 0 || s.q0 > a.M - s.T) s.T = 0;
     s.len = min(max(a.lens[r], 0), a.max_blocks * a.page);
-    s.too_long = s.len > a.max_len;
+    s.too_long = s.len > a.max_len || T > a.max_q;
     s.start = a.window > 0 ? max(s.len - s.T - a.window + 1, 0) & ~(KV_STEP - 1) : 0;
     s.units = s.T == 0 ? 0 : s.too_long ? 1 : max((s.len - s.start + KV_STEP - 1) / KV_STEP, 1);
     s.groups = (s.T * a.G + RW - 1) / RW;

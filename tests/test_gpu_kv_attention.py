@@ -288,6 +288,30 @@ def test_more_rows_than_max_q_are_left_alone():
     assert bool((out[4:] == 3).all())
 
 
+@pytest.mark.parametrize("lens", [[100, 90], [3000, 2500]])
+def test_more_rows_than_max_q_are_seen(lens):
+    c = Case(34, lens, [6, 3], D=64)
+    a = dict(c.args(), max_q=4)
+    want = pkg.kv_attention_run(c.cache(), **c.args())
+    out = torch.full((c.M, c.H * c.G, c.D), 3.0, dtype=torch.bfloat16, device=DEV)
+    pkg.kv_attention_run(c.cache(), **a, out=out)
+    torch.cuda.synchronize()
+    assert torch.isnan(out[:4]).all() and bool((out[4:6] == 3).all())
+    out[:6] = want[:6]
+    c.check(out)
+
+
+def test_q_start_past_all_rows():
+    """Offsets near the end of 32 bits: not computed, and nothing else is."""
+    c = Case(35, [100, 70, 50], [2, 2, 2], D=64)
+    a = c.args()
+    a["q_start"] = torch.tensor([0, 2, 2 ** 31 - 1, -2 ** 31 + 4], dtype=torch.int32, device=DEV)
+    out = torch.full((c.M, c.H * c.G, c.D), 3.0, dtype=torch.bfloat16, device=DEV)
+    got = pkg.kv_attention_run(c.cache(), **dict(a, max_q=32), out=out)
+    torch.cuda.synchronize()
+    assert torch.isfinite(got[:2]).all() and bool((got[2:] == 3).all())
+
+
 def test_q_start_that_cannot_be():
     """Offsets past the rows of q: those requests are not computed."""
     c = Case(19, [100, 70], [2, 2], D=64)
