@@ -30,7 +30,7 @@
 // 256, E4M3: 46.6 us, 5.8 TB/s; 330693 tokens in 48 requests, 8 heads of 128,
 // int8: 126 us, 5.4 TB/s; the joins 6.5 us each), by the vector unit's
 // conversions and softmax for many (128 rows, 46784 tokens: 54.7 us, 340
-// TFLOP/s, join 10.8), by latency for short contexts (1021 tokens: 11 us).
+// TFLOP/s, join 10.2), by latency for short contexts (1021 tokens: 11 us).
 #include <type_traits>
 
 #include "kv_cache.h"
@@ -635,7 +635,9 @@ __global__ void __launch_bounds__(WAVES * 64, NR == 1 && D <= 128 && WAVES == 4 
 // waves for each.  D / 4 lanes take 4 dimensions each of one segment; the
 // waves' groups of them take the segments in turn, eight loads in flight a
 // lane, and join across lanes and in LDS.  Many rows take one wave each, few
-// rows eight.
+// rows eight.  The maximum runs along with the sums (read in a pass before
+// them: 128 rows 10.8 us against 10.2, 64 rows 7.8 against 7.4).  Bound by
+// latency: request, head of the workspace, segments in turn.
 template <int D, int RW, int W>
 __global__ void __launch_bounds__(512) kv_attn_join_kernel(KvAttnArgs) {
     constexpr int TD = D / 4, NG = W * 64 / TD, AHEAD = 8, ROWS = 8 / W;
@@ -665,16 +667,8 @@ __global__ void __launch_bounds__(512) kv_attn_join_kernel(KvAttnArgs) {
     // (never so, unless another call wrote to the workspace in between)
     if (slot < 0 || n < 1 || n > a.part_slots || slot > a.part_slots - n) return;
     const size_t at = (size_t)slot * a.part_rows + row % RW, step = a.part_rows;
+    // with a running maximum, so that values and maxima are loaded together
     float mx = NEG_INF;
-    for (int c = tid; c < n; c += W * 64) mx = fmaxf(mx, a.part_ml[2 * (at + c * step)]);
-#pragma unroll
-    for (int d = 32; d; d >>= 1) mx = fmaxf(mx, __shfl_xor(mx, d));
-    if constexpr (W > 1) {
-        if (lane == 0) smx[wi] = mx;
-        __syncthreads();
-#pragma unroll
-        for (int w = 0; w < W; ++w) mx = fmaxf(mx, smx[w]);
-    }
     f32x4_t o = {0.f, 0.f, 0.f, 0.f};
     float l = 0.f;
     for (int c0 = gi; c0 < n; c0 += NG * AHEAD) {
@@ -686,6 +680,13 @@ __global__ void __launch_bounds__(512) kv_attn_join_kernel(KvAttnArgs) {
             v[i] = *reinterpret_cast<const f32x4_t *>(a.part + (at + c * step) * D + 4 * d4);
             ml[i] = *reinterpret_cast<const f32x2_t *>(a.part_ml + 2 * (at + c * step));
         }
+        float mn = mx;
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) mn = fmaxf(mn, ml[i][0]);
+        const float down = mn == NEG_INF ? 1.f : __builtin_amdgcn_exp2f(mx - mn);
+        mx = mn;
+        l *= down;
+        o *= down;
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
             // (a row of NaN scores has no maximum, but a NaN sum)
@@ -697,6 +698,12 @@ __global__ void __launch_bounds__(512) kv_attn_join_kernel(KvAttnArgs) {
         }
     }
     // the wave's groups of lanes, then the waves
+    float top = mx;
+#pragma unroll
+    for (int d = TD; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+    const float down = top == NEG_INF ? 1.f : __builtin_amdgcn_exp2f(mx - top);
+    l *= down;
+    o *= down;
 #pragma unroll
     for (int d = TD; d < 64; d <<= 1) {
         l += __shfl_xor(l, d);
@@ -705,13 +712,23 @@ __global__ void __launch_bounds__(512) kv_attn_join_kernel(KvAttnArgs) {
     }
     if constexpr (W > 1) {
         if (lane < TD) so[wi][lane] = o;
-        if (lane == 0) sl[wi] = l;
+        if (lane == 0) {
+            sl[wi] = l;
+            smx[wi] = top;
+        }
         __syncthreads();
         if (wi != 0) return;
+        const float mine = top;
+#pragma unroll
+        for (int k = 1; k < W; ++k) top = fmaxf(top, smx[k]);
+        const float own = top == NEG_INF ? 1.f : __builtin_amdgcn_exp2f(mine - top);
+        o *= own;
+        l *= own;
 #pragma unroll
         for (int k = 1; k < W; ++k) {
-            o += so[k][lane % TD];
-            l += sl[k];
+            const float f = top == NEG_INF ? 1.f : __builtin_amdgcn_exp2f(smx[k] - top);
+            o += so[k][lane % TD] * f;
+            l = fmaf(sl[k], f, l);
         }
     }
     if (lane >= TD) return;
