@@ -12,8 +12,9 @@
 // carried in fp64.  Otherwise fp32 decides, except where its value p (of four
 // roundings, so off by at most 4 * 2^-24 |p| < 2.5e-7 |p|) is that near a
 // border: that element is computed again in fp64 from its inputs.  So are,
-// for max |z|, the elements within 2^-21 of fp32's largest.  r for y and the
-// sum of squares are fp32.
+// for max |z|, the elements within 2^-21 of fp32's largest, and all elements of
+// a row whose largest product fp32 has below 2^-60 or as infinite.  r for y and
+// the sum of squares are fp32.
 //
 // One workgroup per row; a thread holds U units of 8 consecutive elements, the
 // four lanes of a quad one block of 32.  Bound by latency for a few rows (2.4
@@ -165,11 +166,11 @@ __global__ void __launch_bounds__(U == 4 ? 256 : 1024) rmsnorm_kernel(RmsArgs a)
         ss += wss[w];
         if (Q) amax = fmax(amax, wmax[w]);
     }
-    // products this small have lost bits in fp32, or all of them: fp64 decides
-    // every element
-    const bool tiny = Q && !ROT && amax < 0x1p-60;
+    // products this small have lost bits in fp32, or all of them, and some past
+    // its range are infinite in it: fp64 decides every element
+    const bool by64 = Q && !ROT && !(amax >= 0x1p-60 && amax < (double)__builtin_inff());
     bool nonzero = true;  // (a row of zeros needs none of that)
-    if (tiny) {
+    if (by64) {
         unsigned any = 0u;
 #pragma unroll
         for (int i = 0; i < U; ++i)
@@ -186,7 +187,7 @@ __global__ void __launch_bounds__(U == 4 ? 256 : 1024) rmsnorm_kernel(RmsArgs a)
     // a row with a NaN or an infinity has no scale: codes 0, scale NaN
     const bool fin = ss < __builtin_inff();
     if (Q && !ROT && fin && nonzero) {
-        const float near = tiny ? 0.f : (float)amax * (1.f - 0x1p-21f);
+        const float near = by64 ? 0.f : (float)amax * (1.f - 0x1p-21f);
         unsigned mine = 0u;  // the thread's elements that may be the largest
 #pragma unroll
         for (int i = 0; i < U; ++i)
@@ -234,7 +235,7 @@ __global__ void __launch_bounds__(U == 4 ? 256 : 1024) rmsnorm_kernel(RmsArgs a)
             }
             u32x2_t o = {(q[0] & 0xFFu) | (q[1] & 0xFFu) << 8 | (q[2] & 0xFFu) << 16 | (unsigned)q[3] << 24,
                          (q[4] & 0xFFu) | (q[5] & 0xFFu) << 8 | (q[6] & 0xFFu) << 16 | (unsigned)q[7] << 24};
-            if (tiny) border = 0xFFu;
+            if (by64) border = 0xFFu;
             if (!fin || !(amax > 0.0)) {
                 o = u32x2_t{0u, 0u};
                 border = 0u;

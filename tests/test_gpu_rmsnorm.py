@@ -170,3 +170,23 @@ def test_other_stream_and_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(bufs, eager)), rep
+
+
+@pytest.mark.parametrize("xt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("res", [False, True])
+@pytest.mark.parametrize("K", [64, 4128, 8224])
+def test_products_past_fp32(K, res, xt):
+    """Rows whose sum of squares is finite and whose products with the weight
+    are not (in fp32): just past its end, far past it, and ordinary rows of
+    the same call.  The codes are the definition's."""
+    g = np.random.default_rng(K)
+    x = g.standard_normal((7, K)) * np.array([1e17, 1e16, 5e16, 1.0, 1e12, 0.0, 1e-3])[:, None]
+    w = g.standard_normal(K) * np.where(np.arange(K) % 3 == 0, 1e22, np.where(np.arange(K) % 7 == 0, 1e30, 1.0))
+    x, w = torch.from_numpy(x).to(xt), torch.from_numpy(w).to(torch.bfloat16)
+    r = torch.from_numpy(0.1 * to_np(x) * g.standard_normal((7, K))).to(xt) if res else None
+    with np.errstate(over="ignore"):
+        p = (to_np(x) + (to_np(r) if res else 0)).astype(np.float32) * to_np(w).astype(np.float32)
+    assert np.isinf(p).any(1).tolist() == [True, True, True, False, True, False, False]
+    for M in (7, 600):
+        rep = lambda t: None if t is None else t.repeat((M + 6) // 7, 1)[:M]  # noqa: E731
+        check(rep(x), rep(r), w, None, 1, 1)
