@@ -492,15 +492,17 @@ __global__ void __launch_bounds__(WAVES * 64, NR == 1 && D <= 128 && WAVES == 4 
         // every row sees all of the steps before this one (the first new token
         // only where there is no tree)
         const int t_clear = a.window > 0 ? t_lo : min(t_hi, (base + (a.tree ? 0 : 1)) & ~(KV_STEP - 1));
-        // vref: a power of two at least as large as every value scale so far;
+        // vref: a power of two at least as large as every value scale so far (0
+        // before the first: a page whose values are all 0 has none, and what it
+        // left in o and ps is nothing but the codes' bias, which f = 0 clears);
         // a page's scale over it, as a power of two in the exponent, and its
-        // inverse (a page whose values are all 0 has no scale)
+        // inverse
         float up = fmaxf(my_vs, 0.f);
 #pragma unroll
         for (int d = 32; d; d >>= 1) up = fmaxf(up, __shfl_xor(up, d));
         up = readlane_f(up, 0);
-        if (t_lo == t_begin || up > vref) {
-            up = up > 0.f ? pow2_above(up) : 1.f;
+        if (up > vref) {
+            up = pow2_above(up);
             const float f = vref / up;
             vref = up;
 #pragma unroll

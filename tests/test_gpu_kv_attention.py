@@ -416,3 +416,135 @@ def test_given_stream_takes_its_own_memory(as_int):
         got = pkg.kv_attention_run(cache, stream=side.cuda_stream if as_int else side, **a)
         torch.cuda.synchronize()
         assert torch.equal(got, first)
+
+
+def reference(c, r, window=0, scale=None):
+    """Request r of a case in 64 bits, with what its tolerance needs: output,
+    sum of p |v| / l, largest sum of |scale q k|, l (p relative to the largest)
+    [T, Hq, ...] and the request's largest value scale that is attended to."""
+    page, D, G, H = c.page, c.D, c.G, c.H
+    e4m3 = c.fmt == pkg.KV_E4M3
+    dec = ref.e4m3_value if e4m3 else (lambda b: b.view(np.int8).astype(np.float64))
+    T, n, scale = int(c.T[r]), int(c.lens[r]), c.D ** -0.5 if scale is None else scale
+    rows = np.arange(c.q_start[r], c.q_start[r] + T)
+    ids = np.asarray(c.table[r][: -(-n // page)])
+    there = (ids >= 0) & (ids < len(c.k))
+    safe = np.where(there, ids, 0)
+    t, pos = np.arange(n), n - T + np.arange(T)
+    see = (t[None, :] <= pos[:, None]) & np.repeat(there, page)[None, :n]
+    if window:
+        see &= t[None, :] > pos[:, None] - window
+    out, A, S, L = np.zeros((T, H * G, D)), np.zeros((T, H * G, D)), np.zeros((T, H * G)), np.ones((T, H * G))
+    for h in range(H):
+        K = (dec(np.ascontiguousarray(c.k[safe, h])) * c.ks[safe, h].astype(np.float64)[:, None, None]).reshape(-1, D)[:n]
+        V = (dec(np.ascontiguousarray(c.v[safe, h])) * c.vs[safe, h].astype(np.float64)[:, None, None]).reshape(-1, D)[:n]
+        for i in range(h * G, (h + 1) * G):
+            s = np.where(see, scale * (c.q[rows, i] @ K.T), -np.inf)
+            top = s.max(1, keepdims=True)
+            p = np.exp(s - np.where(np.isinf(top), 0.0, top))
+            l = np.maximum(p.sum(1), 1e-300)
+            out[:, i], A[:, i] = p @ V / l[:, None], p @ np.abs(V) / l[:, None]
+            S[:, i] = np.where(see, abs(scale) * (np.abs(c.q[rows, i]) @ np.abs(K).T), 0.0).max(1)
+            L[:, i] = l
+    seen = ids[there]
+    return out, A, S, L, float(c.vs[seen].max()) if len(seen) else 0.0
+
+
+def check_requests(c, got, requests, f32=False, window=0, scale=None, teeth=4.0):
+    """The requests' rows against the tolerance of this file's head, with what
+    a probability may lose below f16's normal range counted against the row's
+    own sum l and the request's own scales; the outputs' size has to be `teeth`
+    times it in the median, so that a wrong one is seen."""
+    got = to_np(got)
+    for r in requests:
+        o, A, S, L, vs = reference(c, r, window, scale)
+        n = int(c.lens[r])
+        vmax = vs * (127 if c.fmt == pkg.KV_INT8 else 448)
+        d = (c.D + 4) * 2.0 ** -23 * S[:, :, None]
+        tol = ((2.0 ** -24 if f32 else 2.0 ** -8) * np.abs(o) + (2.0 ** -11 + 2 * d + 2 * n * 2.0 ** -24 + 2.0 ** -20) * A
+               + n * 2.0 ** -25 * 2 * vmax / L[:, :, None])
+        mine = got[c.q_start[r]: c.q_start[r + 1]]
+        assert np.all(np.isfinite(mine)), r
+        err = np.abs(mine - o) / tol.clip(1e-300)
+        assert err.max() <= 1, (r, err.max(), np.argwhere(err > 1)[:3])
+        assert teeth == 0 or np.median(np.abs(o) / tol.clip(1e-300)) >= teeth, (r, np.median(np.abs(o) / tol))
+
+
+def long_case(seed, R, n, T, H, G, D, fmt, pool=700, order=1):
+    """R requests of about n tokens on shuffled pages of a shared pool of 32
+    token pages, value scales over a factor of 100 and rising along each
+    request (order 1), falling (-1) or mixed (0); the softmax of a row lies on
+    few tokens."""
+    c = Case(seed, [32 * pool], [T], H=H, G=G, D=D, page=32, fmt=fmt, pages=pool)
+    g = c.g
+    c.vs *= np.exp(g.uniform(np.log(0.01), 0, pool)).astype(np.float32)[:, None]
+    c.lens = n - g.integers(0, 90, R)
+    cols = -(-n // 32)
+    rank = np.argsort(c.vs[:, 0])
+    if order:
+        c.table = np.stack([rank[np.sort(g.permutation(pool)[:cols])][::order] for _ in range(R)])
+    else:
+        c.table = np.stack([g.permutation(pool)[:cols] for _ in range(R)])
+    c.T = np.full(R, T)
+    c.q_start = np.concatenate([[0], np.cumsum(c.T)])
+    c.M = R * T
+    c.q = to_np(torch.from_numpy(3 * g.standard_normal((c.M, H * G, D))).to(torch.bfloat16))
+    return c
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("order", [-1, 0, 1])
+@pytest.mark.parametrize("R,n,T,H,G,D", [(64, 10240, 1, 16, 1, 64), (60, 8000, 3, 10, 5, 128), (40, 20480, 1, 8, 8, 256),
+                                         (40, 20480, 8, 4, 4, 64), (40, 20480, 8, 4, 8, 128), (40, 20480, 16, 4, 8, 64),
+                                         (40, 20480, 8, 4, 4, 256), (40, 20480, 16, 4, 4, 256)])
+def test_runs_past_64_pages(R, n, T, H, G, D, order, fmt):
+    """Workgroups whose run passes the 64 pages whose entries a wave holds at
+    once, for each number of rows."""
+    note("attention runs past 64 pages fmt=%d order=%d T=%d G=%d D=%d" % (fmt, order, T, G, D))
+    c = long_case(40 + T + D, R, n, T, H, G, D, fmt, order=order)
+    got = pkg.kv_attention_run(c.cache(), **c.args())
+    torch.cuda.synchronize()
+    assert torch.isfinite(got).all()
+    check_requests(c, got, [0, R - 1])
+
+
+@pytest.mark.parametrize("n,T", [(5003, 1), (5003, 9), (9001, 1)])
+def test_cut_contexts_against_their_own_sums(n, T):
+    c = Case(50 + n, [n, 700, 33], [T, 1, 2], H=2, G=4, D=64, page=32, qscale=3.0)
+    for dt in (pkg.OUT_BF16, pkg.OUT_F32):
+        got = pkg.kv_attention_run(c.cache(), **c.args(), out_dtype=dt)
+        torch.cuda.synchronize()
+        check_requests(c, got, range(3), f32=dt == pkg.OUT_F32)
+
+
+def test_scales_of_other_requests_do_not_count():
+    """Value scales 2^80 apart between the requests of a call, each request
+    checked against its own; one has blocks of zeros among small ones."""
+    c = Case(51, [640, 64, 96, 3000, 1500], [1, 1, 3, 2, 1], D=64, page=32, qscale=3.0)
+    nb = lambda r: -(-c.lens[r] // 32)  # noqa: E731
+    for r, s in enumerate([2.0 ** 20, 0.0, 2.0 ** -60, 1e-9, 2.0 ** -30]):
+        c.vs[c.table[r, : nb(r)]] *= np.float32(s)
+    c.vs[c.table[4, : nb(4): 3]] = 0.0
+    for fmt_out in (pkg.OUT_BF16, pkg.OUT_F32):
+        got = pkg.kv_attention_run(c.cache(), **c.args(), out_dtype=fmt_out)
+        torch.cuda.synchronize()
+        check_requests(c, got, [0, 2, 3, 4], f32=fmt_out == pkg.OUT_F32)
+        assert not got[1].any()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("T,H,G,R,n", [(1, 16, 1, 64, 10240), (8, 4, 8, 40, 20480)])
+def test_first_pages_without_values(T, H, G, R, n, fmt):
+    """The first 130 pages of a request are not there, or hold only zeros, and
+    the others' scales are small: those others decide all the bits."""
+    note("attention first pages without values fmt=%d T=%d" % (fmt, T))
+    c = long_case(60 + T, R, n, T, H, G, 64, fmt, order=0)
+    c.vs = ((0.3 + c.g.random(c.vs.shape)) * 2.0 ** -20).astype(np.float32)
+    zero = 5
+    c.vs[zero] = 0.0
+    c.table[c.table == zero] = 6
+    c.table[::2, :130] = -1
+    c.table[1::2, :130] = zero
+    got = pkg.kv_attention_run(c.cache(), **c.args())
+    torch.cuda.synchronize()
+    check_requests(c, got, [0, 1, 2, R - 1])
