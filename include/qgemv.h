@@ -640,8 +640,13 @@ size_t qg_kv_attention_workspace_bytes(int64_t R, int64_t M, int64_t Hq, int64_t
  *  out          device [M][Hq][D] bf16 or fp32, 16-B, rows out_stride
  *               elements apart (a multiple of 8, at least Hq * D).  Rows of
  *               no request are left as they are.
- * Sums and the softmax's statistics are fp32, probabilities enter the second
- * product in f16.  A row's result does not depend on other rows; it is the
+ * Sums and the softmax's statistics are fp32.  Probabilities p, relative to the
+ * largest of a part of the request, enter the second product in f16 as
+ * p * vs / vref, vref being the power of two above the largest value scale met
+ * so far in that part: rounded to 2^-11 of themselves down to 2^-21, with an
+ * error of up to 2^-32 below.  So a row whose weight lies on pages whose value
+ * scale is far below 2^-21 of another page's in its request loses bits, and is
+ * 0 from 2^-32 on.  A row's result does not depend on other rows; it is the
  * same in every run.
  * Errors: QG_EINVAL, QG_ESHAPE, QG_EALIGN, QG_ESIZE, QG_EUNSUPPORTED (a tree
  * with a window, QG_OUT_I32_GROUPS), QG_EHIP.

@@ -12,10 +12,12 @@
 // these are the tokens whose values its V load brings: O^T += V^T P^T takes
 // the probabilities from their registers.  Sums, maxima and O are fp32; p is
 // rounded to f16 (11 bits; the output has 8 in bf16).  The running maximum
-// is only raised when a score passes it by 8 (in powers of two: p <= 2^8 is
-// far inside f16), so most steps neither exchange across lanes nor rescale O.
-// The value scales enter p as vs / vref with vref a power of two at least as
-// large as every vs of the chunk.
+// is only raised when a score passes it by 8 (in powers of two: p <= 2^8, and
+// 2^7 p is inside f16), so most steps neither exchange across lanes nor rescale
+// O.  The value scales enter p as vs / vref with vref a power of two at least
+// as large as every vs that the wave has met in its segment.  So 2^7 p vs / vref
+// is what f16 rounds: to 2^-11 of it down to p vs / vref = 2^-21, below that
+// by up to 2^-32.
 //
 // The work is a line of (request, head, group of 16 NR RS rows, step).  It is
 // cut into one equal run for each of the workgroups that fit the GPU at once,
@@ -43,6 +45,11 @@ typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
 
 constexpr float NEG_INF = -__builtin_inff();
+
+// Probabilities are carried as 2^P_EXP p (in o, l and ps alike, so that it
+// falls out of o / l): with p <= 2^8 that fills f16's range upwards, and what
+// its normal range loses below starts at p vs / vref = 2^-21.
+constexpr float P_EXP = 7.f, P_UNIT = 0x1p7f;
 
 // An int8 code c enters the MFMA as the f16 whose bits are c + 128: a
 // denormal (which the MFMA keeps), worth (c + 128) 2^-24.  The products'
@@ -465,7 +472,7 @@ __global__ void __launch_bounds__(WAVES * 64, NR == 1 && D <= 128 && WAVES == 4 
 #pragma unroll
                 for (int e = 0; e < 8; ++e) sum += __builtin_amdgcn_exp2f(x[e] + nm[n]);
                 sum += __shfl_xor(sum, 16);
-                l[n] += sum + __shfl_xor(sum, 32);
+                l[n] = fmaf(sum + __shfl_xor(sum, 32), P_UNIT, l[n]);
             }
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -512,7 +519,7 @@ __global__ void __launch_bounds__(WAVES * 64, NR == 1 && D <= 128 && WAVES == 4 
                 for (int d = 0; d < DT; ++d) o[n][d] *= f;
             }
         }
-        my_lr = my_vs > 0.f ? __builtin_amdgcn_logf(my_vs / vref) : 0.f;
+        my_lr = (my_vs > 0.f ? __builtin_amdgcn_logf(my_vs / vref) : 0.f) + P_EXP;
         my_rr = my_vs > 0.f ? vref / my_vs : 1.f;
         if constexpr (SHARED) {
             // two steps' parts in registers, two in LDS: a part is written to

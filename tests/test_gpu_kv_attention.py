@@ -548,3 +548,26 @@ def test_first_pages_without_values(T, H, G, R, n, fmt):
     got = pkg.kv_attention_run(c.cache(), **c.args())
     torch.cuda.synchronize()
     check_requests(c, got, [0, 1, 2, R - 1])
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("T,G", [(1, 4), (8, 4), (16, 8)])
+def test_weight_on_pages_of_small_scale(T, G, fmt):
+    """All of a row's weight lies on a page whose value scale is 1.3 * 2^-20
+    beside a page of scale 1 that every row scores far below it.  The equal
+    probabilities p vs / vref 2^7 = 1.3 * 2^-13 are normal in f16: half a step
+    is 2^-11 of each, so of the output."""
+    c = Case(70, [64], [T], H=1, G=G, D=64, page=32, fmt=fmt)
+    far, near = (int(p) for p in c.table[0, :2])
+    low = np.full(64, 100 if fmt == pkg.KV_INT8 else 448.0)
+    c.q = np.abs(c.q) + 1.0
+    c.q = to_np(torch.from_numpy(c.q).to(torch.bfloat16))
+    c.k[far, 0] = (-low).astype(np.int8).view(np.uint8) if fmt == pkg.KV_INT8 else ref.e4m3_bits(low) | 0x80
+    c.k[near] = 0
+    c.ks[:] = 0.1
+    c.vs[far], c.vs[near] = 1.0, 1.3 * 2.0 ** -20
+    got = pkg.kv_attention_run(c.cache(), **c.args(), out_dtype=pkg.OUT_F32)
+    torch.cuda.synchronize()
+    o, A = reference(c, 0)[:2]
+    # half a step of f16, and fp32 sums of 32 products, the scales and exp2
+    assert np.all(np.abs(to_np(got) - o) <= (2.0 ** -11 + 64 * 2.0 ** -24 + 2.0 ** -20) * A)
