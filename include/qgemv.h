@@ -628,7 +628,7 @@ size_t qg_kv_attention_workspace_bytes(int64_t R, int64_t M, int64_t Hq, int64_t
  *               is not attended to.  max_blocks * page <= 2^30.
  *  tree_mask    device uint32 [M] or NULL: bit i = the request's new token i.
  *  window       0 (none), or 1..2^30; with tree_mask: 0 only.
- *  scale        of the scores, finite; usually 1 / sqrt(D).
+ *  scale        of the scores, below 2^127 in magnitude; usually 1 / sqrt(D).
  *  max_q        1..32: no request has more new tokens; of one that has, the
  *               first max_q rows become NaN and the others are left.  R * max_q * Hq < 2^26 (QG_ESHAPE).
  *  max_len      1..max_blocks * page: no request is longer; a longer one gets

@@ -198,7 +198,8 @@ int kv_attention_run(const qg_kv_cache *cache, int64_t R, int64_t M, int64_t Hq,
             !attention_plan(R, M, Hq, cache->Hkv, cache->D, cache->page, max_q, max_len, window, &p, &need) ||
             !row_stride(q_stride, Hq * cache->D) || !row_stride(out_stride, Hq * cache->D))
             return QG_ESHAPE;
-        if (!std::isfinite(scale)) return QG_EINVAL;
+        const float scale2 = scale * 1.44269504088896340736f;  // scores in powers of two
+        if (!std::isfinite(scale2)) return QG_EINVAL;
         if (!q || !q_start || !lens || !table || !out || (need && !workspace)) return QG_EINVAL;
         if (need && workspace_bytes < need) return QG_ESIZE;
         if (!aligned(q, 16) || !aligned(q_start, 4) || !aligned(lens, 4) || !aligned(table, 4) ||
@@ -239,7 +240,7 @@ int kv_attention_run(const qg_kv_cache *cache, int64_t R, int64_t M, int64_t Hq,
         a.part_slots = (int)p.part_slots;
         a.whole = p.whole;
         a.aligned = p.aligned;
-        a.scale = scale * 1.44269504088896340736f;  // scores in powers of two
+        a.scale = scale2;
         a.out_f32 = out_dtype == QG_OUT_F32;
         return hip_status(launch_kv_attention(a, cache->D, cache->fmt == QG_KV_E4M3,
                                               reinterpret_cast<hipStream_t>(stream)));

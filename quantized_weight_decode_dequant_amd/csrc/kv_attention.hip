@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(WAVES * 64, NR == 1 && D <= 128 && WAVES == 4 
             my_page = a.table[(size_t)r * a.max_blocks + page0 + lane];
             if (my_page < 0 || my_page >= a.pages) my_page = -1;
             if (my_page >= 0) {
-                my_ks = a.k_scales[(size_t)my_page * a.Hkv + h];
+                my_ks = a.k_scales[(size_t)my_page * a.Hkv + h] * UNIT;
                 my_vs = a.v_scales[(size_t)my_page * a.Hkv + h];
             }
         }
@@ -362,7 +362,9 @@ __global__ void __launch_bounds__(WAVES * 64, NR == 1 && D <= 128 && WAVES == 4 
             sum += __shfl_xor(sum, 32);
         }
         k0[n] = -(BIAS / UNIT) * sum;
-        cs[n] = ldexpf(fabsf(a.scale) * UNIT, -e2);
+        // (the codes' unit goes to the pages' scales: with it, large queries'
+        // factor would leave fp32's range where the scores do not)
+        cs[n] = ldexpf(fabsf(a.scale), -e2);
     }
 
     f32x4_t o[NR][DT];  // sums of p times values, in units of vref (/ UNIT, biased)

@@ -155,3 +155,12 @@ def test_binding_refuses_host_tensors_and_wrong_types():
         pkg.KVCache(codes.half(), codes.half(), scales, scales)
     with pytest.raises(ValueError, match="unknown cache format"):
         pkg.KVCache.empty(4, 64, 2, 64, fmt=9, device="cpu")
+
+
+def test_attention_scales_past_fp32_in_powers_of_two():
+    """scale * log2(e) is what the kernels take: it has to be finite too."""
+    lib = pkg.raw()
+    ws = pkg.kv_attention_workspace_bytes(3, 5, 8, 2, 128, 64, 4, 2560)
+    desc = cache()
+    for scale, want in ((3e38, L.QG_EINVAL), (-3e38, L.QG_EINVAL), (2.3e38, L.QG_EALIGN), (-2.0 ** 127, L.QG_EALIGN)):
+        assert lib.kv_attention_run(C.addressof(desc), 3, 5, 8, A + 2, 1024, A, A, A, 40, None, 0, scale, 4, 2560, A, ws, A, 1024, 0, None) == want

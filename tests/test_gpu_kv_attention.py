@@ -571,3 +571,29 @@ def test_weight_on_pages_of_small_scale(T, G, fmt):
     o, A = reference(c, 0)[:2]
     # half a step of f16, and fp32 sums of 32 products, the scales and exp2
     assert np.all(np.abs(to_np(got) - o) <= (2.0 ** -11 + 64 * 2.0 ** -24 + 2.0 ** -20) * A)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("qexp,scale,kexp", [(122, None, -104), (120, -1.0, -100), (0, 2.0 ** 118, -104), (-100, 2.0 ** 126, -20)])
+@pytest.mark.parametrize("n", [96, 3000])
+def test_large_queries_and_scales(n, qexp, scale, kexp, fmt):
+    """Queries near bf16's end, and large scales, with scores inside fp32: the
+    token of the largest score is all of the softmax."""
+    c = Case(80, [n], [2], H=1, G=2, D=64, page=32, fmt=fmt)
+    best = [n - 3, 17]                      # for either sign of the scale
+    c.q = np.full(c.q.shape, 2.0 ** qexp)
+    code = np.zeros(n, np.int64)
+    code[best[0]], code[best[1]] = 2, -2
+    for t in range(n):
+        p, o = int(c.table[0, t // 32]), t % 32
+        v = np.full(64, float(code[t]))
+        c.k[p, 0, o] = v.astype(np.int8).view(np.uint8) if fmt == pkg.KV_INT8 else ref.e4m3_bits(v)
+    c.ks[:] = 2.0 ** kexp
+    got = pkg.kv_attention_run(c.cache(), **c.args(), scale=scale)
+    torch.cuda.synchronize()
+    t = best[1] if scale is not None and scale < 0 else best[0]
+    p, o = int(c.table[0, t // 32]), t % 32
+    dec = ref.e4m3_value if fmt == pkg.KV_E4M3 else (lambda b: b.view(np.int8).astype(np.float64))
+    want = dec(np.ascontiguousarray(c.v[p, 0, o])) * float(c.vs[p, 0])
+    # the other tokens are 2^-1000 of it; f16's and bf16's half steps
+    assert np.all(np.abs(to_np(got) - want) <= (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -20) * np.abs(want) + 64 * 2.0 ** -24 * 448 * float(c.vs.max()))
