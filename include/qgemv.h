@@ -630,7 +630,7 @@ size_t qg_kv_attention_workspace_bytes(int64_t R, int64_t M, int64_t Hq, int64_t
  *  window       0 (none), or 1..2^30; with tree_mask: 0 only.
  *  scale        of the scores, below 2^127 in magnitude; usually 1 / sqrt(D).
  *  max_q        1..32: no request has more new tokens; of one that has, the
- *               first max_q rows become NaN and the others are left.  R * max_q * Hq < 2^26 (QG_ESHAPE).
+ *               first max_q rows become NaN and the others are left.  R * max_q * Hq <= 2^26 - 8 (QG_ESHAPE).
  *  max_len      1..max_blocks * page: no request is longer; a longer one gets
  *               rows of NaN.  (The product of requests, heads, row groups and
  *               max_len / 32 has to stay below 2^31: QG_ESHAPE.)

@@ -16,10 +16,10 @@ using namespace qg;
 constexpr int64_t INT32_END = int64_t(1) << 31;
 constexpr int64_t ROWS_MAX = int64_t(1) << 30;
 // A launch has fewer than 2^32 threads: the norm takes up to 1024 a row, the
-// append 8 a token, the attention's join 64 a row and head.
+// append 8 a token, the attention's join 64 a row and head, in workgroups of 8.
 constexpr int64_t NORM_ROWS_MAX = (int64_t(1) << 22) - 1;
 constexpr int64_t APPEND_TOKENS_MAX = int64_t(1) << 28;
-constexpr int64_t JOINS_END = int64_t(1) << 26;
+constexpr int64_t JOINS_MAX = (int64_t(1) << 26) - 8;
 constexpr int64_t LEN_MAX = int64_t(1) << 30;
 constexpr int64_t STRIDE_MAX = int64_t(1) << 31;
 
@@ -50,7 +50,7 @@ bool attention_plan(int64_t R, int64_t M, int64_t Hq, int64_t Hkv, int64_t D, in
                     int64_t max_q, int64_t max_len, int64_t window, KvAttnPlan *p, size_t *bytes) {
     if (R < 0 || R > KV_R_MAX || M < 0 || M > ROWS_MAX || Hkv < 1 || Hkv > 1024 || Hq < 1 || Hq > 8192 ||
         Hq % Hkv || !head_size(D) || !page_size(page) || max_q < 1 || max_q > KV_ROWS_MAX ||
-        max_len < 1 || max_len > LEN_MAX || window < 0 || window > LEN_MAX || R * max_q * Hq >= JOINS_END)
+        max_len < 1 || max_len > LEN_MAX || window < 0 || window > LEN_MAX || R * max_q * Hq > JOINS_MAX)
         return false;
     const int64_t seen = window > 0 && window + max_q - 1 < max_len ? window + max_q - 1 : max_len;
     if (!kv_attention_plan(R, Hkv, Hq / Hkv, D, max_q, seen, p)) return false;

@@ -164,3 +164,18 @@ def test_attention_scales_past_fp32_in_powers_of_two():
     desc = cache()
     for scale, want in ((3e38, L.QG_EINVAL), (-3e38, L.QG_EINVAL), (2.3e38, L.QG_EALIGN), (-2.0 ** 127, L.QG_EALIGN)):
         assert lib.kv_attention_run(C.addressof(desc), 3, 5, 8, A + 2, 1024, A, A, A, 40, None, 0, scale, 4, 2560, A, ws, A, 1024, 0, None) == want
+
+
+def test_attention_joins_that_fill_a_launch():
+    """2731 * 3 * 8191 = 2^26 - 1 joins: 2^23 workgroups of 512 are 2^32 threads."""
+    lib = pkg.raw()
+    desc = cache(Hkv=1)
+
+    def call(R, max_q, Hq, q=A):
+        return lib.kv_attention_run(C.addressof(desc), R, 5, Hq, q, Hq * 128, A, A, A, 40, None, 0, 0.1, max_q, 64, A, 1 << 40, A,
+                                    Hq * 128, 0, None)
+
+    assert call(2731, 3, 8191) == L.QG_ESHAPE
+    assert call(2731, 3, 8190, A + 2) == L.QG_EALIGN
+    assert pkg.kv_attention_workspace_bytes(2731, 5, 8191, 1, 128, 64, 3, 5000) == 0
+    assert pkg.kv_attention_workspace_bytes(2731, 5, 8190, 1, 128, 64, 3, 5000) > 0
