@@ -550,7 +550,8 @@ typedef struct qg_kv_cache {
  *  free_count   device int32 [1], in/out: how many it holds.
  *  q_start      device int32 [R + 1], written: prefix sums of add.
  *  slots        device int32 [max_tokens], written: the slot of each new
- *               token, requests in order; -1 behind the last one.
+ *               token, requests in order; -1 behind the last one, and where
+ *               the page id found is outside [0, pages).
  *  positions    device int32 [max_tokens], written: its position in its
  *               request; 0 behind the last one.
  *  status       device int32 [1], written: 0, or a sum of 1 (not enough free

@@ -44,6 +44,13 @@ __device__ __forceinline__ Req request(const KvTablesArgs &a, int r) {
     return q;
 }
 
+// Where token pos of request r lies; -1 on a page id outside the pool (which
+// the shift could wrap into it).
+__device__ __forceinline__ int slot_of(const KvTablesArgs &a, int r, int pos) {
+    const int page = a.table[(size_t)r * a.max_blocks + (pos >> a.page_bits)];
+    return page >= 0 && page < a.pages ? (page << a.page_bits) + (pos & (a.page - 1)) : -1;
+}
+
 // the last i with p[i] <= x, for p[0] = 0 <= x < p[n] ascending
 __device__ __forceinline__ int find(const int *p, int n, int x) {
     int lo = 0, hi = n;
@@ -194,7 +201,7 @@ __global__ void __launch_bounds__(TB) kv_tables_kernel(KvTablesArgs a) {
             if (i < tokens) {
                 const int r = find(q0, R, i);
                 pos = request(a, r).kept + (i - q0[r]);
-                slot = (a.table[(size_t)r * a.max_blocks + (pos >> a.page_bits)] << a.page_bits) + (pos & (a.page - 1));
+                slot = slot_of(a, r, pos);
             }
             a.slots[i] = slot;
             a.positions[i] = pos;
@@ -224,7 +231,7 @@ __global__ void __launch_bounds__(256) kv_slots_kernel(KvTablesArgs a) {
         if (i < tokens) {
             const int r = find(q0, R, i);
             pos = a.lens[r] - (q0[r + 1] - i);
-            slot = (a.table[(size_t)r * a.max_blocks + (pos >> a.page_bits)] << a.page_bits) + (pos & (a.page - 1));
+            slot = slot_of(a, r, pos);
         }
         a.slots[i] = slot;
         a.positions[i] = pos;

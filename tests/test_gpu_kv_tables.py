@@ -143,3 +143,24 @@ def test_graph_steps_on_its_own_buffers():
         for x, y in ((outs[0], q_start), (outs[1], slots), (outs[2], pos), (plain.lens, plain.plain.lens), (plain.table, plain.plain.table)):
             assert np.array_equal(x.cpu().numpy(), y)
         assert plain.free[: int(plain.count)].tolist() == plain.plain.free
+
+
+@pytest.mark.parametrize("max_tokens", [50, 5000])
+@pytest.mark.parametrize("page", [32, 256])
+def test_slots_of_pages_that_are_not_there(page, max_tokens):
+    """Page ids outside the pool, from the table or the free list, give slots
+    outside it too (-1), however large they are."""
+    pages, bits = 20, page.bit_length() - 1
+    t = lambda a: torch.tensor(a, dtype=torch.int32, device=DEV)  # noqa: E731
+    bad = [-1, pages, 1 << (32 - bits), (1 << (32 - bits)) + 3, 1 << (31 - bits), 2 ** 31 - 1, -2 ** 31]
+    ids = bad + [3]
+    lens, add = t([5] * len(ids) + [0] * len(ids)), t([3] * (2 * len(ids)))
+    table = t([[i, -1] for i in ids] + [[-1, -1]] * len(ids))
+    free, count = t(ids[::-1] + [-1] * (pages - len(ids))), t([len(ids)])
+    got = pkg.kv_tables_run(page, lens, add, table, free, count, max_tokens)
+    torch.cuda.synchronize()
+    assert int(got[3]) == 0 and table[len(ids):, 0].tolist() == ids
+    want = []
+    for first in (5, 0):
+        want += [3 * page + first + k if i == 3 else -1 for i in ids for k in range(3)]
+    assert got[1].tolist() == want + [-1] * (max_tokens - len(want))
