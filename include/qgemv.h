@@ -647,8 +647,10 @@ size_t qg_kv_attention_workspace_bytes(int64_t R, int64_t M, int64_t Hq, int64_t
  * so far in that part: rounded to 2^-11 of themselves down to 2^-21, with an
  * error of up to 2^-32 below.  So a row whose weight lies on pages whose value
  * scale is far below 2^-21 of another page's in its request loses bits, and is
- * 0 from 2^-32 on.  A row's result does not depend on other rows; it is the
- * same in every run.
+ * 0 from 2^-32 on.  A row's result does not depend on what other rows, or
+ * other requests' pages, hold, and is the same in every run; where its sums are
+ * cut, and so its last bits, goes by all requests' lengths and by R, Hq, max_q,
+ * max_len and window.
  * Errors: QG_EINVAL, QG_ESHAPE, QG_EALIGN, QG_ESIZE, QG_EUNSUPPORTED (a tree
  * with a window, QG_OUT_I32_GROUPS), QG_EHIP.
  */

@@ -597,3 +597,34 @@ def test_large_queries_and_scales(n, qexp, scale, kexp, fmt):
     want = dec(np.ascontiguousarray(c.v[p, 0, o])) * float(c.vs[p, 0])
     # the other tokens are 2^-1000 of it; f16's and bf16's half steps
     assert np.all(np.abs(to_np(got) - want) <= (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -20) * np.abs(want) + 64 * 2.0 ** -24 * 448 * float(c.vs.max()))
+
+
+@pytest.mark.parametrize("lens,T", [([300, 500, 31], [5, 1, 3]), ([2500, 9000, 40], [5, 1, 16])])
+def test_rows_depend_on_no_other_rows_values(lens, T):
+    """Bit-equal whatever other requests' queries, pages and scales hold, NaN
+    among it, for the same lengths; uncut contexts also for a request alone."""
+    c = Case(90, lens, T, D=128)
+    a = c.args()
+    first = pkg.kv_attention_run(c.cache(), **a)
+    whole = max(lens) <= 512
+    for r in range(3):
+        own = {int(p) for p in c.table[r] if p >= 0}
+        others = np.array([p not in own for p in range(c.pages)])
+        b = object.__new__(Case)
+        b.__dict__.update(c.__dict__)
+        b.k, b.v, b.ks, b.vs = c.k.copy(), c.v.copy(), c.ks.copy(), c.vs.copy()
+        b.k[others] = c.g.integers(0, 127, b.k[others].shape)
+        b.vs[others] *= 1000
+        b.ks[others] = np.nan
+        mine = slice(int(c.q_start[r]), int(c.q_start[r + 1]))
+        q = torch.full_like(a["q"], float("nan"))
+        q[mine] = a["q"][mine]
+        got = pkg.kv_attention_run(b.cache(), **dict(a, q=q))
+        torch.cuda.synchronize()
+        assert torch.equal(got[mine], first[mine]), r
+        if whole:
+            one = dict(a, q=a["q"][mine].clone(), q_start=torch.tensor([0, T[r]], dtype=torch.int32, device=DEV),
+                       lens=a["lens"][r:r + 1].clone(), table=a["table"][r:r + 1].clone())
+            alone = pkg.kv_attention_run(c.cache(), **one)
+            torch.cuda.synchronize()
+            assert torch.equal(alone, first[mine]), r
