@@ -51,6 +51,11 @@ constexpr float NEG_INF = -__builtin_inff();
 // its normal range loses below starts at p vs / vref = 2^-21.
 constexpr float P_EXP = 7.f, P_UNIT = 0x1p7f;
 
+// A wave's o and l leave it in this unit (with P_UNIT's inverse in it): sums
+// of p <= 2^8 over up to 2^16 tokens of values near fp32's end stay inside it,
+// and the smallest scale that an append writes, 2^-107, keeps 18 bits.
+constexpr float OUT_UNIT = 0x1p-31f;
+
 // An int8 code c enters the MFMA as the f16 whose bits are c + 128: a
 // denormal (which the MFMA keeps), worth (c + 128) 2^-24.  The products'
 // accumulators are corrected by -128 times the other operand's sum.
@@ -555,14 +560,16 @@ __global__ void __launch_bounds__(WAVES * 64, NR == 1 && D <= 128 && WAVES == 4 
         pages(t_hi);
         first_loads();
     }
-    // in true units
+    // o in OUT_UNITs
+    const float out_unit = vref * OUT_UNIT;
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
         const float back = -BIAS * ps[n];
+        l[n] *= OUT_UNIT;
 #pragma unroll
         for (int d = 0; d < DT; ++d)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[n][d][e] = fmaf(o[n][d][e], UNIT, back) * vref;
+            for (int e = 0; e < 4; ++e) o[n][d][e] = fmaf(o[n][d][e], UNIT, back) * out_unit;
     }
     // join the waves that split the tokens, half of them at a time
     if constexpr (TS > 1) {

@@ -628,3 +628,21 @@ def test_rows_depend_on_no_other_rows_values(lens, T):
             alone = pkg.kv_attention_run(c.cache(), **one)
             torch.cuda.synchronize()
             assert torch.equal(alone, first[mine]), r
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("exp", [118, 100, -107])
+@pytest.mark.parametrize("n,T,G", [(96, 1, 2), (5003, 1, 2), (5003, 8, 8)])
+def test_values_near_the_ends_of_fp32(n, T, G, exp, fmt):
+    """Value scales so large that unnormalised sums of the values pass fp32's
+    range, and the smallest that kv_append_run writes: the mean of all tokens
+    (scores of 0)."""
+    c = Case(85, [n, 40], [T, 1], H=1, G=G, D=64, page=32, fmt=fmt)
+    c.q[:] = 0.0
+    v = 60 + c.g.integers(0, 60, c.v.shape)
+    c.v = v.astype(np.uint8) if fmt == pkg.KV_INT8 else ref.e4m3_bits(v)
+    c.vs = ((0.5 + 0.5 * c.g.random(c.vs.shape)) * 2.0 ** exp).astype(np.float32)
+    for dt in (pkg.OUT_BF16, pkg.OUT_F32):
+        got = pkg.kv_attention_run(c.cache(), **c.args(), out_dtype=dt)
+        torch.cuda.synchronize()
+        check_requests(c, got, [0, 1], f32=dt == pkg.OUT_F32)
