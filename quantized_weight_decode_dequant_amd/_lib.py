@@ -530,9 +530,8 @@ def kv_tables_run(page: int, lens, add, table, free_pages, free_count, max_token
                   q_start=None, slots=None, positions=None, status=None, stream=None):
     """One step of block tables, lengths and the free list (all updated in
     place); int32 tensors: lens, add, keep [R], table [R, max_blocks],
-    free_pages [pages], free_count [1].  Outputs that are given may be longer
-    than needed; the rest of them is left alone.  Returns (q_start [R + 1],
-    slots [max_tokens], positions [max_tokens], status [1])."""
+    free_pages [pages], free_count [1].  Returns (q_start [R + 1], slots
+    [max_tokens], positions [max_tokens], status [1])."""
     torch = _torch()
     i32 = torch.int32
     if lens.dim() != 1 or table.dim() != 2 or free_pages.dim() != 1:
@@ -544,7 +543,7 @@ def kv_tables_run(page: int, lens, add, table, free_pages, free_count, max_token
             return _empty(n, i32, lens.device, stream)
         if t.dim() != 1 or t.shape[0] < n:
             raise ValueError("%s must hold at least %d values" % (name, n))
-        return t if t.shape[0] == n else t[:n]
+        return t
 
     q_start, status = out(q_start, R + 1, "q_start"), out(status, 1, "status")
     slots, positions = out(slots, max_tokens, "slots"), out(positions, max_tokens, "positions")

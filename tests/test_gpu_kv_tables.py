@@ -164,15 +164,3 @@ def test_slots_of_pages_that_are_not_there(page, max_tokens):
     for first in (5, 0):
         want += [3 * page + first + k if i == 3 else -1 for i in ids for k in range(3)]
     assert got[1].tolist() == want + [-1] * (max_tokens - len(want))
-
-
-def test_outputs_that_are_longer_than_asked_for():
-    """Buffers given for the largest step: what comes back is this step's part."""
-    t = lambda a: torch.tensor(a, dtype=torch.int32, device=DEV)  # noqa: E731
-    big = [torch.full((40,), 7, dtype=torch.int32, device=DEV) for _ in range(4)]
-    got = pkg.kv_tables_run(32, t([0, 0]), t([3, 2]), t([[-1], [-1]]), t([1, 0]), t([2]), 6, q_start=big[0], slots=big[1],
-                            positions=big[2], status=big[3])
-    assert [x.numel() for x in got] == [3, 6, 6, 1]
-    assert all(a.data_ptr() == b.data_ptr() for a, b in zip(got, big))
-    assert got[0].tolist() == [0, 3, 5] and got[1].tolist() == [0, 1, 2, 32, 33, -1] and got[2].tolist() == [0, 1, 2, 0, 1, 0]
-    assert all(bool((b[n:] == 7).all()) for b, n in zip(big, (3, 6, 6, 1)))
