@@ -531,7 +531,9 @@ def kv_tables_run(page: int, lens, add, table, free_pages, free_count, max_token
     """One step of block tables, lengths and the free list (all updated in
     place); int32 tensors: lens, add, keep [R], table [R, max_blocks],
     free_pages [pages], free_count [1].  Returns (q_start [R + 1], slots
-    [max_tokens], positions [max_tokens], status [1])."""
+    [max_tokens], positions [max_tokens], status [1]); one that was given comes
+    back as it is, and what it holds behind these sizes is left alone (not
+    cut off: two views cost a tenth of a step of the tables)."""
     torch = _torch()
     i32 = torch.int32
     if lens.dim() != 1 or table.dim() != 2 or free_pages.dim() != 1:

@@ -164,3 +164,19 @@ def test_slots_of_pages_that_are_not_there(page, max_tokens):
     for first in (5, 0):
         want += [3 * page + first + k if i == 3 else -1 for i in ids for k in range(3)]
     assert got[1].tolist() == want + [-1] * (max_tokens - len(want))
+
+
+def test_outputs_that_are_longer_than_asked_for():
+    """Buffers given for the largest step come back as they are, their tails
+    untouched; the append takes no more slots than it has rows."""
+    t = lambda a: torch.tensor(a, dtype=torch.int32, device=DEV)  # noqa: E731
+    big = [torch.full((40,), 7, dtype=torch.int32, device=DEV) for _ in range(4)]
+    got = pkg.kv_tables_run(32, t([0, 0]), t([3, 2]), t([[-1], [-1]]), t([1, 0]), t([2]), 6, q_start=big[0], slots=big[1],
+                            positions=big[2], status=big[3])
+    assert all(a is b for a, b in zip(got, big))
+    assert [x[:n].tolist() for x, n in zip(got, (3, 6, 6, 1))] == [[0, 3, 5], [0, 1, 2, 32, 33, -1], [0, 1, 2, 0, 1, 0], [0]]
+    assert all(bool((b[n:] == 7).all()) for b, n in zip(big, (3, 6, 6, 1)))
+    cache = pkg.KVCache.empty(2, 32, 1, 64)
+    rows = torch.zeros(6, 1, 64, dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(ValueError, match="slots must be"):
+        pkg.kv_append_run(cache, rows, rows, got[1])
