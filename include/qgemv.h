@@ -478,7 +478,7 @@ int qg_plain_read(const void *buf, size_t bytes, uint32_t *sink, int grid, void 
  *  residual_out device [M][K] of res_dtype, 16-B, receives r rounded to it;
  *               may be `residual` itself.  NULL: not written.  Must be NULL
  *               when residual is.
- *  weight       device bf16 [K], 16-B.
+ *  weight       device bf16 [K], 16-B, finite values.
  *  eps          > 0, finite.
  *  signs        device int8 [K], 16-B, each +1 or -1, or NULL (no rotation);
  *               NULL when Xq is.
@@ -487,7 +487,8 @@ int qg_plain_read(const void *buf, size_t bytes, uint32_t *sink, int grid, void 
  *  Xq, x_scales device int8 [M][K], 16-B, and fp32 [M], or both NULL; one of
  *               y and Xq is required.
  * The sum of squares is fp32.  A row of zeros gives Xq = 0, scale 0; a row
- * whose sum of squares is not finite gives Xq = 0 and scale NaN.  Outputs may
+ * whose sum of squares is not finite (NaN, infinities, |r| from about 10^17 on)
+ * gives Xq = 0 and scale NaN, and y what rs = NaN or 0 gives.  Outputs may
  * not overlap each other or the inputs, residual_out = residual apart.
  * Errors: QG_EINVAL, QG_ESHAPE, QG_EALIGN, QG_EUNSUPPORTED (QG_OUT_I32_GROUPS
  * as a type), QG_EHIP.
@@ -519,7 +520,8 @@ typedef enum { QG_KV_INT8 = 0, QG_KV_E4M3 = 1 } qg_kv_format;
 
 typedef struct qg_kv_cache {
     void *k, *v;                  /* device codes [pages][Hkv][page * D], 16-B */
-    float *k_scales, *v_scales;   /* device fp32 [pages][Hkv], not negative */
+    float *k_scales, *v_scales;   /* device fp32 [pages][Hkv]: 0, or from 2^-107
+                                     on (what kv_append_run writes) and finite */
     int64_t pages;                /* >= 1, pages * page < 2^31 */
     int32_t page;                 /* 32, 64, 128 or 256 */
     int32_t Hkv;                  /* 1..1024 */
@@ -599,8 +601,10 @@ int kv_append_run(const qg_kv_cache *cache, int64_t M, const void *K, int64_t k_
                   const void *V, int64_t v_stride, const int32_t *slots, void *stream);
 
 /*
- * Bytes of workspace kv_attention_run needs (0 for contexts so short that
- * the work on a request's tokens is not cut).  Pure host function; 0 for arguments the call would refuse.
+ * Bytes of workspace kv_attention_run needs (0 where the work on a request's
+ * tokens is not cut: max_len, or window + max_q - 1 if that is less, up to 1024
+ * with at most 16 rows (max_q * Hq / Hkv) and D <= 128, else up to 512).  Pure
+ * host function; 0 for arguments the call would refuse.
  */
 size_t qg_kv_attention_workspace_bytes(int64_t R, int64_t M, int64_t Hq, int64_t Hkv, int64_t D,
                                        int64_t page, int64_t max_q, int64_t max_len,
@@ -641,7 +645,8 @@ size_t qg_kv_attention_workspace_bytes(int64_t R, int64_t M, int64_t Hq, int64_t
  *  out          device [M][Hq][D] bf16 or fp32, 16-B, rows out_stride
  *               elements apart (a multiple of 8, at least Hq * D).  Rows of
  *               no request are left as they are.
- * Sums and the softmax's statistics are fp32.  Probabilities p, relative to the
+ * Sums and the softmax's statistics are fp32; a row with a score past its range
+ * may be NaN.  Probabilities p, relative to the
  * largest of a part of the request, enter the second product in f16 as
  * p * vs / vref, vref being the power of two above the largest value scale met
  * so far in that part: rounded to 2^-11 of themselves down to 2^-21, with an

@@ -10,14 +10,17 @@
 //
 // One workgroup per (run of slots that lie in one page, head, K or V): the
 // largest magnitude first, then, with the values read again from the caches,
-// the codes (held in registers, before the packed conversions: 25.2 us against
-// 26.8 for 11460 tokens of prompts, but 7.4 against 6.0 for 64 single tokens).
-// Latency bounds a few tokens (slot, run, values, scale in turn: 5.3 us for 64
-// single ones, 8 heads of 128), the two passes many (11460: 21 us, 3.4 TB/s).  Keys: a thread codes 16 dimensions of a token, one 16-byte piece
-// of the block, with the tokens along the lanes, so that a wave writes whole
-// kilobytes.  Values, which the block holds by token within a dimension: a
-// thread codes 2 x 2 dimensions of 8 tokens, two whole 16-byte pieces; where
-// some of the 8 tokens are not the run's, byte by byte.
+// the codes.  Latency bounds a few tokens: slot, run, values, scale in turn,
+// 5.2 us for 64 single ones (8 heads of 128, pages of 64) where no scale grows;
+// then a page's codes, read and written back one 16-byte piece a lane after the
+// other: 8.3 us where 6% of the blocks grow, as they do for tokens that are
+// alike, 9.5 where all do (heads of 256, pages of 256: 8, 21 and 33 us).  The
+// two passes bound many tokens (11460 of 7 prompts: 21 us, 3.4 TB/s).  Keys: a
+// thread codes 16 dimensions of a token, one 16-byte piece of the block, with
+// the tokens along the lanes, so that a wave writes whole kilobytes.  Values,
+// which the block holds by token within a dimension: a thread codes 2 x 2
+// dimensions of 8 tokens, two whole 16-byte pieces; where some of the 8 tokens
+// are not the run's, byte by byte.
 #include <type_traits>
 
 #include "kv_cache.h"
@@ -240,9 +243,19 @@ void run(const KvAppendArgs &a, bool e4m3, hipStream_t s) {
 
 hipError_t launch_kv_append(const KvAppendArgs &args, bool e4m3, hipStream_t s) {
     KvAppendArgs a = args;
-    // Few tokens (a decode step, a draft): a wave for each token that may
-    // start a run.  Many (prompts, whose runs are pages): a workgroup of four
-    // waves for each 32 tokens, the shortest page.
+    // Few tokens: a wave for each token that may start a run.  Many (prompts,
+    // whose runs are pages): a workgroup of four waves for each 32 tokens, the
+    // shortest page, which takes the runs that start there in turn.  What the
+    // runs are stands in `slots`, on the GPU, so M decides alone.  Measured
+    // (int8, 8 heads of 128, pages of 64; waves against workgroups): single
+    // tokens, 64 of them 5.2 us against 58, 1024 18 against 64, 1025 19 against
+    // 68, 4096 58 against 133; drafts of 16 tokens, 16 of them 14.3 against
+    // 12.6, 64 47 against 14, 65 48 against 14; one prompt of 300 tokens 10.4
+    // against 6.0, of 1000 16 against 6.6, of 11460 84 against 20 (pages of 128).
+    // So the rule fits single tokens up to 1024 and prompts above; drafts and
+    // prompts of up to 1024 tokens take up to 5 times what the other variant
+    // would (a prompt of 1024 on pages and heads of 256: 112 against 23), more
+    // single tokens than 1024 up to 3.6 times.
     if (a.M <= 1024) {
         a.chunk = 1;
         run<64>(a, e4m3, s);

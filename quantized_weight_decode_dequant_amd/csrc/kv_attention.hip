@@ -26,13 +26,14 @@
 // (batch-one decode), a cut falls on each one's start too, so that no
 // workgroup has two segments.  A workgroup's waves split the segment's steps
 // (TS of them) and the rows (RS) and join in LDS; a second kernel joins the
-// segments.  Short contexts are not cut.
+// segments.  Short contexts are not cut (WHOLE_MAX_8, WHOLE_MAX_4).
 //
 // Bound by the cache's stream for up to 16 rows (131072 tokens, 4 heads of
-// 256, E4M3: 46.6 us, 5.8 TB/s; 330693 tokens in 48 requests, 8 heads of 128,
-// int8: 126 us, 5.4 TB/s; the joins 6.5 us each), by the vector unit's
-// conversions and softmax for many (128 rows, 46784 tokens: 54.7 us, 340
-// TFLOP/s, join 10.2), by latency for short contexts (1021 tokens: 11 us).
+// 256, E4M3: 46.5 us, 5.8 TB/s; 330693 tokens in 48 requests, 8 heads of 128,
+// int8: 126 us, 5.4 TB/s; the joins 6.4 us each), by the vector unit's
+// conversions, which each of the RS waves does for itself, and softmax for many
+// (128 rows, 46784 tokens: 54.5 us, 340 TFLOP/s, join 10.2), by latency for
+// short contexts (1021 tokens: 11.7 us) and windows (512 of 131072 tokens: 10.5).
 #include <type_traits>
 
 #include "kv_cache.h"
@@ -774,10 +775,18 @@ constexpr Shape shape_of(int D, int64_t rows) {
 }
 
 constexpr int WAVES = 4;
-// Contexts up to here are not cut: a second launch would cost more than the
-// steps that the waves of a workgroup then take in turn.  With 16 rows or
-// fewer to a KV head 8 waves take them (1021 tokens, one request: 12.4 us
-// uncut, 13.7 with 4 waves, 13.0 cut; 2048: 16.7 and 13.2 cut).
+// Contexts (max_len, or what a window leaves of it) up to here are not cut: a
+// second launch would cost more than the steps that the waves of a workgroup
+// then take in turn.  With 16 rows or fewer to a KV head, D <= 128, 8 waves
+// take them.  Measured, 8 heads of 128, uncut against cut, one request and
+// eight of them: 1024 tokens, 4 rows 11.8 us against 13.3 and 12.3 against
+// 16.8, 1536 13.3 against 13.4 and 14.2 against 17.4.  Otherwise 4 waves: 512
+// tokens, 32 rows 13.4 against 16.2 and 13.5 against 19.2, 64 rows 19.0
+// against 17.2 and 18.9 against 22.7, 128 rows 27.6 against 19.8 and 28.4
+// against 32.3; 768 tokens, 32 rows 15.1 against 16.5 and 15.2 against 22.1,
+// 64 rows 23.4 against 18.2 and 23.7 against 27.0, 128 rows 37 against 23 and
+// 38 against 33; D = 256 (4 heads), 512 tokens, 8 rows 12.4 against 15.5 and
+// 12.6 against 16.6, 64 rows 29.9 against 18.0 and 30.6 against 24.3.
 constexpr int WHOLE_WAVES = 8, WHOLE_MAX_8 = 1024, WHOLE_MAX_4 = 512;
 
 template <bool E4M3, int D, int NR, int RS>
