@@ -520,7 +520,7 @@ typedef enum { QG_KV_INT8 = 0, QG_KV_E4M3 = 1 } qg_kv_format;
 
 typedef struct qg_kv_cache {
     void *k, *v;                  /* device codes [pages][Hkv][page * D], 16-B */
-    float *k_scales, *v_scales;   /* device fp32 [pages][Hkv]: 0, or from 2^-107
+    float *k_scales, *v_scales;   /* device fp32 [pages][Hkv]: 0, or from 2^-109
                                      on (what kv_append_run writes) and finite */
     int64_t pages;                /* >= 1, pages * page < 2^31 */
     int32_t page;                 /* 32, 64, 128 or 256 */

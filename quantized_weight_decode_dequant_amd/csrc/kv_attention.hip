@@ -54,7 +54,7 @@ constexpr float P_EXP = 7.f, P_UNIT = 0x1p7f;
 
 // A wave's o and l leave it in this unit (with P_UNIT's inverse in it): sums
 // of p <= 2^8 over up to 2^16 tokens of values near fp32's end stay inside it,
-// and the smallest scale that an append writes, 2^-107, keeps 18 bits.
+// and the smallest scale that an append writes, 2^-109, keeps 16 bits.
 constexpr float OUT_UNIT = 0x1p-31f;
 
 // An int8 code c enters the MFMA as the f16 whose bits are c + 128: a
