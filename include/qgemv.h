@@ -498,6 +498,50 @@ int rmsnorm_quant_run(const void *x, int x_dtype, const void *residual, void *re
                       int64_t M, int64_t K, void *y, int8_t *Xq, float *x_scales, void *stream);
 
 /*
+ * qk_norm_rope_run -- what stands between the projection of queries and keys
+ * and the cache: the root-mean-square norm of each head and the rotation by
+ * the token's position, in one pass,
+ *     y = x * w / sqrt(mean(x^2) + eps)  over the head's D dimensions,
+ *     (a, b) <- (a cos t - b sin t, b cos t + a sin t)  for its first
+ *         `rotated` dimensions in pairs, t = position * inv_freq[pair];
+ * the dimensions behind them are normed only.
+ *
+ *  q, k         device [M][Hq][D] and [M][Hkv][D], bf16 (x_dtype =
+ *               QG_OUT_BF16) or fp32 (QG_OUT_F32), 16-B; token m at q +
+ *               m * q_stride elements (a multiple of 8, at least Hq * D), so a
+ *               joint projection's output can be given as it is.
+ *  M            tokens, 0..2^26 - 8.
+ *  Hq, Hkv      heads, 0..8192 and 0..1024; a side of 0 heads is not there.
+ *  D            a multiple of 8, 8..512.
+ *  q_weight, k_weight   device bf16 [D], 16-B, or NULL: that side's heads are
+ *               rotated without a norm.
+ *  eps          > 0, finite (where there is a weight).
+ *  positions    device int32 [axes][M] (one axis: kv_tables_run's positions).
+ *  axes         1..4; more than one: positions in time, height and width.
+ *  axis         device uint8 [rotated / 2], the axis whose position turns
+ *               each pair (one outside [0, axes): the pair is not turned), or
+ *               NULL: axis 0 for all.
+ *  inv_freq     device fp32 [rotated / 2].
+ *  rotated      a multiple of 16, 0..D; with 0, positions and inv_freq may be
+ *               NULL (norm only).
+ *  interleaved  0: pair i is dimensions i and i + rotated / 2; 1: 2 i and 2 i + 1.
+ *  q_out, k_out device bf16 [M][Hq][D] and [M][Hkv][D], 16-B, with strides as
+ *               above.  May be bf16 q and k themselves (same stride);
+ *               otherwise outputs overlap neither the inputs nor each other.
+ * Norm and rotation are fp32, the angle is an fp64 product reduced there to
+ * half a turn (a position of 2^30 costs 10^-6 of a turn at most); one rounding, to bf16, at
+ * the end.  A head whose sum of squares is not finite gives zeros or NaN.
+ * Errors: QG_EINVAL, QG_ESHAPE, QG_EALIGN, QG_EUNSUPPORTED (QG_OUT_I32_GROUPS
+ * as a type), QG_EHIP.
+ */
+int qk_norm_rope_run(const void *q, int64_t q_stride, const void *k, int64_t k_stride, int x_dtype,
+                     int64_t M, int64_t Hq, int64_t Hkv, int64_t D, const void *q_weight,
+                     const void *k_weight, float eps, const int32_t *positions, int axes,
+                     const uint8_t *axis, const float *inv_freq, int64_t rotated, int interleaved,
+                     void *q_out, int64_t q_out_stride, void *k_out, int64_t k_out_stride,
+                     void *stream);
+
+/*
  * A cache of keys and values in 8 bits, in pages.
  *
  * A decode pass reads the weights and the cache ("Real engines fall below the

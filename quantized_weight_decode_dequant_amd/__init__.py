@@ -12,7 +12,7 @@ from ._lib import (  # noqa: F401
     MOE_NOALLOC_SCRATCH_BYTES, QG_ESIZE,
     qgemm_skinny_run, qgemv_pack, qgemv_run, raw, status_string, qg_batch_plan_build,
     qg_batch_run, qg_batch_worklist_bytes, qg_plain_read, GemvDesc, BatchPlan, Plan,
-    KV_INT8, KV_E4M3, KVCache, CacheDesc, rmsnorm_quant_run, kv_tables_run, kv_append_run,
+    KV_INT8, KV_E4M3, KVCache, CacheDesc, rmsnorm_quant_run, qk_norm_rope_run, kv_tables_run, kv_append_run,
     kv_attention_run, kv_attention_workspace_bytes,
 )
 

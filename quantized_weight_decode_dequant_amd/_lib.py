@@ -65,6 +65,7 @@ EXPORTS = (
     "qg_batch_run",
     "qg_plain_read",
     "rmsnorm_quant_run",
+    "qk_norm_rope_run",
     "kv_tables_run",
     "kv_append_run",
     "qg_kv_attention_workspace_bytes",
@@ -152,6 +153,9 @@ def raw():
             lib.qg_plain_read.restype = i
             lib.rmsnorm_quant_run.argtypes = [p, i, p, p, i, p, C.c_float, p, i64, i64, p, p, p, p]
             lib.rmsnorm_quant_run.restype = i
+            lib.qk_norm_rope_run.argtypes = [p, i64, p, i64, i, i64, i64, i64, i64, p, p, C.c_float, p, i, p, p,
+                                             i64, i, p, i64, p, i64, p]
+            lib.qk_norm_rope_run.restype = i
             lib.kv_tables_run.argtypes = [i64, i64, i64, i64, i64, p, p, p, p, p, p, p, p, p, p, p]
             lib.kv_tables_run.restype = i
             lib.kv_append_run.argtypes = [p, i64, p, i64, p, i64, p, p]
@@ -490,6 +494,50 @@ def rmsnorm_quant_run(x, weight, eps: float, residual=None, residual_out=None, s
           M, K, _arg(y, torch.bfloat16, mk, dev, "y"), _arg(Xq, i8, mk, dev, "Xq"),
           _arg(x_scales, torch.float32, (M,), dev, "x_scales"))
     return residual_out, y, Xq, x_scales
+
+
+def qk_norm_rope_run(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps: float = 1e-6, axis=None,
+                     interleaved: bool = False, q_out=None, k_out=None, stream=None):
+    """Norm of each head and rotation by position; q [M, Hq, D] and k [M, Hkv,
+    D] (or None) bf16 or fp32, rows at any multiple of 8 elements; positions
+    int32 [M] or [axes, M]; inv_freq fp32 [rotated / 2]; axis uint8 [rotated /
+    2] with several axes; q_weight, k_weight bf16 [D] (None: no norm).  Returns
+    (q_out, k_out), bf16; q_out may be q and k_out k."""
+    torch = _torch()
+    bf16 = torch.bfloat16
+    if q.dim() != 3:
+        raise ValueError("q must be [M, Hq, D]")
+    M, Hq, D = q.shape
+    xt, dev = _float_type(q, "q"), _device(q)
+    if k is not None and (k.dim() != 3 or k.shape[0] != M or k.shape[2] != D):
+        raise ValueError("k must be [%d, Hkv, %d] (got %s)" % (M, D, tuple(k.shape)))
+    if k is None and k_out is not None:
+        raise ValueError("k_out without k")
+    Hkv = k.shape[1] if k is not None else 0
+    if q_out is None:
+        q_out = _empty((M, Hq, D), bf16, q.device, stream)
+    if k_out is None and k is not None:
+        k_out = _empty((M, Hkv, D), bf16, q.device, stream)
+    if q_out.shape != q.shape or (k is not None and k_out.shape != k.shape):
+        raise ValueError("q_out and k_out must have the shapes of q and k")
+    if positions.dim() not in (1, 2) or inv_freq.dim() != 1:
+        raise ValueError("positions must be [M] or [axes, M], inv_freq [rotated / 2]")
+    axes, half = (1 if positions.dim() == 1 else positions.shape[0]), inv_freq.shape[0]
+    if M == 0:
+        return q_out, k_out
+    qp, qs = _rows(q, Hq, D, q.dtype, dev, "q")
+    qo, qos = _rows(q_out, Hq, D, bf16, dev, "q_out")
+    kp = ko = None
+    ks = kos = 0
+    if k is not None:
+        kp, ks = _rows(k, Hkv, D, q.dtype, dev, "k")
+        ko, kos = _rows(k_out, Hkv, D, bf16, dev, "k_out")
+    _call(dev, stream, "qk_norm_rope_run", raw().qk_norm_rope_run, qp, qs, kp, ks, xt, M, Hq, Hkv, D,
+          _arg(q_weight, bf16, (D,), dev, "q_weight"), _arg(k_weight, bf16, (D,), dev, "k_weight"), eps,
+          _arg(positions, torch.int32, (M,) if positions.dim() == 1 else (axes, M), dev, "positions"), axes,
+          _arg(axis, torch.uint8, (half,), dev, "axis"), _arg(inv_freq, torch.float32, (half,), dev, "inv_freq"),
+          2 * half, 1 if interleaved else 0, qo, qos, ko, kos)
+    return q_out, k_out
 
 
 class KVCache:

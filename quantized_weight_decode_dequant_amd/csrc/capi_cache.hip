@@ -1,12 +1,13 @@
 // C ABI of the operators between the products (declared in include/qgemv.h):
-// the norm, and the paged 8-bit cache with its tables, its append and its
-// attention.  As in capi.hip, arguments are checked on the host before any
+// the norms, the rotation, and the paged 8-bit cache with its tables, its
+// append and its attention.  As in capi.hip, arguments are checked on the host before any
 // HIP call.
 #include <cmath>
 #include <cstdint>
 
 #include "../../include/qgemv.h"
 #include "kv_cache.h"
+#include "qk_rope.h"
 #include "rmsnorm.h"
 
 namespace {
@@ -20,6 +21,8 @@ constexpr int64_t ROWS_MAX = int64_t(1) << 30;
 constexpr int64_t NORM_ROWS_MAX = (int64_t(1) << 22) - 1;
 constexpr int64_t APPEND_TOKENS_MAX = int64_t(1) << 28;
 constexpr int64_t JOINS_MAX = (int64_t(1) << 26) - 8;
+// (the rotation takes 64 a token, more only of up to 2048 tokens)
+constexpr int64_t ROPE_TOKENS_MAX = (int64_t(1) << 26) - 8;
 constexpr int64_t LEN_MAX = int64_t(1) << 30;
 constexpr int64_t STRIDE_MAX = int64_t(1) << 31;
 
@@ -96,6 +99,56 @@ int rmsnorm_quant_run(const void *x, int x_dtype, const void *residual, void *re
         return hip_status(launch_rmsnorm(a, x_dtype == QG_OUT_F32,
                                          !residual ? 0 : res_dtype == QG_OUT_F32 ? 2 : 1,
                                          reinterpret_cast<hipStream_t>(stream)));
+    } catch (...) {
+        return QG_EINTERNAL;
+    }
+}
+
+int qk_norm_rope_run(const void *q, int64_t q_stride, const void *k, int64_t k_stride, int x_dtype,
+                     int64_t M, int64_t Hq, int64_t Hkv, int64_t D, const void *q_weight,
+                     const void *k_weight, float eps, const int32_t *positions, int axes,
+                     const uint8_t *axis, const float *inv_freq, int64_t rotated, int interleaved,
+                     void *q_out, int64_t q_out_stride, void *k_out, int64_t k_out_stride,
+                     void *stream) {
+    try {
+        if (x_dtype == QG_OUT_I32_GROUPS) return QG_EUNSUPPORTED;
+        if ((x_dtype != QG_OUT_BF16 && x_dtype != QG_OUT_F32) || (interleaved != 0 && interleaved != 1))
+            return QG_EINVAL;
+        if (M < 0 || M > ROPE_TOKENS_MAX || Hq < 0 || Hq > 8192 || Hkv < 0 || Hkv > 1024 || D < 8 ||
+            D > ROPE_D_MAX || D % 8 || rotated < 0 || rotated > D || rotated % 16 || axes < 1 || axes > 4 ||
+            (Hq > 0 && (!row_stride(q_stride, Hq * D) || !row_stride(q_out_stride, Hq * D))) ||
+            (Hkv > 0 && (!row_stride(k_stride, Hkv * D) || !row_stride(k_out_stride, Hkv * D))))
+            return QG_ESHAPE;
+        if ((Hq > 0 && (!q || !q_out)) || (Hkv > 0 && (!k || !k_out)) || (rotated > 0 && (!positions || !inv_freq)))
+            return QG_EINVAL;
+        if ((q_weight || k_weight) && (!(eps > 0.f) || !std::isfinite(eps))) return QG_EINVAL;
+        if (!aligned(q, 16) || !aligned(k, 16) || !aligned(q_weight, 16) || !aligned(k_weight, 16) ||
+            !aligned(positions, 4) || !aligned(inv_freq, 4) || !aligned(q_out, 16) || !aligned(k_out, 16))
+            return QG_EALIGN;
+        if (M == 0 || Hq + Hkv == 0) return QG_OK;
+        QkRopeArgs a;
+        a.q = q;
+        a.k = k;
+        a.q_weight = reinterpret_cast<const uint16_t *>(q_weight);
+        a.k_weight = reinterpret_cast<const uint16_t *>(k_weight);
+        a.positions = positions;
+        a.axis = axis;
+        a.inv_freq = inv_freq;
+        a.q_out = reinterpret_cast<uint16_t *>(q_out);
+        a.k_out = reinterpret_cast<uint16_t *>(k_out);
+        a.q_stride = q_stride;
+        a.k_stride = k_stride;
+        a.qo_stride = q_out_stride;
+        a.ko_stride = k_out_stride;
+        a.M = (int)M;
+        a.Hq = (int)Hq;
+        a.H = (int)(Hq + Hkv);
+        a.D = (int)D;
+        a.half = (int)(rotated / 2);
+        a.axes = axes;
+        a.parts = a.per_wave = 0;
+        a.eps = eps;
+        return hip_status(launch_qk_rope(a, x_dtype == QG_OUT_F32, interleaved != 0, reinterpret_cast<hipStream_t>(stream)));
     } catch (...) {
         return QG_EINTERNAL;
     }
