@@ -710,6 +710,51 @@ int kv_attention_run(const qg_kv_cache *cache, int64_t R, int64_t M, int64_t Hq,
                      void *workspace, size_t workspace_bytes, void *out, int64_t out_stride,
                      int out_dtype, void *stream);
 
+/* Bytes of workspace sample_run needs (0 for arguments it would refuse). */
+size_t qg_sample_workspace_bytes(int64_t M, int64_t V);
+
+/*
+ * sample_run -- each row's next token from the output head's logits, by
+ * inversion of a given uniform number.  With w_i = exp((x_i - max x) / T), of
+ * a row's V tokens are kept
+ *     top-k  the first k by logit, the largest first (equal ones: the lower
+ *            token first),
+ *     top-p  of those, the ones before which, in that order, lies less than p
+ *            of top-k's sum of w,
+ *     min-p  of those, the ones with w_i >= min_p;
+ * the largest (the first of several) always is.  The token is the first, in
+ * the order of tokens, at which the sum of the kept w exceeds u times all of
+ * it.  One row: a decode step; T rows: the tokens to hold a draft against.
+ *
+ *  logits       device [M][V] bf16 (x_dtype = QG_OUT_BF16) or fp32
+ *               (QG_OUT_F32); rows `stride` elements apart (at least V), of any
+ *               alignment.  Read only.  NaN is never taken; a row of nothing
+ *               but -infinity and NaN gives token -1 and logprob NaN; +infinity
+ *               leaves only the infinite ones.
+ *  M            rows; M times the chunks of 4096 tokens of a row below 2^24.
+ *  V            1..2^20.
+ *  u            device fp32 [M], in [0, 1) (values outside are taken as the
+ *               nearest inside).
+ *  temperature  device fp32 [M], or NULL (1); 0, below or NaN: the largest logit.
+ *  top_k        device int32 [M], or NULL; 0, below or >= V: off.
+ *  top_p        device fp32 [M], or NULL; >= 1 or NaN: off; <= 0: one token.
+ *  min_p        device fp32 [M], or NULL; <= 0 or NaN: off; above 1: as 1.
+ *  workspace    device buffer, 16-B, of qg_sample_workspace_bytes; scratch:
+ *               calls that may overlap, or graphs that may run at once, need
+ *               one each.
+ *  tokens       device int32 [M], written.
+ *  logprobs     device fp32 [M], written: ln of the token's share of the kept
+ *               sum.  NULL: not written.
+ * Weights are fp64, rounded to multiples of 2^-42 (tokens below half of that
+ * are never drawn); their sums are exact, so results do not depend on any
+ * order and are the same in every run.
+ * Errors: QG_EINVAL, QG_ESHAPE, QG_EALIGN, QG_ESIZE, QG_EUNSUPPORTED
+ * (QG_OUT_I32_GROUPS as a type), QG_EHIP.
+ */
+int sample_run(const void *logits, int x_dtype, int64_t M, int64_t V, int64_t stride, const float *u,
+               const float *temperature, const int32_t *top_k, const float *top_p, const float *min_p,
+               void *workspace, size_t workspace_bytes, int32_t *tokens, float *logprobs, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

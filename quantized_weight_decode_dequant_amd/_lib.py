@@ -70,6 +70,8 @@ EXPORTS = (
     "kv_append_run",
     "qg_kv_attention_workspace_bytes",
     "kv_attention_run",
+    "qg_sample_workspace_bytes",
+    "sample_run",
 )
 
 
@@ -165,6 +167,10 @@ def raw():
             lib.kv_attention_run.argtypes = [p, i64, i64, i64, p, i64, p, p, p, i64, p, i64,
                                              C.c_float, i64, i64, p, sz, p, i64, i, p]
             lib.kv_attention_run.restype = i
+            lib.qg_sample_workspace_bytes.argtypes = [i64, i64]
+            lib.qg_sample_workspace_bytes.restype = sz
+            lib.sample_run.argtypes = [p, i, i64, i64, i64, p, p, p, p, p, p, sz, p, p, p]
+            lib.sample_run.restype = i
             _lib = lib
     return _lib
 
@@ -668,3 +674,40 @@ def kv_attention_run(cache: KVCache, q, q_start, lens, table, max_q: int, max_le
           _arg(workspace, workspace.dtype, workspace.shape, dev, "workspace") if nbytes else None, nbytes,
           op, os_, out_dtype)
     return out
+
+
+# ------------------------------------------------------------------ the next token
+def sample_workspace_bytes(M: int, V: int) -> int:
+    return raw().qg_sample_workspace_bytes(M, V)
+
+
+def sample_run(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, workspace=None, tokens=None,
+               logprobs=None, stream=None):
+    """Each row's next token; logits [M, V] bf16 or fp32 (rows at any stride),
+    u fp32 [M] in [0, 1); temperature, top_p, min_p fp32 [M] and top_k int32
+    [M], or None.  Returns (tokens int32 [M], logprobs); logprobs (fp32 [M])
+    are written where a tensor is given."""
+    torch = _torch()
+    f32, i32 = torch.float32, torch.int32
+    if logits.dim() != 2:
+        raise ValueError("logits must be [M, V]")
+    M, V = logits.shape
+    xt, dev, r = _float_type(logits, "logits"), _device(logits), (M,)
+    row, dim = logits.stride()
+    if V > 1 and dim != 1:
+        raise ValueError("logits: a row's tokens must be dense")
+    if tokens is None:
+        tokens = _empty(M, i32, logits.device, stream)
+    if M == 0:
+        return tokens, logprobs
+    lib = raw()
+    if workspace is None:
+        nbytes = lib.qg_sample_workspace_bytes(M, V)
+        workspace = _empty(max(nbytes, 16), torch.uint8, logits.device, stream)
+    nbytes = workspace.numel() * workspace.element_size()
+    _call(dev, stream, "sample_run", lib.sample_run, logits.data_ptr(), xt, M, V, row if M > 1 else V,
+          _arg(u, f32, r, dev, "u"), _arg(temperature, f32, r, dev, "temperature"), _arg(top_k, i32, r, dev, "top_k"),
+          _arg(top_p, f32, r, dev, "top_p"), _arg(min_p, f32, r, dev, "min_p"),
+          _arg(workspace, workspace.dtype, workspace.shape, dev, "workspace"), nbytes,
+          _arg(tokens, i32, r, dev, "tokens"), _arg(logprobs, f32, r, dev, "logprobs"))
+    return tokens, logprobs

@@ -1,6 +1,6 @@
 // C ABI of the operators between the products (declared in include/qgemv.h):
-// the norms, the rotation, and the paged 8-bit cache with its tables, its
-// append and its attention.  As in capi.hip, arguments are checked on the host before any
+// the norms, the rotation, the paged 8-bit cache with its tables, its append
+// and its attention, and the sampling behind the last product.  As in capi.hip, arguments are checked on the host before any
 // HIP call.
 #include <cmath>
 #include <cstdint>
@@ -9,6 +9,7 @@
 #include "kv_cache.h"
 #include "qk_rope.h"
 #include "rmsnorm.h"
+#include "sample.h"
 
 namespace {
 
@@ -23,6 +24,8 @@ constexpr int64_t APPEND_TOKENS_MAX = int64_t(1) << 28;
 constexpr int64_t JOINS_MAX = (int64_t(1) << 26) - 8;
 // (the rotation takes 64 a token, more only of up to 2048 tokens)
 constexpr int64_t ROPE_TOKENS_MAX = (int64_t(1) << 26) - 8;
+// (the sampling takes a workgroup of 256 for each chunk of a row)
+constexpr int64_t SAMPLE_GROUPS_MAX = (int64_t(1) << 24) - 1;
 constexpr int64_t LEN_MAX = int64_t(1) << 30;
 constexpr int64_t STRIDE_MAX = int64_t(1) << 31;
 
@@ -47,6 +50,35 @@ int check_cache(const qg_kv_cache *c) {
 }
 
 bool row_stride(int64_t stride, int64_t width) { return stride >= width && stride % 8 == 0 && stride < STRIDE_MAX; }
+
+// Where a sampling call's workspace holds what, from its start on; the last
+// is its size.  False: refused.
+struct SampleLayout {
+    int64_t chunks;
+    size_t rows, masses, counts, kept, listed, tops, top_at, lists, bytes;
+};
+bool sample_layout(int64_t M, int64_t V, SampleLayout *l) {
+    if (M < 0 || V < 1 || V > SAMPLE_V_MAX) return false;
+    l->chunks = (V + SAMPLE_CHUNK - 1) / SAMPLE_CHUNK;
+    if (M > SAMPLE_GROUPS_MAX / l->chunks) return false;
+    size_t at = 0;
+    const auto take = [&](size_t each) {
+        const size_t here = at;
+        at += (each * (size_t)M + 255) / 256 * 256;
+        return here;
+    };
+    const size_t C = (size_t)l->chunks;
+    l->rows = take(sizeof(SampleRow));
+    l->masses = take(8 * SAMPLE_BINS);
+    l->counts = take(4 * SAMPLE_BINS);
+    l->kept = take(8 * C);
+    l->listed = take(4 * C);
+    l->tops = take(4 * C);
+    l->top_at = take(4 * C);
+    l->lists = take(4 * SAMPLE_LIST * C);
+    l->bytes = at;
+    return true;
+}
 
 // shape rules and plan of an attention call (false: refused)
 bool attention_plan(int64_t R, int64_t M, int64_t Hq, int64_t Hkv, int64_t D, int64_t page,
@@ -297,6 +329,55 @@ int kv_attention_run(const qg_kv_cache *cache, int64_t R, int64_t M, int64_t Hq,
         a.out_f32 = out_dtype == QG_OUT_F32;
         return hip_status(launch_kv_attention(a, cache->D, cache->fmt == QG_KV_E4M3,
                                               reinterpret_cast<hipStream_t>(stream)));
+    } catch (...) {
+        return QG_EINTERNAL;
+    }
+}
+
+size_t qg_sample_workspace_bytes(int64_t M, int64_t V) {
+    SampleLayout l;
+    return sample_layout(M, V, &l) ? l.bytes : 0;
+}
+
+int sample_run(const void *logits, int x_dtype, int64_t M, int64_t V, int64_t stride, const float *u,
+               const float *temperature, const int32_t *top_k, const float *top_p, const float *min_p,
+               void *workspace, size_t workspace_bytes, int32_t *tokens, float *logprobs, void *stream) {
+    try {
+        if (x_dtype == QG_OUT_I32_GROUPS) return QG_EUNSUPPORTED;
+        if (x_dtype != QG_OUT_BF16 && x_dtype != QG_OUT_F32) return QG_EINVAL;
+        SampleLayout l;
+        if (!sample_layout(M, V, &l) || stride < V || stride >= STRIDE_MAX) return QG_ESHAPE;
+        if (!logits || !u || !tokens || (M > 0 && !workspace)) return QG_EINVAL;
+        if (workspace_bytes < l.bytes) return QG_ESIZE;
+        if (!aligned(logits, x_dtype == QG_OUT_F32 ? 4 : 2) || !aligned(workspace, 16)) return QG_EALIGN;
+        for (const void *p : {(const void *)u, (const void *)temperature, (const void *)top_k,
+                              (const void *)top_p, (const void *)min_p, (const void *)tokens,
+                              (const void *)logprobs})
+            if (!aligned(p, 4)) return QG_EALIGN;
+        if (M == 0) return QG_OK;
+        uint8_t *w = reinterpret_cast<uint8_t *>(workspace);
+        SampleArgs a;
+        a.logits = logits;
+        a.stride = stride;
+        a.u = u;
+        a.temperature = temperature;
+        a.top_p = top_p;
+        a.min_p = min_p;
+        a.top_k = top_k;
+        a.tokens = tokens;
+        a.logprobs = logprobs;
+        a.rows = reinterpret_cast<SampleRow *>(w + l.rows);
+        a.masses = reinterpret_cast<unsigned long long *>(w + l.masses);
+        a.counts = reinterpret_cast<unsigned *>(w + l.counts);
+        a.kept = reinterpret_cast<unsigned long long *>(w + l.kept);
+        a.listed = reinterpret_cast<unsigned *>(w + l.listed);
+        a.tops = reinterpret_cast<float *>(w + l.tops);
+        a.top_at = reinterpret_cast<int32_t *>(w + l.top_at);
+        a.lists = reinterpret_cast<unsigned *>(w + l.lists);
+        a.M = (int)M;
+        a.V = (int)V;
+        a.chunks = (int)l.chunks;
+        return hip_status(launch_sample(a, x_dtype == QG_OUT_F32, reinterpret_cast<hipStream_t>(stream)));
     } catch (...) {
         return QG_EINTERNAL;
     }

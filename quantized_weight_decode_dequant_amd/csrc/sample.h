@@ -1,0 +1,52 @@
+// Arguments and workspace of the sampling kernels (sample.hip), filled by the
+// C ABI.
+#pragma once
+
+#include "qg_internal.h"
+
+namespace qg {
+
+constexpr int64_t SAMPLE_V_MAX = int64_t(1) << 20;
+constexpr int SAMPLE_THREADS = 256;
+constexpr int SAMPLE_PER_THREAD = 16;
+constexpr int SAMPLE_CHUNK = SAMPLE_THREADS * SAMPLE_PER_THREAD;  // tokens of one workgroup
+constexpr int SAMPLE_BINS = 2048;
+constexpr int SAMPLE_LIST = 256;  // a chunk's undecided tokens that are kept as a list
+static_assert(SAMPLE_V_MAX / SAMPLE_CHUNK <= SAMPLE_THREADS, "a row's chunks are one for each thread");
+
+// What the workgroups of a row leave for each other.
+struct SampleRow {
+    unsigned arrived[2];        // workgroups of a row that are done with a kernel
+    int done;                   // the token is written already
+    int full;                   // bins below are kept whole
+    int p_lo, p_hi;             // bins among which top-p's border lies (p_lo > p_hi: none)
+    int k_bin;                  // the bin of top-k's border (-1: none)
+    unsigned k_left;            // tokens of k_bin that top-k keeps
+    unsigned long long p_mass;  // mass of the bins below p_lo
+    unsigned long long k_mass;  // mass of the bins below k_bin
+    unsigned long long mass;    // of all bins
+    unsigned long long pad;
+};
+
+struct SampleArgs {
+    const void *logits;
+    int64_t stride;  // elements between rows
+    const float *u, *temperature, *top_p, *min_p;
+    const int32_t *top_k;
+    int32_t *tokens;
+    float *logprobs;
+    // workspace, by row
+    SampleRow *rows;             // [M]
+    unsigned long long *masses;  // [M][SAMPLE_BINS]
+    unsigned *counts;            // [M][SAMPLE_BINS]
+    unsigned long long *kept;    // [M][chunks]: mass of a chunk that is kept for sure
+    unsigned *listed;            // [M][chunks]: undecided tokens of a chunk
+    float *tops;                 // [M][chunks]: largest logit
+    int32_t *top_at;             // [M][chunks]: the first token that has it
+    unsigned *lists;             // [M][chunks][SAMPLE_LIST]: keys
+    int M, V, chunks;
+};
+
+hipError_t launch_sample(const SampleArgs &a, bool x_f32, hipStream_t s);
+
+}  // namespace qg

@@ -26,3 +26,40 @@ def rope(x, w, eps, positions, axis, inv_freq, interleaved):
         z[:, :, b] = y[:, :, b] * c + y[:, :, a] * s
         size[:, :, a] = size[:, :, b] = np.abs(y[:, :, a]) + np.abs(y[:, :, b])
     return z, size, far
+
+
+def sample(x, u, T=None, k=None, p=None, minp=None):
+    """(tokens, logprobs, kept) of logits [M, V]: by sorting."""
+    M, V = x.shape
+    tokens, logp, keeps = np.full(M, -1), np.full(M, np.nan), []
+    for m in range(M):
+        row = np.where(np.isnan(x[m]), -np.inf, x[m])
+        top = row.max()
+        keep = np.zeros(V, bool)
+        keeps.append(keep)
+        if top == -np.inf:
+            continue
+        t = 1.0 if T is None else float(T[m])
+        kk = 0 if k is None else int(k[m])
+        if not t > 0:
+            t, kk = 1.0, 1
+        with np.errstate(invalid="ignore", over="ignore"):
+            w = np.exp(np.where(row == top, 0.0, (row - top) / t if np.isfinite(t) else np.where(row == -np.inf, -np.inf, 0.0)))
+        order = np.argsort(-row, kind="stable")
+        n = V if kk <= 0 or kk > V else kk
+        ws = w[order[:n]]
+        before = np.concatenate([[0.0], np.cumsum(ws)[:-1]])
+        pp, mp = 1.0 if p is None else float(p[m]), 0.0 if minp is None else float(minp[m])
+        ok = np.ones(n, bool)
+        if pp < 1:
+            ok &= before < pp * ws.sum()
+        if mp > 0:
+            ok &= ws >= min(mp, 1.0)
+        ok[0] = True
+        keep[order[:n][ok]] = True
+        c = np.cumsum(np.where(keep, w, 0.0))
+        uu = min(max(float(u[m]), 0.0), 1.0) if not np.isnan(u[m]) else 0.0
+        i = int(np.searchsorted(c, uu * c[-1], side="right"))
+        i = min(i, int(np.searchsorted(c, c[-1])))
+        tokens[m], logp[m] = i, np.log(w[i] / c[-1])
+    return tokens, logp, keeps
