@@ -24,8 +24,9 @@ constexpr int64_t APPEND_TOKENS_MAX = int64_t(1) << 28;
 constexpr int64_t JOINS_MAX = (int64_t(1) << 26) - 8;
 // (the rotation takes 64 a token, more only of up to 2048 tokens)
 constexpr int64_t ROPE_TOKENS_MAX = (int64_t(1) << 26) - 8;
-// (the sampling takes a workgroup of 256 for each chunk of a row)
-constexpr int64_t SAMPLE_GROUPS_MAX = (int64_t(1) << 24) - 1;
+// (the sampling takes a workgroup of 256 for each chunk of a row, and one of
+// 1024 for each row)
+constexpr int64_t SAMPLE_GROUPS_MAX = (int64_t(1) << 22) - 1;
 constexpr int64_t LEN_MAX = int64_t(1) << 30;
 constexpr int64_t STRIDE_MAX = int64_t(1) << 31;
 
@@ -55,7 +56,7 @@ bool row_stride(int64_t stride, int64_t width) { return stride >= width && strid
 // is its size.  False: refused.
 struct SampleLayout {
     int64_t chunks;
-    size_t rows, masses, counts, kept, listed, tops, top_at, lists, bytes;
+    size_t rows, masses, counts, kept, tops, top_at, lists, bytes;
 };
 bool sample_layout(int64_t M, int64_t V, SampleLayout *l) {
     if (M < 0 || V < 1 || V > SAMPLE_V_MAX) return false;
@@ -72,10 +73,9 @@ bool sample_layout(int64_t M, int64_t V, SampleLayout *l) {
     l->masses = take(8 * SAMPLE_BINS);
     l->counts = take(4 * SAMPLE_BINS);
     l->kept = take(8 * C);
-    l->listed = take(4 * C);
     l->tops = take(4 * C);
     l->top_at = take(4 * C);
-    l->lists = take(4 * SAMPLE_LIST * C);
+    l->lists = take(8 * SAMPLE_LIST);
     l->bytes = at;
     return true;
 }
@@ -370,10 +370,9 @@ int sample_run(const void *logits, int x_dtype, int64_t M, int64_t V, int64_t st
         a.masses = reinterpret_cast<unsigned long long *>(w + l.masses);
         a.counts = reinterpret_cast<unsigned *>(w + l.counts);
         a.kept = reinterpret_cast<unsigned long long *>(w + l.kept);
-        a.listed = reinterpret_cast<unsigned *>(w + l.listed);
         a.tops = reinterpret_cast<float *>(w + l.tops);
         a.top_at = reinterpret_cast<int32_t *>(w + l.top_at);
-        a.lists = reinterpret_cast<unsigned *>(w + l.lists);
+        a.lists = reinterpret_cast<u32x2_t *>(w + l.lists);
         a.M = (int)M;
         a.V = (int)V;
         a.chunks = (int)l.chunks;

@@ -11,21 +11,23 @@ constexpr int SAMPLE_THREADS = 256;
 constexpr int SAMPLE_PER_THREAD = 16;
 constexpr int SAMPLE_CHUNK = SAMPLE_THREADS * SAMPLE_PER_THREAD;  // tokens of one workgroup
 constexpr int SAMPLE_BINS = 2048;
-constexpr int SAMPLE_LIST = 256;  // a chunk's undecided tokens that are kept as a list
+constexpr int SAMPLE_ROW_THREADS = 1024;  // of the kernels with a workgroup a row
+constexpr int SAMPLE_LIST = 8192;         // a row's undecided tokens that are kept as a list
 static_assert(SAMPLE_V_MAX / SAMPLE_CHUNK <= SAMPLE_THREADS, "a row's chunks are one for each thread");
 
-// What the workgroups of a row leave for each other.
+// What a row's kernels leave for each other.
 struct SampleRow {
-    unsigned arrived[2];        // workgroups of a row that are done with a kernel
     int done;                   // the token is written already
     int full;                   // bins below are kept whole
     int p_lo, p_hi;             // bins among which top-p's border lies (p_lo > p_hi: none)
     int k_bin;                  // the bin of top-k's border (-1: none)
     unsigned k_left;            // tokens of k_bin that top-k keeps
+    unsigned listed;            // undecided tokens (those in the border's bins)
+    unsigned pad;
     unsigned long long p_mass;  // mass of the bins below p_lo
     unsigned long long k_mass;  // mass of the bins below k_bin
     unsigned long long mass;    // of all bins
-    unsigned long long pad;
+    unsigned long long pad2;
 };
 
 struct SampleArgs {
@@ -40,10 +42,9 @@ struct SampleArgs {
     unsigned long long *masses;  // [M][SAMPLE_BINS]
     unsigned *counts;            // [M][SAMPLE_BINS]
     unsigned long long *kept;    // [M][chunks]: mass of a chunk that is kept for sure
-    unsigned *listed;            // [M][chunks]: undecided tokens of a chunk
     float *tops;                 // [M][chunks]: largest logit
     int32_t *top_at;             // [M][chunks]: the first token that has it
-    unsigned *lists;             // [M][chunks][SAMPLE_LIST]: keys
+    u32x2_t *lists;              // [M][SAMPLE_LIST]: (key, chunk) of undecided tokens
     int M, V, chunks;
 };
 

@@ -20,13 +20,17 @@
 // of the border's bins are listed, and among these a radix descent over their
 // logits finds the border.
 //
-// Three kernels, a workgroup for each chunk of 4096 tokens of a row:
-//   sample_top    the chunk's largest logit
-//   sample_bins   counts and masses by bins; the row's last workgroup finds the
-//                 borders' bins.  Rows without top-k and top-p end here.
-//   sample_pick   the chunk's kept mass and list; the row's last workgroup
-//                 finds the borders and the token
-// "Last" is told by a counter that the first kernel clears: nobody waits.
+// Five kernels (three where no row has top-k or top-p), of a workgroup for
+// each chunk of 4096 tokens, or of one for each row:
+//   sample_top    (chunk) its largest logit
+//   sample_bins   (chunk) counts and masses by bins, or the kept mass
+//   sample_find   (row)   the borders' bins; the token of a row without them
+//   sample_list   (chunk) its kept mass, and its part of the list
+//   sample_pick   (row)   the borders and the token
+// One launch each, rather than a row's last workgroup going on: the fences
+// which that takes cost 462 us where the kernel's work is 30 (192 rows).
+#include <type_traits>
+
 #include "sample.h"
 
 namespace qg {
@@ -35,25 +39,26 @@ namespace {
 
 typedef unsigned long long u64;
 
-constexpr int TH = SAMPLE_THREADS, E = SAMPLE_PER_THREAD, NB = SAMPLE_BINS;
+constexpr int TH = SAMPLE_THREADS, RTH = SAMPLE_ROW_THREADS, E = SAMPLE_PER_THREAD, NB = SAMPLE_BINS;
 constexpr float NEG_INF = -__builtin_inff();
 constexpr double UNIT = 0x1p42;  // of masses
 
 __device__ __forceinline__ float f32_of(unsigned w) { return __builtin_bit_cast(float, w); }
 __device__ __forceinline__ unsigned bits_of(float f) { return __builtin_bit_cast(unsigned, f); }
 
-// E logits from token `at` on; NaN past the row's end
-template <bool F32>
-__device__ __forceinline__ void load_logits(const void *logits, int64_t row, int at, int V, float (&x)[E]) {
-    constexpr int N = F32 ? 4 : 8;  // logits of 16 bytes
+// n logits from token `at` on; NaN past the row's end
+template <bool F32, int n>
+__device__ __forceinline__ void load_logits(const void *logits, int64_t row, int at, int V, float (&x)[n]) {
+    constexpr int N = F32 || n < 8 ? 4 : 8;  // of one load
     const char *p = (const char *)logits + (row + at) * (F32 ? 4 : 2);
 #pragma unroll
-    for (int i = 0; i < E; i += N) {
+    for (int i = 0; i < n; i += N) {
         if (at + i + N <= V) {
-            u32x4_t w;
-            __builtin_memcpy(&w, p + i * (F32 ? 4 : 2), 16);  // rows are aligned to an element only
+            constexpr int WORDS = F32 ? 4 : N / 2;
+            unsigned w[WORDS];
+            __builtin_memcpy(w, p + i * (F32 ? 4 : 2), WORDS * 4);  // rows are aligned to an element only
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+            for (int e = 0; e < WORDS; ++e) {
                 const unsigned u = w[e];
                 if (F32) {
                     x[i + e] = f32_of(u);
@@ -139,8 +144,8 @@ __device__ __forceinline__ int bin_of(float x, float top) {
     return min(max((int)(bits_of(d) >> 16) - ((127 - 4) << 7), 0), NB - 1);
 }
 
-// Sum over the workgroup's threads before this one, and over all.
-template <typename T>
+// Sum over the workgroup's threads before this one, and over all (W waves).
+template <int W, typename T>
 __device__ __forceinline__ T scan_before(T v, T *waves, T &total) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     T upto = v;
@@ -155,13 +160,15 @@ __device__ __forceinline__ T scan_before(T v, T *waves, T &total) {
     T before = 0;
     total = 0;
 #pragma unroll
-    for (int w = 0; w < TH / 64; ++w) {
-        if (w < wave) before += waves[w];
-        total += waves[w];
+    for (int w = 0; w < W; ++w) {
+        const T u = waves[w];
+        if (w < wave) before += u;
+        total += u;
     }
     return before + upto - v;
 }
 
+template <int W>
 __device__ __forceinline__ u64 sum_all(u64 v, u64 *waves) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
@@ -171,10 +178,11 @@ __device__ __forceinline__ u64 sum_all(u64 v, u64 *waves) {
     __syncthreads();
     u64 total = 0;
 #pragma unroll
-    for (int w = 0; w < TH / 64; ++w) total += waves[w];
+    for (int w = 0; w < W; ++w) total += waves[w];
     return total;
 }
 
+template <int W>
 __device__ __forceinline__ float max_all(float v, float *waves) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
@@ -184,36 +192,15 @@ __device__ __forceinline__ float max_all(float v, float *waves) {
     __syncthreads();
     v = waves[0];
 #pragma unroll
-    for (int w = 1; w < TH / 64; ++w) v = fmaxf(v, waves[w]);
+    for (int w = 1; w < W; ++w) v = fmaxf(v, waves[w]);
     return v;
 }
 
-// What a workgroup keeps in LDS.
-struct Shared {
-    double pow[32];
-    union {
-        u64 wave64[TH / 64];
-        unsigned wave32[TH / 64];
-        float wavef[TH / 64];
-    };
-    u64 found64[2];
-    unsigned found32[4];
-    unsigned last;
-    u64 mass[NB];     // by bin; later by digit
-    unsigned count[NB];
-    unsigned ties[TH];  // by chunk
-};
-
-// Whether this is the row's last workgroup in a kernel: what the others wrote
-// before is then to be seen.
-__device__ __forceinline__ bool arrive_last(unsigned *arrived, unsigned of, Shared &sh) {
-    __threadfence();
-    __syncthreads();
-    if (threadIdx.x == 0) sh.last = atomicAdd(arrived, 1u) == of - 1;
-    __syncthreads();
-    if (!sh.last) return false;
-    __threadfence();
-    return true;
+// A row's largest logit, from its chunks'.
+template <int W>
+__device__ __forceinline__ float top_of(const SampleArgs &a, int m, float &mine, float *waves) {
+    mine = (int)threadIdx.x < a.chunks ? a.tops[(size_t)m * a.chunks + threadIdx.x] : NEG_INF;
+    return max_all<W>(mine, waves);
 }
 
 // ------------------------------------------------------------------ the chunks' largest
@@ -230,15 +217,11 @@ __global__ void __launch_bounds__(TH) sample_top_kernel(SampleArgs a) {
             a.counts[(size_t)m * NB + i] = 0;
         }
     }
-    if (c == 0 && tid == 0) {
-        a.rows[m].arrived[0] = a.rows[m].arrived[1] = 0;
-        a.rows[m].done = 0;
-    }
     float top = NEG_INF;
 #pragma unroll
     for (int e = 0; e < E; ++e) top = fmaxf(top, x[e]);  // (past NaN)
     if (tid == 0) first = 0x7FFFFFFF;
-    top = max_all(top, waves);
+    top = max_all<TH / 64>(top, waves);
     int at = 0x7FFFFFFF;
 #pragma unroll
     for (int e = E - 1; e >= 0; --e)
@@ -251,7 +234,73 @@ __global__ void __launch_bounds__(TH) sample_top_kernel(SampleArgs a) {
     }
 }
 
-// ------------------------------------------------------------------ the token
+// ------------------------------------------------------------------ counts and masses by bins
+template <bool F32>
+__global__ void __launch_bounds__(TH) sample_bins_kernel(SampleArgs a) {
+    __shared__ double pow[32];
+    __shared__ u64 waves[TH / 64];
+    __shared__ u64 masses[NB];
+    __shared__ unsigned counts[NB];
+    const int c = blockIdx.x % a.chunks, m = blockIdx.x / a.chunks, tid = threadIdx.x;
+    const Ask q = ask_of(a, m);
+    if (q.greedy) return;
+    float x[E], mine;
+    load_logits<F32>(a.logits, (int64_t)m * a.stride, c * SAMPLE_CHUNK + tid * E, a.V, x);
+    make_powers(pow);
+    if (q.filters())
+        for (int i = tid; i < NB; i += TH) {
+            masses[i] = 0;
+            counts[i] = 0;
+        }
+    const float top = top_of<TH / 64>(a, m, mine, (float *)waves);
+    if (!q.filters()) {
+        u64 sum = 0;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const double v = weight(x[e], top, q.c, pow);
+            sum += v >= q.minp ? mass_of(v) : 0;
+        }
+        sum = sum_all<TH / 64>(sum, waves);
+        if (tid == 0) a.kept[(size_t)m * a.chunks + c] = sum;
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        if (x[e] == x[e]) {
+            const int b = bin_of(x[e], top);
+            if (q.k > 0) atomicAdd(&counts[b], 1u);
+            if (q.p < 1.0) atomicAdd(&masses[b], mass_of(weight(x[e], top, q.c, pow)));
+        }
+    }
+    __syncthreads();
+    for (int i = tid; i < NB; i += TH) {
+        if (counts[i]) atomicAdd(&a.counts[(size_t)m * NB + i], counts[i]);
+        if (masses[i]) atomicAdd(&a.masses[(size_t)m * NB + i], masses[i]);
+    }
+}
+
+// ------------------------------------------------------------------ by rows
+// What a row's workgroup keeps in LDS.
+constexpr int DIGITS = RTH;  // of a level of the descent
+struct Shared {
+    double pow[32];
+    union {
+        u64 wave64[RTH / 64];
+        unsigned wave32[RTH / 64];
+        float wavef[RTH / 64];
+    };
+    u64 found64[2];
+    unsigned found32[4];
+    union {
+        u64 mass[DIGITS];   // by digit
+        u64 more[TH];       // by chunk
+    };
+    union {
+        unsigned count[DIGITS];
+        unsigned ties[TH];
+    };
+};
+
 // A row's cut in terms of its undecided tokens: those of larger keys are kept,
 // and the first `ties` of this key.
 struct Cut {
@@ -264,13 +313,15 @@ __device__ __forceinline__ bool undecided(const SampleRow &r, int b) {
 }
 
 // The token, from the chunks' kept masses (`mine`: of chunk tid) and, where
-// there are filters, their numbers of the cut key's tokens (sh.ties).
+// there are filters (`row`), their numbers of the cut key's tokens
+// (`ties_before`: before chunk tid).
 template <bool F32>
-__device__ void pick(const SampleArgs &a, int m, const Ask &q, float top, u64 mine, const SampleRow *row, Cut cut,
-                     Shared &sh) {
+__device__ __forceinline__ void pick(const SampleArgs &a, int m, const Ask &q, float top, u64 mine, const SampleRow *row, Cut cut,
+                                     unsigned ties_before, Shared &sh) {
+    constexpr int W = RTH / 64, PE = SAMPLE_CHUNK / RTH;
     const int tid = threadIdx.x;
     u64 total;
-    const u64 before = scan_before(mine, sh.wave64, total);
+    const u64 before = scan_before<W>(mine, sh.wave64, total);
     if (total == 0) {  // (only -infinities and NaN)
         if (tid == 0) {
             a.tokens[m] = -1;
@@ -283,139 +334,101 @@ __device__ void pick(const SampleArgs &a, int m, const Ask &q, float top, u64 mi
     r = r < total ? r : total - 1;
     if (mine > 0 && r >= before && r - before < mine) {
         sh.found32[0] = (unsigned)tid;
+        sh.found32[1] = ties_before;
         sh.found64[0] = r - before;
     }
     __syncthreads();
-    const int c = (int)sh.found32[0];
+    const int at = (int)sh.found32[0] * SAMPLE_CHUNK + tid * PE;
     r = sh.found64[0];
-    unsigned ties_before = 0, n;
-    if (row) {
-        ties_before = scan_before(tid < c ? sh.ties[tid] : 0u, sh.wave32, n);
-        ties_before = n;
-    }
-    float x[E];
-    const int at = c * SAMPLE_CHUNK + tid * E;
+    float x[PE];
     load_logits<F32>(a.logits, (int64_t)m * a.stride, at, a.V, x);
-    // this thread's tokens of the cut key come after this many others
-    unsigned mine_ties = 0;
+    unsigned place = 0;  // of this thread's first token of the cut key among all
     if (row) {
+        unsigned n = 0, all;
 #pragma unroll
-        for (int e = 0; e < E; ++e) mine_ties += x[e] == x[e] && key_of(x[e]) == cut.key && undecided(*row, bin_of(x[e], top));
-        ties_before += scan_before(mine_ties, sh.wave32, n);
+        for (int e = 0; e < PE; ++e) n += x[e] == x[e] && key_of(x[e]) == cut.key && undecided(*row, bin_of(x[e], top));
+        place = sh.found32[1];
+        place += scan_before<W>(n, sh.wave32, all);
     }
-    u64 w[E], sum = 0;
+    u64 w[PE], sum = 0;
+    double v[PE];
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-        const double v = weight(x[e], top, q.c, sh.pow);
-        bool keep = v >= q.minp;
+    for (int e = 0; e < PE; ++e) {
+        v[e] = weight(x[e], top, q.c, sh.pow);
+        bool keep = v[e] >= q.minp;
         if (row && x[e] == x[e]) {
             const int b = bin_of(x[e], top);
             const unsigned key = key_of(x[e]);
             if (undecided(*row, b)) {
-                keep &= key > cut.key || (key == cut.key && ties_before < cut.ties);
-                ties_before += key == cut.key;
+                keep &= key > cut.key || (key == cut.key && place < cut.ties);
+                place += key == cut.key;
             } else {
                 keep &= b < row->full;
             }
         }
-        w[e] = keep && x[e] == x[e] ? mass_of(v) : 0;
+        w[e] = keep && x[e] == x[e] ? mass_of(v[e]) : 0;
         sum += w[e];
     }
-    u64 from = scan_before(sum, sh.wave64, sum);
+    u64 from = scan_before<W>(sum, sh.wave64, sum);
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
+    for (int e = 0; e < PE; ++e) {
         if (w[e] > 0 && r >= from && r - from < w[e]) {
             a.tokens[m] = at + e;
-            if (a.logprobs)
-                a.logprobs[m] = (float)log(weight(x[e], top, q.c, sh.pow) / ((double)total * (1.0 / UNIT)));
+            if (a.logprobs) a.logprobs[m] = (float)log(v[e] / ((double)total * (1.0 / UNIT)));
         }
         from += w[e];
     }
 }
 
-// ------------------------------------------------------------------ counts and masses by bins
 template <bool F32>
-__global__ void __launch_bounds__(TH) sample_bins_kernel(SampleArgs a) {
+__global__ void __launch_bounds__(RTH) sample_find_kernel(SampleArgs a) {
     __shared__ Shared sh;
-    const int c = blockIdx.x % a.chunks, m = blockIdx.x / a.chunks, tid = threadIdx.x;
+    constexpr int W = RTH / 64, PER = NB / RTH;
+    const int m = blockIdx.x, tid = threadIdx.x;
     SampleRow *row = a.rows + m;
     const Ask q = ask_of(a, m);
-    float x[E];
-    if (!q.greedy) load_logits<F32>(a.logits, (int64_t)m * a.stride, c * SAMPLE_CHUNK + tid * E, a.V, x);
+    const bool filters = !q.greedy && q.filters();
+    u64 mass[PER], sum = 0;  // of PER consecutive bins
+    unsigned count[PER], n = 0;
+    if (filters) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            mass[i] = a.masses[(size_t)m * NB + tid * PER + i];
+            count[i] = a.counts[(size_t)m * NB + tid * PER + i];
+            sum += mass[i];
+            n += count[i];
+        }
+    }
+    const u64 kept = !q.greedy && !filters && tid < a.chunks ? a.kept[(size_t)m * a.chunks + tid] : 0;
     make_powers(sh.pow);
-    const float mine = tid < a.chunks ? a.tops[(size_t)m * a.chunks + tid] : NEG_INF;
-    const float top = max_all(mine, sh.wavef);
-    if (q.greedy) {
-        if (c != 0) return;
-        if (tid == 0) sh.found32[0] = 0x7FFFFFFF;
+    float mine;
+    const float top = top_of<W>(a, m, mine, sh.wavef);
+    const bool none = top == NEG_INF;  // of finite or infinite logits
+    if (q.greedy || none || !filters) {
+        if (tid == 0) {
+            sh.found32[0] = 0x7FFFFFFF;
+            row->done = 1;
+        }
         __syncthreads();
+        if (!q.greedy) {
+            pick<F32>(a, m, q, top, none ? 0 : kept, nullptr, Cut{0, 0}, 0, sh);
+            return;
+        }
         if (tid < a.chunks && mine == top) atomicMin(&sh.found32[0], (unsigned)a.top_at[(size_t)m * a.chunks + tid]);
         __syncthreads();
         if (tid == 0) {
-            const bool none = top == NEG_INF;
             a.tokens[m] = none ? -1 : (int)sh.found32[0];
             if (a.logprobs) a.logprobs[m] = none ? __builtin_nanf("") : 0.f;
-            row->done = 1;
         }
         return;
-    }
-    const bool filters = q.filters() && top != NEG_INF;
-    if (!filters) {
-        u64 sum = 0;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const double v = weight(x[e], top, q.c, sh.pow);
-            sum += v >= q.minp && top != NEG_INF ? mass_of(v) : 0;  // (a row of -infinities has no token)
-        }
-        sum = sum_all(sum, sh.wave64);
-        if (tid == 0) a.kept[(size_t)m * a.chunks + c] = sum;
-    } else {
-        for (int i = tid; i < NB; i += TH) {
-            sh.mass[i] = 0;
-            sh.count[i] = 0;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            if (x[e] == x[e]) {
-                const int b = bin_of(x[e], top);
-                if (q.k > 0) atomicAdd(&sh.count[b], 1u);
-                if (q.p < 1.0) atomicAdd(&sh.mass[b], mass_of(weight(x[e], top, q.c, sh.pow)));
-            }
-        }
-        __syncthreads();
-        for (int i = tid; i < NB; i += TH) {
-            if (sh.count[i]) atomicAdd(&a.counts[(size_t)m * NB + i], sh.count[i]);
-            if (sh.mass[i]) atomicAdd(&a.masses[(size_t)m * NB + i], sh.mass[i]);
-        }
-    }
-    if (!arrive_last(&row->arrived[0], (unsigned)a.chunks, sh)) return;
-    if (!filters) {
-        const u64 kept = tid < a.chunks ? a.kept[(size_t)m * a.chunks + tid] : 0;
-        pick<F32>(a, m, q, top, kept, nullptr, Cut{0, 0}, sh);
-        if (tid == 0) row->done = 1;
-        return;
-    }
-    // the borders' bins: 8 consecutive bins a thread
-    constexpr int PER = NB / TH;
-    u64 mass[PER], sum = 0;
-    unsigned count[PER], n = 0;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        mass[i] = a.masses[(size_t)m * NB + tid * PER + i];
-        count[i] = a.counts[(size_t)m * NB + tid * PER + i];
-        sum += mass[i];
-        n += count[i];
     }
     u64 total;
     unsigned tokens;
-    const u64 mass_before = scan_before(sum, sh.wave64, total);
-    const unsigned count_before = scan_before(n, sh.wave32, tokens);
+    const u64 mass_before = scan_before<W>(sum, sh.wave64, total);
+    const unsigned count_before = scan_before<W>(n, sh.wave32, tokens);
     if (tid == 0) {
-        sh.found32[0] = NB;  // top-k's bin, the tokens before it
-        sh.found64[0] = total;  // mass before it
-        sh.found64[1] = total;  // and behind it
-        sh.found32[2] = sh.found32[3] = NB;  // top-p's bins
+        sh.found64[0] = sh.found64[1] = total;  // mass before top-k's bin, and with it
+        sh.found32[2] = sh.found32[3] = NB - 1;      // top-p's bins
     }
     __syncthreads();
     const bool by_k = q.k > 0 && (unsigned)q.k < tokens;  // (tokens: without NaN)
@@ -438,8 +451,9 @@ __global__ void __launch_bounds__(TH) sample_bins_kernel(SampleArgs a) {
     const u64 lo = sh.found64[0], hi = sh.found64[1];  // top-k's mass lies between
     const int k_bin = by_k ? (int)sh.found32[0] : -1;
     const unsigned k_left = sh.found32[1];
+    const bool by_p = q.p < 1.0;
     __syncthreads();
-    if (q.p < 1.0) {
+    if (by_p) {
         const u64 want_lo = max((u64)ceil(q.p * (double)lo), (u64)1), want_hi = max((u64)ceil(q.p * (double)hi), (u64)1);
         u64 s = mass_before;
 #pragma unroll
@@ -454,112 +468,37 @@ __global__ void __launch_bounds__(TH) sample_bins_kernel(SampleArgs a) {
     }
     __syncthreads();
     if (tid == 0) {
-        const bool by_p = q.p < 1.0;
-        const int p_lo = (int)sh.found32[2];
-        row->p_lo = by_p ? p_lo : NB;
-        row->p_hi = by_p ? min((int)sh.found32[3], NB - 1) : -1;
-        row->p_mass = sh.found64[0];
-        row->k_bin = k_bin;
-        row->k_left = k_left;
-        row->k_mass = lo;
-        row->mass = total;
-        row->full = by_p ? p_lo : by_k ? k_bin : NB;
-        row->done = 0;
+        SampleRow r;
+        r.done = 0;
+        r.p_lo = by_p ? (int)sh.found32[2] : NB;
+        r.p_hi = by_p ? (int)sh.found32[3] : -1;
+        r.full = by_p ? r.p_lo : by_k ? k_bin : NB;
+        r.k_bin = k_bin;
+        r.k_left = k_left;
+        r.listed = 0;
+        r.pad = 0;
+        r.p_mass = sh.found64[0];
+        r.k_mass = lo;
+        r.mass = total;
+        r.pad2 = 0;
+        *row = r;
     }
 }
 
-// ------------------------------------------------------------------ the borders, and the token
-// f(key) for each undecided token of the row, a wave a chunk, and end(chunk)
-// behind each chunk's.
-template <bool F32, typename Fn, typename End>
-__device__ void each_undecided(const SampleArgs &a, int m, const SampleRow &r, float top, Fn f, End end) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    for (int c = wave; c < a.chunks; c += TH / 64) {
-        const size_t at = (size_t)m * a.chunks + c;
-        const unsigned n = a.listed[at];
-        if (n <= SAMPLE_LIST) {
-            for (unsigned i = lane; i < n; i += 64) f(a.lists[at * SAMPLE_LIST + i]);
-        } else {  // too many for the list: from the logits again
-            const int stop = min((c + 1) * SAMPLE_CHUNK, a.V);
-            for (int i = c * SAMPLE_CHUNK + lane; i < stop; i += 64) {
-                const int64_t j = (int64_t)m * a.stride + i;
-                const float x = F32 ? ((const float *)a.logits)[j] : f32_of((unsigned)((const uint16_t *)a.logits)[j] << 16);
-                if (x == x && undecided(r, bin_of(x, top))) f(key_of(x));
-            }
-        }
-        end(c);
-    }
-}
-
-// Among the undecided tokens that `in` takes, the largest first: where `want`
-// tokens are together (or, by mass, where the mass before and with them
-// reaches `want`).  Digits of 8 bits from the top; `above` is what lies above
-// the cut's key.
-template <bool F32, bool MASS, typename In>
-__device__ Cut descend(const SampleArgs &a, int m, const SampleRow &r, float top, double c, u64 want, u64 &above, In in,
-                       Shared &sh) {
-    unsigned prefix = 0;
-    above = 0;
-    unsigned here = 0;
-    for (int shift = 24; shift >= (F32 ? 0 : 16); shift -= 8) {
-        __syncthreads();
-        for (int i = threadIdx.x; i < 256; i += TH) {
-            sh.mass[i] = 0;
-            sh.count[i] = 0;
-        }
-        __syncthreads();
-        each_undecided<F32>(
-            a, m, r, top,
-            [&](unsigned key) {
-                if (shift < 24 && (key >> (shift + 8)) != (prefix >> (shift + 8))) return;
-                const float x = logit_of(key);
-                if (!in(key, bin_of(x, top))) return;
-                const unsigned d = 255u - ((key >> shift) & 255u);
-                atomicAdd(&sh.count[d], 1u);
-                if (MASS) atomicAdd(&sh.mass[d], mass_of(weight(x, top, c, sh.pow)));
-            },
-            [](int) {});
-        __syncthreads();
-        const unsigned n = sh.count[threadIdx.x];
-        const u64 v = MASS ? sh.mass[threadIdx.x] : (u64)n;
-        u64 total;
-        const u64 before = above + scan_before(v, sh.wave64, total);
-        if (threadIdx.x == 0) sh.found32[0] = 256;
-        __syncthreads();
-        if (before < want && before + v >= want) {
-            sh.found32[0] = threadIdx.x;
-            sh.found32[1] = n;
-            sh.found64[0] = before;
-        }
-        __syncthreads();
-        if (sh.found32[0] == 256) {  // (not reached: everything)
-            above += total;
-            return Cut{0, 0};
-        }
-        prefix |= (255u - sh.found32[0]) << shift;
-        here = sh.found32[1];
-        above = sh.found64[0];
-    }
-    if (!F32) prefix |= prefix & 0x80000000u ? 0u : 0xFFFFu;  // (the low half of a negative bf16's key)
-    u64 ties = want - above;
-    if (MASS) {
-        const u64 w = mass_of(weight(logit_of(prefix), top, c, sh.pow));
-        ties = w > 0 ? (ties + w - 1) / w : here;
-    }
-    return Cut{prefix, ties < here ? (unsigned)ties : here};
-}
-
+// ------------------------------------------------------------------ the list
 template <bool F32>
-__global__ void __launch_bounds__(TH) sample_pick_kernel(SampleArgs a) {
-    __shared__ Shared sh;
+__global__ void __launch_bounds__(TH) sample_list_kernel(SampleArgs a) {
+    __shared__ double pow[32];
+    __shared__ u64 waves[TH / 64];
+    __shared__ unsigned first;
     const int c = blockIdx.x % a.chunks, m = blockIdx.x / a.chunks, tid = threadIdx.x;
     const SampleRow r = a.rows[m];
     if (r.done) return;
     const Ask q = ask_of(a, m);
-    float x[E];
+    float x[E], mine;
     load_logits<F32>(a.logits, (int64_t)m * a.stride, c * SAMPLE_CHUNK + tid * E, a.V, x);
-    make_powers(sh.pow);
-    const float top = max_all(tid < a.chunks ? a.tops[(size_t)m * a.chunks + tid] : NEG_INF, sh.wavef);
+    make_powers(pow);
+    const float top = top_of<TH / 64>(a, m, mine, (float *)waves);
     u64 sum = 0;
     unsigned open = 0, n = 0;
 #pragma unroll
@@ -567,101 +506,201 @@ __global__ void __launch_bounds__(TH) sample_pick_kernel(SampleArgs a) {
         if (!(x[e] == x[e])) continue;
         const int b = bin_of(x[e], top);
         if (b < r.full) {
-            const double v = weight(x[e], top, q.c, sh.pow);
+            const double v = weight(x[e], top, q.c, pow);
             sum += v >= q.minp ? mass_of(v) : 0;
         } else if (undecided(r, b)) {
             open |= 1u << e;
             ++n;
         }
     }
-    sum = sum_all(sum, sh.wave64);
+    sum = sum_all<TH / 64>(sum, waves);
     unsigned all;
-    unsigned place = scan_before(n, sh.wave32, all);
-    const size_t at = (size_t)m * a.chunks + c;
-    if (all <= SAMPLE_LIST) {
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            if (open >> e & 1) a.lists[at * SAMPLE_LIST + place++] = key_of(x[e]);
-    }
+    unsigned place = scan_before<TH / 64>(n, (unsigned *)waves, all);
     if (tid == 0) {
-        a.kept[at] = sum;
-        a.listed[at] = all;
+        a.kept[(size_t)m * a.chunks + c] = sum;
+        // (chunks come in any order: what is made of the list does not depend on it)
+        if (all > 0) first = atomicAdd(&a.rows[m].listed, all);
     }
-    if (!arrive_last(&a.rows[m].arrived[1], (unsigned)a.chunks, sh)) return;
+    if (all == 0) return;
+    __syncthreads();
+    place += first;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        if (open >> e & 1) {
+            if (place < SAMPLE_LIST) a.lists[(size_t)m * SAMPLE_LIST + place] = u32x2_t{key_of(x[e]), (unsigned)c};
+            ++place;
+        }
+    }
+}
+
+// ------------------------------------------------------------------ the borders, and the token
+constexpr int HELD = SAMPLE_LIST / RTH;  // tokens of the list a thread holds
+
+template <bool F32>
+__global__ void __launch_bounds__(RTH) sample_pick_kernel(SampleArgs a) {
+    __shared__ Shared sh;
+    constexpr int W = RTH / 64;
+    const int m = blockIdx.x, tid = threadIdx.x;
+    const SampleRow r = a.rows[m];
+    if (r.done) return;
+    const Ask q = ask_of(a, m);
+    const unsigned held = r.listed <= SAMPLE_LIST ? r.listed : 0;
+    u32x2_t list[HELD];
+#pragma unroll
+    for (int i = 0; i < HELD; ++i) {
+        const unsigned at = i * RTH + tid;
+        list[i] = at < held ? a.lists[(size_t)m * SAMPLE_LIST + at] : u32x2_t{0u, 0u};
+    }
+    u64 kept = tid < a.chunks ? a.kept[(size_t)m * a.chunks + tid] : 0;
+    make_powers(sh.pow);
+    float mine;
+    const float top = top_of<W>(a, m, mine, sh.wavef);
+
+    // f(key, bin, chunk) for each undecided token
+    const auto each = [&](auto f) {
+        if (r.listed <= SAMPLE_LIST) {
+#pragma unroll
+            for (int i = 0; i < HELD; ++i)
+                if ((unsigned)(i * RTH + tid) < held) f(list[i][0], bin_of(logit_of(list[i][0]), top), (int)list[i][1]);
+        } else {  // more than the list holds: from the logits again
+            for (int i = tid; i < a.V; i += RTH) {
+                const int64_t at = (int64_t)m * a.stride + i;
+                const float x = F32 ? ((const float *)a.logits)[at] : f32_of((unsigned)((const uint16_t *)a.logits)[at] << 16);
+                if (!(x == x)) continue;
+                const int b = bin_of(x, top);
+                if (undecided(r, b)) f(key_of(x), b, i / SAMPLE_CHUNK);
+            }
+        }
+    };
+    const auto mass_at = [&](unsigned key) { return mass_of(weight(logit_of(key), top, q.c, sh.pow)); };
+
+    // Among the undecided tokens that `in` takes, the largest first: where
+    // `want` of them are together (or, by mass, where the mass with them reaches
+    // `want`).  Digits of 10 bits, from the first in which keys differ.
+    const auto descend = [&](auto by_mass, u64 want, auto in) {
+        constexpr bool MASS = decltype(by_mass)::value;
+        unsigned least = ~0u, most = 0;
+        each([&](unsigned key, int b, int) {
+            if (in(key, b)) {
+                least = min(least, key);
+                most = max(most, key);
+            }
+        });
+#pragma unroll
+        for (int d = 32; d; d >>= 1) {
+            least = min(least, (unsigned)__shfl_xor((int)least, d));
+            most = max(most, (unsigned)__shfl_xor((int)most, d));
+        }
+        __syncthreads();
+        if (tid == 0) {
+            sh.found32[2] = ~0u;
+            sh.found32[3] = 0;
+        }
+        __syncthreads();
+        if ((tid & 63) == 0) {
+            atomicMin(&sh.found32[2], least);
+            atomicMax(&sh.found32[3], most);
+        }
+        __syncthreads();
+        least = sh.found32[2];
+        most = sh.found32[3];
+        if (least > most) return Cut{0, 0};  // (no such token)
+        int bits = 32 - __clz((int)(least ^ most));  // (0: one key)
+        unsigned prefix = bits < 32 ? most >> bits << bits : 0u, here = 0;
+        u64 above = 0;
+        do {
+            const int shift = max(bits - 10, 0);
+            sh.mass[tid] = 0;
+            sh.count[tid] = 0;
+            __syncthreads();
+            each([&](unsigned key, int b, int) {
+                if (!in(key, b) || (bits < 32 && (key >> bits) != (prefix >> bits))) return;
+                const unsigned d = (DIGITS - 1) - ((key >> shift) & (DIGITS - 1) & ((1u << (bits - shift)) - 1));
+                atomicAdd(&sh.count[d], 1u);
+                if (MASS) atomicAdd(&sh.mass[d], mass_at(key));
+            });
+            __syncthreads();
+            const unsigned n = sh.count[tid];
+            const u64 v = MASS ? sh.mass[tid] : (u64)n;
+            u64 total;
+            const u64 before = above + scan_before<W>(v, sh.wave64, total);
+            if (tid == 0) sh.found32[0] = DIGITS;
+            __syncthreads();
+            if (before < want && before + v >= want) {
+                sh.found32[0] = tid;
+                sh.found32[1] = n;
+                sh.found64[0] = before;
+            }
+            __syncthreads();
+            const unsigned d = sh.found32[0];
+            if (d == DIGITS) return Cut{0, 0};  // (not reached: all are kept)
+            prefix |= (DIGITS - 1 - d) << shift;
+            here = sh.found32[1];
+            above = sh.found64[0];
+            bits = shift;
+            __syncthreads();
+        } while (bits > 0);
+        u64 ties = want - above;
+        if (MASS) {
+            const u64 w = mass_at(prefix);
+            ties = w > 0 ? (ties + w - 1) / w : here;
+        }
+        return Cut{prefix, ties < here ? (unsigned)ties : here};
+    };
 
     Cut cut{0, 0xFFFFFFFFu};
-    u64 above, k_total = r.mass;
-    unsigned k_key = 0;
+    u64 mass = r.mass;  // what top-k keeps
     if (r.k_bin >= 0) {
-        cut = descend<F32, false>(a, m, r, top, q.c, r.k_left, above, [&](unsigned, int b) { return b == r.k_bin; }, sh);
-        k_key = cut.key;
+        cut = descend(std::false_type(), r.k_left, [&](unsigned, int b) { return b == r.k_bin; });
         if (q.p < 1.0) {
-            // top-k's mass: of the bins before, and of its bin's tokens that are kept
             u64 s = 0;
-            each_undecided<F32>(
-                a, m, r, top,
-                [&](unsigned key) {
-                    const float v = logit_of(key);
-                    if (key > k_key && bin_of(v, top) == r.k_bin) s += mass_of(weight(v, top, q.c, sh.pow));
-                },
-                [](int) {});
-            k_total = r.k_mass + sum_all(s, sh.wave64) + (u64)cut.ties * mass_of(weight(logit_of(k_key), top, q.c, sh.pow));
+            each([&](unsigned key, int b, int) { s += key > cut.key && b == r.k_bin ? mass_at(key) : 0; });
+            mass = r.k_mass + sum_all<W>(s, sh.wave64) + (u64)cut.ties * mass_at(cut.key);
         }
     }
     if (q.p < 1.0) {
-        const u64 want = max((u64)ceil(q.p * (double)k_total), (u64)1) - r.p_mass;
-        const unsigned k_ties = cut.ties;
-        cut = descend<F32, true>(a, m, r, top, q.c, want, above,
-                                 [&](unsigned key, int b) { return b >= r.p_lo && b <= r.p_hi && key >= k_key; }, sh);
-        if (r.k_bin >= 0 && cut.key <= k_key) cut = Cut{k_key, cut.key == k_key ? min(cut.ties, k_ties) : k_ties};
+        const Cut k = cut;
+        const u64 want = max((u64)ceil(q.p * (double)mass), (u64)1) - r.p_mass;
+        cut = descend(std::true_type(), want, [&](unsigned key, int b) { return b >= r.p_lo && b <= r.p_hi && key >= k.key; });
+        if (r.k_bin >= 0 && cut.key <= k.key) cut = Cut{k.key, cut.key == k.key ? min(cut.ties, k.ties) : k.ties};
     }
     // what the chunks keep of their undecided tokens: those above the cut ...
     __syncthreads();
-    const int lane = tid & 63;
-    u64 more = 0;
-    unsigned ties = 0;
-    each_undecided<F32>(
-        a, m, r, top,
-        [&](unsigned key) {
-            if (key > cut.key) {
-                const double v = weight(logit_of(key), top, q.c, sh.pow);
-                more += v >= q.minp ? mass_of(v) : 0;
-            }
-            ties += key == cut.key;
-        },
-        [&](int chunk) {
-#pragma unroll
-            for (int d = 32; d; d >>= 1) {
-                more += __shfl_xor(more, d);
-                ties += __shfl_xor(ties, d);
-            }
-            if (lane == 0) {
-                sh.mass[chunk] = more;
-                sh.ties[chunk] = ties;
-            }
-            more = 0;
-            ties = 0;
-        });
+    if (tid < TH) {
+        sh.more[tid] = 0;
+        sh.ties[tid] = 0;
+    }
+    __syncthreads();
+    each([&](unsigned key, int, int c) {
+        if (key > cut.key) {
+            const double v = weight(logit_of(key), top, q.c, sh.pow);
+            if (v >= q.minp) atomicAdd(&sh.more[c], mass_of(v));
+        } else if (key == cut.key) {
+            atomicAdd(&sh.ties[c], 1u);
+        }
+    });
     __syncthreads();
     // ... and of the cut's key, the first tokens of the row
-    u64 kept = 0;
-    unsigned t;
-    const unsigned mine = tid < a.chunks ? sh.ties[tid] : 0;
-    const unsigned ties_before = scan_before(mine, sh.wave32, t);
+    const unsigned ties = tid < a.chunks ? sh.ties[tid] : 0;
+    unsigned all;
+    const unsigned ties_before = scan_before<W>(ties, sh.wave32, all);
     if (tid < a.chunks) {
-        const unsigned take = min(mine, ties_before < cut.ties ? cut.ties - ties_before : 0u);
+        const unsigned take = min(ties, ties_before < cut.ties ? cut.ties - ties_before : 0u);
         const double v = take ? weight(logit_of(cut.key), top, q.c, sh.pow) : 0.0;
-        kept = a.kept[(size_t)m * a.chunks + tid] + sh.mass[tid] + (take && v >= q.minp ? take * mass_of(v) : 0);
+        kept += sh.more[tid] + (take && v >= q.minp ? take * mass_of(v) : 0);
     }
-    pick<F32>(a, m, q, top, kept, &r, cut, sh);
+    pick<F32>(a, m, q, top, kept, &r, cut, ties_before, sh);
 }
 
 template <bool F32>
 void run(const SampleArgs &a, hipStream_t s) {
-    const dim3 grid((unsigned)((int64_t)a.M * a.chunks));
-    hipLaunchKernelGGL((sample_top_kernel<F32>), grid, dim3(TH), 0, s, a);
-    hipLaunchKernelGGL((sample_bins_kernel<F32>), grid, dim3(TH), 0, s, a);
-    if (a.top_k || a.top_p) hipLaunchKernelGGL((sample_pick_kernel<F32>), grid, dim3(TH), 0, s, a);
+    const dim3 chunks((unsigned)((int64_t)a.M * a.chunks)), rows((unsigned)a.M);
+    hipLaunchKernelGGL((sample_top_kernel<F32>), chunks, dim3(TH), 0, s, a);
+    hipLaunchKernelGGL((sample_bins_kernel<F32>), chunks, dim3(TH), 0, s, a);
+    hipLaunchKernelGGL((sample_find_kernel<F32>), rows, dim3(RTH), 0, s, a);
+    if (!a.top_k && !a.top_p) return;
+    hipLaunchKernelGGL((sample_list_kernel<F32>), chunks, dim3(TH), 0, s, a);
+    hipLaunchKernelGGL((sample_pick_kernel<F32>), rows, dim3(RTH), 0, s, a);
 }
 
 }  // namespace
