@@ -731,7 +731,7 @@ size_t qg_sample_workspace_bytes(int64_t M, int64_t V);
  *               alignment.  Read only.  NaN is never taken; a row of nothing
  *               but -infinity and NaN gives token -1 and logprob NaN; +infinity
  *               leaves only the infinite ones.
- *  M            rows; M times the chunks of 4096 tokens of a row below 2^22.
+ *  M            rows; M times the chunks of 4096 tokens of a row below 2^24.
  *  V            1..2^20.
  *  u            device fp32 [M], in [0, 1) (values outside are taken as the
  *               nearest inside).

@@ -24,9 +24,8 @@ constexpr int64_t APPEND_TOKENS_MAX = int64_t(1) << 28;
 constexpr int64_t JOINS_MAX = (int64_t(1) << 26) - 8;
 // (the rotation takes 64 a token, more only of up to 2048 tokens)
 constexpr int64_t ROPE_TOKENS_MAX = (int64_t(1) << 26) - 8;
-// (the sampling takes a workgroup of 256 for each chunk of a row, and one of
-// 1024 for each row)
-constexpr int64_t SAMPLE_GROUPS_MAX = (int64_t(1) << 22) - 1;
+// (the sampling takes a workgroup of 256 for each chunk of a row)
+constexpr int64_t SAMPLE_GROUPS_MAX = (int64_t(1) << 24) - 1;
 constexpr int64_t LEN_MAX = int64_t(1) << 30;
 constexpr int64_t STRIDE_MAX = int64_t(1) << 31;
 

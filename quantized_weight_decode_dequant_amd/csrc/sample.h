@@ -11,8 +11,7 @@ constexpr int SAMPLE_THREADS = 256;
 constexpr int SAMPLE_PER_THREAD = 16;
 constexpr int SAMPLE_CHUNK = SAMPLE_THREADS * SAMPLE_PER_THREAD;  // tokens of one workgroup
 constexpr int SAMPLE_BINS = 2048;
-constexpr int SAMPLE_ROW_THREADS = 1024;  // of the kernels with a workgroup a row
-constexpr int SAMPLE_LIST = 8192;         // a row's undecided tokens that are kept as a list
+constexpr int SAMPLE_LIST = 8192;  // a row's undecided tokens that are kept as a list
 static_assert(SAMPLE_V_MAX / SAMPLE_CHUNK <= SAMPLE_THREADS, "a row's chunks are one for each thread");
 
 // What a row's kernels leave for each other.
@@ -44,7 +43,7 @@ struct SampleArgs {
     unsigned long long *kept;    // [M][chunks]: mass of a chunk that is kept for sure
     float *tops;                 // [M][chunks]: largest logit
     int32_t *top_at;             // [M][chunks]: the first token that has it
-    u32x2_t *lists;              // [M][SAMPLE_LIST]: (key, chunk) of undecided tokens
+    u32x2_t *lists;              // [M][SAMPLE_LIST]: (key, token) of undecided tokens
     int M, V, chunks;
 };
 

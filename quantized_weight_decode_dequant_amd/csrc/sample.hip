@@ -39,7 +39,7 @@ namespace {
 
 typedef unsigned long long u64;
 
-constexpr int TH = SAMPLE_THREADS, RTH = SAMPLE_ROW_THREADS, E = SAMPLE_PER_THREAD, NB = SAMPLE_BINS;
+constexpr int TH = SAMPLE_THREADS, W = TH / 64, E = SAMPLE_PER_THREAD, NB = SAMPLE_BINS;
 constexpr float NEG_INF = -__builtin_inff();
 constexpr double UNIT = 0x1p42;  // of masses
 
@@ -144,8 +144,8 @@ __device__ __forceinline__ int bin_of(float x, float top) {
     return min(max((int)(bits_of(d) >> 16) - ((127 - 4) << 7), 0), NB - 1);
 }
 
-// Sum over the workgroup's threads before this one, and over all (W waves).
-template <int W, typename T>
+// Sum over the workgroup's threads before this one, and over all.
+template <typename T>
 __device__ __forceinline__ T scan_before(T v, T *waves, T &total) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     T upto = v;
@@ -168,7 +168,6 @@ __device__ __forceinline__ T scan_before(T v, T *waves, T &total) {
     return before + upto - v;
 }
 
-template <int W>
 __device__ __forceinline__ u64 sum_all(u64 v, u64 *waves) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
@@ -182,7 +181,6 @@ __device__ __forceinline__ u64 sum_all(u64 v, u64 *waves) {
     return total;
 }
 
-template <int W>
 __device__ __forceinline__ float max_all(float v, float *waves) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
@@ -197,10 +195,9 @@ __device__ __forceinline__ float max_all(float v, float *waves) {
 }
 
 // A row's largest logit, from its chunks'.
-template <int W>
 __device__ __forceinline__ float top_of(const SampleArgs &a, int m, float &mine, float *waves) {
     mine = (int)threadIdx.x < a.chunks ? a.tops[(size_t)m * a.chunks + threadIdx.x] : NEG_INF;
-    return max_all<W>(mine, waves);
+    return max_all(mine, waves);
 }
 
 // ------------------------------------------------------------------ the chunks' largest
@@ -221,7 +218,7 @@ __global__ void __launch_bounds__(TH) sample_top_kernel(SampleArgs a) {
 #pragma unroll
     for (int e = 0; e < E; ++e) top = fmaxf(top, x[e]);  // (past NaN)
     if (tid == 0) first = 0x7FFFFFFF;
-    top = max_all<TH / 64>(top, waves);
+    top = max_all(top, waves);
     int at = 0x7FFFFFFF;
 #pragma unroll
     for (int e = E - 1; e >= 0; --e)
@@ -252,7 +249,7 @@ __global__ void __launch_bounds__(TH) sample_bins_kernel(SampleArgs a) {
             masses[i] = 0;
             counts[i] = 0;
         }
-    const float top = top_of<TH / 64>(a, m, mine, (float *)waves);
+    const float top = top_of(a, m, mine, (float *)waves);
     if (!q.filters()) {
         u64 sum = 0;
 #pragma unroll
@@ -260,7 +257,7 @@ __global__ void __launch_bounds__(TH) sample_bins_kernel(SampleArgs a) {
             const double v = weight(x[e], top, q.c, pow);
             sum += v >= q.minp ? mass_of(v) : 0;
         }
-        sum = sum_all<TH / 64>(sum, waves);
+        sum = sum_all(sum, waves);
         if (tid == 0) a.kept[(size_t)m * a.chunks + c] = sum;
         return;
     }
@@ -281,30 +278,24 @@ __global__ void __launch_bounds__(TH) sample_bins_kernel(SampleArgs a) {
 
 // ------------------------------------------------------------------ by rows
 // What a row's workgroup keeps in LDS.
-constexpr int DIGITS = RTH;  // of a level of the descent
+constexpr int DIGITS = TH;  // of a level of the descent
 struct Shared {
     double pow[32];
     union {
-        u64 wave64[RTH / 64];
-        unsigned wave32[RTH / 64];
-        float wavef[RTH / 64];
+        u64 wave64[W];
+        unsigned wave32[W];
+        float wavef[W];
     };
     u64 found64[2];
     unsigned found32[4];
-    union {
-        u64 mass[DIGITS];   // by digit
-        u64 more[TH];       // by chunk
-    };
-    union {
-        unsigned count[DIGITS];
-        unsigned ties[TH];
-    };
+    u64 mass[TH];  // by digit, then by chunk
+    unsigned count[TH];
 };
 
 // A row's cut in terms of its undecided tokens: those of larger keys are kept,
-// and the first `ties` of this key.
+// and of this key the first `ties` as far as `token`.
 struct Cut {
-    unsigned key, ties;
+    unsigned key, token, ties;
 };
 
 // Whether a filter's border lies in this bin.
@@ -318,10 +309,9 @@ __device__ __forceinline__ bool undecided(const SampleRow &r, int b) {
 template <bool F32>
 __device__ __forceinline__ void pick(const SampleArgs &a, int m, const Ask &q, float top, u64 mine, const SampleRow *row, Cut cut,
                                      unsigned ties_before, Shared &sh) {
-    constexpr int W = RTH / 64, PE = SAMPLE_CHUNK / RTH;
     const int tid = threadIdx.x;
     u64 total;
-    const u64 before = scan_before<W>(mine, sh.wave64, total);
+    const u64 before = scan_before(mine, sh.wave64, total);
     if (total == 0) {  // (only -infinities and NaN)
         if (tid == 0) {
             a.tokens[m] = -1;
@@ -338,52 +328,53 @@ __device__ __forceinline__ void pick(const SampleArgs &a, int m, const Ask &q, f
         sh.found64[0] = r - before;
     }
     __syncthreads();
-    const int at = (int)sh.found32[0] * SAMPLE_CHUNK + tid * PE;
+    const int at = (int)sh.found32[0] * SAMPLE_CHUNK + tid * E;
     r = sh.found64[0];
-    float x[PE];
+    float x[E];
     load_logits<F32>(a.logits, (int64_t)m * a.stride, at, a.V, x);
     unsigned place = 0;  // of this thread's first token of the cut key among all
-    if (row) {
+    const bool by_ties = row && cut.ties != ~0u;
+    if (by_ties) {
         unsigned n = 0, all;
 #pragma unroll
-        for (int e = 0; e < PE; ++e) n += x[e] == x[e] && key_of(x[e]) == cut.key && undecided(*row, bin_of(x[e], top));
+        for (int e = 0; e < E; ++e) n += x[e] == x[e] && key_of(x[e]) == cut.key && undecided(*row, bin_of(x[e], top));
         place = sh.found32[1];
-        place += scan_before<W>(n, sh.wave32, all);
+        place += scan_before(n, sh.wave32, all);
     }
-    u64 w[PE], sum = 0;
-    double v[PE];
+    u64 w[E], sum = 0;
 #pragma unroll
-    for (int e = 0; e < PE; ++e) {
-        v[e] = weight(x[e], top, q.c, sh.pow);
-        bool keep = v[e] >= q.minp;
+    for (int e = 0; e < E; ++e) {
+        const double v = weight(x[e], top, q.c, sh.pow);
+        bool keep = v >= q.minp;
         if (row && x[e] == x[e]) {
             const int b = bin_of(x[e], top);
             const unsigned key = key_of(x[e]);
             if (undecided(*row, b)) {
-                keep &= key > cut.key || (key == cut.key && place < cut.ties);
-                place += key == cut.key;
+                const bool tie = key == cut.key;
+                keep &= key > cut.key || (tie && (unsigned)(at + e) <= cut.token && place < cut.ties);
+                place += by_ties && tie;
             } else {
                 keep &= b < row->full;
             }
         }
-        w[e] = keep && x[e] == x[e] ? mass_of(v[e]) : 0;
+        w[e] = keep && x[e] == x[e] ? mass_of(v) : 0;
         sum += w[e];
     }
-    u64 from = scan_before<W>(sum, sh.wave64, sum);
+    u64 from = scan_before(sum, sh.wave64, sum);
 #pragma unroll
-    for (int e = 0; e < PE; ++e) {
+    for (int e = 0; e < E; ++e) {
         if (w[e] > 0 && r >= from && r - from < w[e]) {
             a.tokens[m] = at + e;
-            if (a.logprobs) a.logprobs[m] = (float)log(v[e] / ((double)total * (1.0 / UNIT)));
+            if (a.logprobs) a.logprobs[m] = (float)log(weight(x[e], top, q.c, sh.pow) / ((double)total * (1.0 / UNIT)));
         }
         from += w[e];
     }
 }
 
 template <bool F32>
-__global__ void __launch_bounds__(RTH) sample_find_kernel(SampleArgs a) {
+__global__ void __launch_bounds__(TH) sample_find_kernel(SampleArgs a) {
     __shared__ Shared sh;
-    constexpr int W = RTH / 64, PER = NB / RTH;
+    constexpr int PER = NB / TH;
     const int m = blockIdx.x, tid = threadIdx.x;
     SampleRow *row = a.rows + m;
     const Ask q = ask_of(a, m);
@@ -402,7 +393,7 @@ __global__ void __launch_bounds__(RTH) sample_find_kernel(SampleArgs a) {
     const u64 kept = !q.greedy && !filters && tid < a.chunks ? a.kept[(size_t)m * a.chunks + tid] : 0;
     make_powers(sh.pow);
     float mine;
-    const float top = top_of<W>(a, m, mine, sh.wavef);
+    const float top = top_of(a, m, mine, sh.wavef);
     const bool none = top == NEG_INF;  // of finite or infinite logits
     if (q.greedy || none || !filters) {
         if (tid == 0) {
@@ -411,7 +402,7 @@ __global__ void __launch_bounds__(RTH) sample_find_kernel(SampleArgs a) {
         }
         __syncthreads();
         if (!q.greedy) {
-            pick<F32>(a, m, q, top, none ? 0 : kept, nullptr, Cut{0, 0}, 0, sh);
+            pick<F32>(a, m, q, top, none ? 0 : kept, nullptr, Cut{0, 0, 0}, 0, sh);
             return;
         }
         if (tid < a.chunks && mine == top) atomicMin(&sh.found32[0], (unsigned)a.top_at[(size_t)m * a.chunks + tid]);
@@ -424,8 +415,8 @@ __global__ void __launch_bounds__(RTH) sample_find_kernel(SampleArgs a) {
     }
     u64 total;
     unsigned tokens;
-    const u64 mass_before = scan_before<W>(sum, sh.wave64, total);
-    const unsigned count_before = scan_before<W>(n, sh.wave32, tokens);
+    const u64 mass_before = scan_before(sum, sh.wave64, total);
+    const unsigned count_before = scan_before(n, sh.wave32, tokens);
     if (tid == 0) {
         sh.found64[0] = sh.found64[1] = total;  // mass before top-k's bin, and with it
         sh.found32[2] = sh.found32[3] = NB - 1;      // top-p's bins
@@ -498,7 +489,7 @@ __global__ void __launch_bounds__(TH) sample_list_kernel(SampleArgs a) {
     float x[E], mine;
     load_logits<F32>(a.logits, (int64_t)m * a.stride, c * SAMPLE_CHUNK + tid * E, a.V, x);
     make_powers(pow);
-    const float top = top_of<TH / 64>(a, m, mine, (float *)waves);
+    const float top = top_of(a, m, mine, (float *)waves);
     u64 sum = 0;
     unsigned open = 0, n = 0;
 #pragma unroll
@@ -513,9 +504,9 @@ __global__ void __launch_bounds__(TH) sample_list_kernel(SampleArgs a) {
             ++n;
         }
     }
-    sum = sum_all<TH / 64>(sum, waves);
+    sum = sum_all(sum, waves);
     unsigned all;
-    unsigned place = scan_before<TH / 64>(n, (unsigned *)waves, all);
+    unsigned place = scan_before(n, (unsigned *)waves, all);
     if (tid == 0) {
         a.kept[(size_t)m * a.chunks + c] = sum;
         // (chunks come in any order: what is made of the list does not depend on it)
@@ -527,43 +518,88 @@ __global__ void __launch_bounds__(TH) sample_list_kernel(SampleArgs a) {
 #pragma unroll
     for (int e = 0; e < E; ++e) {
         if (open >> e & 1) {
-            if (place < SAMPLE_LIST) a.lists[(size_t)m * SAMPLE_LIST + place] = u32x2_t{key_of(x[e]), (unsigned)c};
+            if (place < SAMPLE_LIST) a.lists[(size_t)m * SAMPLE_LIST + place] = u32x2_t{key_of(x[e]), (unsigned)(c * SAMPLE_CHUNK + tid * E + e)};
             ++place;
         }
     }
 }
 
 // ------------------------------------------------------------------ the borders, and the token
-constexpr int HELD = SAMPLE_LIST / RTH;  // tokens of the list a thread holds
-
 template <bool F32>
-__global__ void __launch_bounds__(RTH) sample_pick_kernel(SampleArgs a) {
+__global__ void __launch_bounds__(TH) sample_pick_kernel(SampleArgs a) {
     __shared__ Shared sh;
-    constexpr int W = RTH / 64;
+    __shared__ union {
+        u32x2_t list[SAMPLE_LIST];
+        u64 order[TH];  // of a short list
+    } ls;
     const int m = blockIdx.x, tid = threadIdx.x;
     const SampleRow r = a.rows[m];
     if (r.done) return;
     const Ask q = ask_of(a, m);
-    const unsigned held = r.listed <= SAMPLE_LIST ? r.listed : 0;
-    u32x2_t list[HELD];
-#pragma unroll
-    for (int i = 0; i < HELD; ++i) {
-        const unsigned at = i * RTH + tid;
-        list[i] = at < held ? a.lists[(size_t)m * SAMPLE_LIST + at] : u32x2_t{0u, 0u};
+    const u32x2_t *list = a.lists + (size_t)m * SAMPLE_LIST;
+    const bool brief = r.listed <= TH;  // a token of the list for each thread
+    u32x2_t own = {0u, 0u};
+    if (brief) {
+        if ((unsigned)tid < r.listed) own = list[tid];
+    } else if (r.listed <= SAMPLE_LIST) {
+#pragma unroll 8
+        for (unsigned i = tid; i < r.listed; i += TH) ls.list[i] = list[i];
     }
     u64 kept = tid < a.chunks ? a.kept[(size_t)m * a.chunks + tid] : 0;
     make_powers(sh.pow);
     float mine;
-    const float top = top_of<W>(a, m, mine, sh.wavef);
+    const float top = top_of(a, m, mine, sh.wavef);
+    const auto mass_at = [&](unsigned key) { return mass_of(weight(logit_of(key), top, q.c, sh.pow)); };
+
+    if (brief) {
+        // every token's rank and the mass before it, against all others
+        const bool valid = (unsigned)tid < r.listed;
+        const double v = valid ? weight(logit_of(own[0]), top, q.c, sh.pow) : 0.0;
+        const u64 w = mass_of(v), order = ((u64)own[0] << 32) | ~own[1];  // larger: earlier
+        const int b = valid ? bin_of(logit_of(own[0]), top) : NB;
+        ls.order[tid] = order;
+        sh.mass[tid] = w;
+        if (tid == 0) sh.found64[0] = ~0ull;
+        const unsigned sooner = (unsigned)__syncthreads_count(b < r.k_bin);  // listed, before top-k's bin
+        unsigned rank = 0;
+        u64 before = r.p_mass;
+        if (valid)
+            for (unsigned j = 0; j < r.listed; ++j) {
+                const bool first = ls.order[j] > order;
+                rank += first;
+                before += first ? sh.mass[j] : 0;
+            }
+        bool keep = valid && (r.k_bin < 0 || rank < r.k_left + sooner);
+        if (q.p < 1.0) {
+            u64 mass = r.mass;  // what top-k keeps
+            if (r.k_bin >= 0) mass = r.k_mass + sum_all(keep && b == r.k_bin ? w : 0, sh.wave64);
+            keep &= b <= r.p_hi && before < max((u64)ceil(q.p * (double)mass), (u64)1);
+        }
+        __syncthreads();
+        sh.mass[tid] = 0;
+        __syncthreads();
+        // kept is what comes first, as far as the last of them
+        u64 last = keep ? order : ~0ull;
+#pragma unroll
+        for (int d = 32; d; d >>= 1) last = min(last, (u64)__shfl_xor(last, d));
+        if ((tid & 63) == 0) atomicMin(&sh.found64[0], last);
+        if (keep && v >= q.minp) atomicAdd(&sh.mass[own[1] / SAMPLE_CHUNK], w);
+        __syncthreads();
+        last = sh.found64[0];
+        if (tid < a.chunks) kept += sh.mass[tid];
+        pick<F32>(a, m, q, top, kept, &r, Cut{(unsigned)(last >> 32), ~(unsigned)last, ~0u}, 0, sh);
+        return;
+    }
 
     // f(key, bin, chunk) for each undecided token
     const auto each = [&](auto f) {
         if (r.listed <= SAMPLE_LIST) {
-#pragma unroll
-            for (int i = 0; i < HELD; ++i)
-                if ((unsigned)(i * RTH + tid) < held) f(list[i][0], bin_of(logit_of(list[i][0]), top), (int)list[i][1]);
+            for (unsigned i = tid; i < r.listed; i += TH) {
+                const u32x2_t t = ls.list[i];
+                f(t[0], bin_of(logit_of(t[0]), top), (int)(t[1] / SAMPLE_CHUNK));
+            }
         } else {  // more than the list holds: from the logits again
-            for (int i = tid; i < a.V; i += RTH) {
+            for (int i = tid; i < a.V; i += TH) {
                 const int64_t at = (int64_t)m * a.stride + i;
                 const float x = F32 ? ((const float *)a.logits)[at] : f32_of((unsigned)((const uint16_t *)a.logits)[at] << 16);
                 if (!(x == x)) continue;
@@ -572,11 +608,10 @@ __global__ void __launch_bounds__(RTH) sample_pick_kernel(SampleArgs a) {
             }
         }
     };
-    const auto mass_at = [&](unsigned key) { return mass_of(weight(logit_of(key), top, q.c, sh.pow)); };
 
     // Among the undecided tokens that `in` takes, the largest first: where
     // `want` of them are together (or, by mass, where the mass with them reaches
-    // `want`).  Digits of 10 bits, from the first in which keys differ.
+    // `want`).  Digits of 8 bits, from the first in which keys differ.
     const auto descend = [&](auto by_mass, u64 want, auto in) {
         constexpr bool MASS = decltype(by_mass)::value;
         unsigned least = ~0u, most = 0;
@@ -604,18 +639,18 @@ __global__ void __launch_bounds__(RTH) sample_pick_kernel(SampleArgs a) {
         __syncthreads();
         least = sh.found32[2];
         most = sh.found32[3];
-        if (least > most) return Cut{0, 0};  // (no such token)
-        int bits = 32 - __clz((int)(least ^ most));  // (0: one key)
+        if (least > most) return Cut{0, ~0u, 0};  // (no such token)
+        int bits = least == most ? 0 : 32 - __clz((int)(least ^ most));
         unsigned prefix = bits < 32 ? most >> bits << bits : 0u, here = 0;
         u64 above = 0;
         do {
-            const int shift = max(bits - 10, 0);
+            const int shift = max(bits - 8, 0);
             sh.mass[tid] = 0;
             sh.count[tid] = 0;
             __syncthreads();
             each([&](unsigned key, int b, int) {
                 if (!in(key, b) || (bits < 32 && (key >> bits) != (prefix >> bits))) return;
-                const unsigned d = (DIGITS - 1) - ((key >> shift) & (DIGITS - 1) & ((1u << (bits - shift)) - 1));
+                const unsigned d = (DIGITS - 1) - ((key >> shift) & ((1u << (bits - shift)) - 1));
                 atomicAdd(&sh.count[d], 1u);
                 if (MASS) atomicAdd(&sh.mass[d], mass_at(key));
             });
@@ -623,7 +658,7 @@ __global__ void __launch_bounds__(RTH) sample_pick_kernel(SampleArgs a) {
             const unsigned n = sh.count[tid];
             const u64 v = MASS ? sh.mass[tid] : (u64)n;
             u64 total;
-            const u64 before = above + scan_before<W>(v, sh.wave64, total);
+            const u64 before = above + scan_before(v, sh.wave64, total);
             if (tid == 0) sh.found32[0] = DIGITS;
             __syncthreads();
             if (before < want && before + v >= want) {
@@ -633,7 +668,7 @@ __global__ void __launch_bounds__(RTH) sample_pick_kernel(SampleArgs a) {
             }
             __syncthreads();
             const unsigned d = sh.found32[0];
-            if (d == DIGITS) return Cut{0, 0};  // (not reached: all are kept)
+            if (d == DIGITS) return Cut{0, ~0u, 0};  // (not reached: all are kept)
             prefix |= (DIGITS - 1 - d) << shift;
             here = sh.found32[1];
             above = sh.found64[0];
@@ -645,49 +680,48 @@ __global__ void __launch_bounds__(RTH) sample_pick_kernel(SampleArgs a) {
             const u64 w = mass_at(prefix);
             ties = w > 0 ? (ties + w - 1) / w : here;
         }
-        return Cut{prefix, ties < here ? (unsigned)ties : here};
+        return Cut{prefix, ~0u, ties < here ? (unsigned)ties : here};
     };
 
-    Cut cut{0, 0xFFFFFFFFu};
+    __syncthreads();
+    Cut cut{0, ~0u, 0};
     u64 mass = r.mass;  // what top-k keeps
     if (r.k_bin >= 0) {
         cut = descend(std::false_type(), r.k_left, [&](unsigned, int b) { return b == r.k_bin; });
         if (q.p < 1.0) {
             u64 s = 0;
             each([&](unsigned key, int b, int) { s += key > cut.key && b == r.k_bin ? mass_at(key) : 0; });
-            mass = r.k_mass + sum_all<W>(s, sh.wave64) + (u64)cut.ties * mass_at(cut.key);
+            mass = r.k_mass + sum_all(s, sh.wave64) + (u64)cut.ties * mass_at(cut.key);
         }
     }
     if (q.p < 1.0) {
         const Cut k = cut;
         const u64 want = max((u64)ceil(q.p * (double)mass), (u64)1) - r.p_mass;
         cut = descend(std::true_type(), want, [&](unsigned key, int b) { return b >= r.p_lo && b <= r.p_hi && key >= k.key; });
-        if (r.k_bin >= 0 && cut.key <= k.key) cut = Cut{k.key, cut.key == k.key ? min(cut.ties, k.ties) : k.ties};
+        if (r.k_bin >= 0 && cut.key <= k.key) cut = Cut{k.key, ~0u, cut.key == k.key ? min(cut.ties, k.ties) : k.ties};
     }
     // what the chunks keep of their undecided tokens: those above the cut ...
     __syncthreads();
-    if (tid < TH) {
-        sh.more[tid] = 0;
-        sh.ties[tid] = 0;
-    }
+    sh.mass[tid] = 0;
+    sh.count[tid] = 0;
     __syncthreads();
     each([&](unsigned key, int, int c) {
         if (key > cut.key) {
             const double v = weight(logit_of(key), top, q.c, sh.pow);
-            if (v >= q.minp) atomicAdd(&sh.more[c], mass_of(v));
+            if (v >= q.minp) atomicAdd(&sh.mass[c], mass_of(v));
         } else if (key == cut.key) {
-            atomicAdd(&sh.ties[c], 1u);
+            atomicAdd(&sh.count[c], 1u);
         }
     });
     __syncthreads();
     // ... and of the cut's key, the first tokens of the row
-    const unsigned ties = tid < a.chunks ? sh.ties[tid] : 0;
+    const unsigned ties = sh.count[tid];
     unsigned all;
-    const unsigned ties_before = scan_before<W>(ties, sh.wave32, all);
+    const unsigned ties_before = scan_before(ties, sh.wave32, all);
     if (tid < a.chunks) {
         const unsigned take = min(ties, ties_before < cut.ties ? cut.ties - ties_before : 0u);
         const double v = take ? weight(logit_of(cut.key), top, q.c, sh.pow) : 0.0;
-        kept += sh.more[tid] + (take && v >= q.minp ? take * mass_of(v) : 0);
+        kept += sh.mass[tid] + (take && v >= q.minp ? take * mass_of(v) : 0);
     }
     pick<F32>(a, m, q, top, kept, &r, cut, ties_before, sh);
 }
@@ -697,10 +731,10 @@ void run(const SampleArgs &a, hipStream_t s) {
     const dim3 chunks((unsigned)((int64_t)a.M * a.chunks)), rows((unsigned)a.M);
     hipLaunchKernelGGL((sample_top_kernel<F32>), chunks, dim3(TH), 0, s, a);
     hipLaunchKernelGGL((sample_bins_kernel<F32>), chunks, dim3(TH), 0, s, a);
-    hipLaunchKernelGGL((sample_find_kernel<F32>), rows, dim3(RTH), 0, s, a);
+    hipLaunchKernelGGL((sample_find_kernel<F32>), rows, dim3(TH), 0, s, a);
     if (!a.top_k && !a.top_p) return;
     hipLaunchKernelGGL((sample_list_kernel<F32>), chunks, dim3(TH), 0, s, a);
-    hipLaunchKernelGGL((sample_pick_kernel<F32>), rows, dim3(RTH), 0, s, a);
+    hipLaunchKernelGGL((sample_pick_kernel<F32>), rows, dim3(TH), 0, s, a);
 }
 
 }  // namespace
