@@ -71,7 +71,7 @@ bool sample_layout(int64_t M, int64_t V, SampleLayout *l) {
     l->rows = take(sizeof(SampleRow));
     l->masses = take(8 * SAMPLE_BINS);
     l->counts = take(4 * SAMPLE_BINS);
-    l->kept = take(8 * C);
+    l->kept = take(8 * C * SAMPLE_SUBS);
     l->tops = take(4 * C);
     l->top_at = take(4 * C);
     l->lists = take(8 * SAMPLE_LIST);
@@ -375,6 +375,7 @@ int sample_run(const void *logits, int x_dtype, int64_t M, int64_t V, int64_t st
         a.M = (int)M;
         a.V = (int)V;
         a.chunks = (int)l.chunks;
+        a.few = M * l.chunks <= 1024;
         return hip_status(launch_sample(a, x_dtype == QG_OUT_F32, reinterpret_cast<hipStream_t>(stream)));
     } catch (...) {
         return QG_EINTERNAL;

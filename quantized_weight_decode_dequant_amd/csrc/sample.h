@@ -12,6 +12,7 @@ constexpr int SAMPLE_PER_THREAD = 16;
 constexpr int SAMPLE_CHUNK = SAMPLE_THREADS * SAMPLE_PER_THREAD;  // tokens of one workgroup
 constexpr int SAMPLE_BINS = 2048;
 constexpr int SAMPLE_LIST = 8192;  // a row's undecided tokens that are kept as a list
+constexpr int SAMPLE_SUBS = SAMPLE_THREADS / 64;  // parts of a chunk, a wave's 1024 tokens each
 static_assert(SAMPLE_V_MAX / SAMPLE_CHUNK <= SAMPLE_THREADS, "a row's chunks are one for each thread");
 
 // What a row's kernels leave for each other.
@@ -40,11 +41,12 @@ struct SampleArgs {
     SampleRow *rows;             // [M]
     unsigned long long *masses;  // [M][SAMPLE_BINS]
     unsigned *counts;            // [M][SAMPLE_BINS]
-    unsigned long long *kept;    // [M][chunks]: mass of a chunk that is kept for sure
+    unsigned long long *kept;    // [M][chunks][SAMPLE_SUBS]: mass that is kept for sure
     float *tops;                 // [M][chunks]: largest logit
     int32_t *top_at;             // [M][chunks]: the first token that has it
     u32x2_t *lists;              // [M][SAMPLE_LIST]: (key, token) of undecided tokens
     int M, V, chunks;
+    bool few;  // workgroups than fill the GPU: read ahead of a row's settings
 };
 
 hipError_t launch_sample(const SampleArgs &a, bool x_f32, hipStream_t s);

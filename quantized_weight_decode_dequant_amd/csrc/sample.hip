@@ -144,16 +144,34 @@ __device__ __forceinline__ int bin_of(float x, float top) {
     return min(max((int)(bits_of(d) >> 16) - ((127 - 4) << 7), 0), NB - 1);
 }
 
+// v of the lane that a DPP control names; 0 where it names none.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ unsigned from_lane(unsigned v) {
+    return (unsigned)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, false);
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ u64 from_lane(u64 v) {
+    return (u64)from_lane<CTRL, ROWS>((unsigned)v) | ((u64)from_lane<CTRL, ROWS>((unsigned)(v >> 32)) << 32);
+}
+
+// Sum over the wave's lanes up to this one: within rows of 16 lanes (shifts by
+// 1, 2, 4, 8), then each row's last lane into the rows behind.
+template <typename T>
+__device__ __forceinline__ T scan_wave(T v) {
+    v += from_lane<0x111, 0xF>(v);
+    v += from_lane<0x112, 0xF>(v);
+    v += from_lane<0x114, 0xF>(v);
+    v += from_lane<0x118, 0xF>(v);
+    v += from_lane<0x142, 0xA>(v);
+    v += from_lane<0x143, 0xC>(v);
+    return v;
+}
+
 // Sum over the workgroup's threads before this one, and over all.
 template <typename T>
 __device__ __forceinline__ T scan_before(T v, T *waves, T &total) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    T upto = v;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const T u = __shfl_up(upto, d);
-        if (lane >= d) upto += u;
-    }
+    const T upto = scan_wave(v);
     __syncthreads();
     if (lane == 63) waves[wave] = upto;
     __syncthreads();
@@ -169,24 +187,27 @@ __device__ __forceinline__ T scan_before(T v, T *waves, T &total) {
 }
 
 __device__ __forceinline__ u64 sum_all(u64 v, u64 *waves) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-#pragma unroll
-    for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
-    __syncthreads();
-    if (lane == 0) waves[wave] = v;
-    __syncthreads();
-    u64 total = 0;
-#pragma unroll
-    for (int w = 0; w < W; ++w) total += waves[w];
+    u64 total;
+    scan_before(v, waves, total);
     return total;
+}
+
+template <int CTRL>
+__device__ __forceinline__ float max_lane(float v) {
+    const int u = (int)bits_of(v);
+    return fmaxf(v, f32_of((unsigned)__builtin_amdgcn_update_dpp(u, u, CTRL, 0xF, 0xF, false)));
 }
 
 __device__ __forceinline__ float max_all(float v, float *waves) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-#pragma unroll
-    for (int d = 32; d; d >>= 1) v = fmaxf(v, __shfl_xor(v, d));
+    v = max_lane<0x111>(v);
+    v = max_lane<0x112>(v);
+    v = max_lane<0x114>(v);
+    v = max_lane<0x118>(v);
+    v = max_lane<0x142>(v);
+    v = max_lane<0x143>(v);  // lane 63 has the wave's
     __syncthreads();
-    if (lane == 0) waves[wave] = v;
+    if (lane == 63) waves[wave] = v;
     __syncthreads();
     v = waves[0];
 #pragma unroll
@@ -240,15 +261,16 @@ __global__ void __launch_bounds__(TH) sample_bins_kernel(SampleArgs a) {
     __shared__ unsigned counts[NB];
     const int c = blockIdx.x % a.chunks, m = blockIdx.x / a.chunks, tid = threadIdx.x;
     const Ask q = ask_of(a, m);
-    if (q.greedy) return;
+    if (!a.few && q.greedy) return;
     float x[E], mine;
     load_logits<F32>(a.logits, (int64_t)m * a.stride, c * SAMPLE_CHUNK + tid * E, a.V, x);
     make_powers(pow);
-    if (q.filters())
-        for (int i = tid; i < NB; i += TH) {
-            masses[i] = 0;
-            counts[i] = 0;
-        }
+#pragma unroll
+    for (int i = 0; i < NB / TH; ++i) {
+        masses[i * TH + tid] = 0;
+        counts[i * TH + tid] = 0;
+    }
+    if (q.greedy) return;
     const float top = top_of(a, m, mine, (float *)waves);
     if (!q.filters()) {
         u64 sum = 0;
@@ -257,8 +279,8 @@ __global__ void __launch_bounds__(TH) sample_bins_kernel(SampleArgs a) {
             const double v = weight(x[e], top, q.c, pow);
             sum += v >= q.minp ? mass_of(v) : 0;
         }
-        sum = sum_all(sum, waves);
-        if (tid == 0) a.kept[(size_t)m * a.chunks + c] = sum;
+        sum = scan_wave(sum);
+        if ((tid & 63) == 63) a.kept[((size_t)m * a.chunks + c) * SAMPLE_SUBS + tid / 64] = sum;
         return;
     }
 #pragma unroll
@@ -270,9 +292,17 @@ __global__ void __launch_bounds__(TH) sample_bins_kernel(SampleArgs a) {
         }
     }
     __syncthreads();
-    for (int i = tid; i < NB; i += TH) {
-        if (counts[i]) atomicAdd(&a.counts[(size_t)m * NB + i], counts[i]);
-        if (masses[i]) atomicAdd(&a.masses[(size_t)m * NB + i], masses[i]);
+    unsigned n[NB / TH];
+    u64 w[NB / TH];
+#pragma unroll
+    for (int i = 0; i < NB / TH; ++i) {
+        n[i] = counts[i * TH + tid];
+        w[i] = masses[i * TH + tid];
+    }
+#pragma unroll
+    for (int i = 0; i < NB / TH; ++i) {
+        if (n[i]) atomicAdd(&a.counts[(size_t)m * NB + i * TH + tid], n[i]);
+        if (w[i]) atomicAdd(&a.masses[(size_t)m * NB + i * TH + tid], w[i]);
     }
 }
 
@@ -288,9 +318,10 @@ struct Shared {
     };
     u64 found64[2];
     unsigned found32[4];
-    u64 mass[TH];  // by digit, then by chunk
-    unsigned count[TH];
+    u64 mass[TH * SAMPLE_SUBS];  // by digit, then by part of a chunk
+    unsigned count[TH * SAMPLE_SUBS];
 };
+constexpr int SUB = SAMPLE_CHUNK / SAMPLE_SUBS;  // tokens of a part
 
 // A row's cut in terms of its undecided tokens: those of larger keys are kept,
 // and of this key the first `ties` as far as `token`.
@@ -303,15 +334,18 @@ __device__ __forceinline__ bool undecided(const SampleRow &r, int b) {
     return (b >= r.p_lo && b <= r.p_hi) || b == r.k_bin;
 }
 
-// The token, from the chunks' kept masses (`mine`: of chunk tid) and, where
-// there are filters (`row`), their numbers of the cut key's tokens
-// (`ties_before`: before chunk tid).
+// The token, from the kept masses of the chunks' parts (`mine`: of chunk tid)
+// and, where there are filters (`row`), their numbers of the cut key's tokens
+// (`ties`; `ties_before`: before chunk tid).
 template <bool F32>
-__device__ __forceinline__ void pick(const SampleArgs &a, int m, const Ask &q, float top, u64 mine, const SampleRow *row, Cut cut,
-                                     unsigned ties_before, Shared &sh) {
+__device__ __forceinline__ void pick(const SampleArgs &a, int m, const Ask &q, float top, const u64 (&mine)[SAMPLE_SUBS], const SampleRow *row,
+                                     Cut cut, const unsigned *ties, unsigned ties_before, Shared &sh) {
+    constexpr int PE = SUB / TH;
     const int tid = threadIdx.x;
-    u64 total;
-    const u64 before = scan_before(mine, sh.wave64, total);
+    u64 total, sum = 0;
+#pragma unroll
+    for (int i = 0; i < SAMPLE_SUBS; ++i) sum += mine[i];
+    u64 before = scan_before(sum, sh.wave64, total);
     if (total == 0) {  // (only -infinities and NaN)
         if (tid == 0) {
             a.tokens[m] = -1;
@@ -322,30 +356,37 @@ __device__ __forceinline__ void pick(const SampleArgs &a, int m, const Ask &q, f
     const double u = (double)a.u[m];
     u64 r = u > 0.0 ? (u64)(fmin(u, 1.0) * (double)total) : 0;
     r = r < total ? r : total - 1;
-    if (mine > 0 && r >= before && r - before < mine) {
-        sh.found32[0] = (unsigned)tid;
-        sh.found32[1] = ties_before;
-        sh.found64[0] = r - before;
+    const bool by_ties = row && ties;
+#pragma unroll
+    for (int i = 0; i < SAMPLE_SUBS; ++i) {
+        if (mine[i] > 0 && r >= before && r - before < mine[i]) {
+            sh.found32[0] = (unsigned)(tid * SAMPLE_SUBS + i);
+            sh.found32[1] = ties_before;
+            sh.found64[0] = r - before;
+        }
+        before += mine[i];
+        if (by_ties) ties_before += ties[i];
     }
     __syncthreads();
-    const int at = (int)sh.found32[0] * SAMPLE_CHUNK + tid * E;
+    const int at = (int)sh.found32[0] * SUB + tid * PE;
     r = sh.found64[0];
-    float x[E];
+    float x[PE];
     load_logits<F32>(a.logits, (int64_t)m * a.stride, at, a.V, x);
     unsigned place = 0;  // of this thread's first token of the cut key among all
-    const bool by_ties = row && cut.ties != ~0u;
     if (by_ties) {
         unsigned n = 0, all;
 #pragma unroll
-        for (int e = 0; e < E; ++e) n += x[e] == x[e] && key_of(x[e]) == cut.key && undecided(*row, bin_of(x[e], top));
+        for (int e = 0; e < PE; ++e) n += x[e] == x[e] && key_of(x[e]) == cut.key && undecided(*row, bin_of(x[e], top));
         place = sh.found32[1];
         place += scan_before(n, sh.wave32, all);
     }
-    u64 w[E], sum = 0;
+    u64 w[PE];
+    double v[PE];
+    sum = 0;
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-        const double v = weight(x[e], top, q.c, sh.pow);
-        bool keep = v >= q.minp;
+    for (int e = 0; e < PE; ++e) {
+        v[e] = weight(x[e], top, q.c, sh.pow);
+        bool keep = v[e] >= q.minp;
         if (row && x[e] == x[e]) {
             const int b = bin_of(x[e], top);
             const unsigned key = key_of(x[e]);
@@ -357,18 +398,31 @@ __device__ __forceinline__ void pick(const SampleArgs &a, int m, const Ask &q, f
                 keep &= b < row->full;
             }
         }
-        w[e] = keep && x[e] == x[e] ? mass_of(v) : 0;
+        w[e] = keep && x[e] == x[e] ? mass_of(v[e]) : 0;
         sum += w[e];
     }
     u64 from = scan_before(sum, sh.wave64, sum);
+    int hit = -1;
+    double share = 0.0;
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
+    for (int e = 0; e < PE; ++e) {
         if (w[e] > 0 && r >= from && r - from < w[e]) {
-            a.tokens[m] = at + e;
-            if (a.logprobs) a.logprobs[m] = (float)log(weight(x[e], top, q.c, sh.pow) / ((double)total * (1.0 / UNIT)));
+            hit = at + e;
+            share = v[e];
         }
         from += w[e];
     }
+    if (hit >= 0) {
+        a.tokens[m] = hit;
+        if (a.logprobs) a.logprobs[m] = (float)log(share / ((double)total * (1.0 / UNIT)));
+    }
+}
+
+// The kept masses of chunk tid's parts.
+__device__ __forceinline__ void load_kept(const SampleArgs &a, int m, bool there, u64 (&kept)[SAMPLE_SUBS]) {
+#pragma unroll
+    for (int i = 0; i < SAMPLE_SUBS; ++i)
+        kept[i] = there && (int)threadIdx.x < a.chunks ? a.kept[((size_t)m * a.chunks + threadIdx.x) * SAMPLE_SUBS + i] : 0;
 }
 
 template <bool F32>
@@ -390,7 +444,8 @@ __global__ void __launch_bounds__(TH) sample_find_kernel(SampleArgs a) {
             n += count[i];
         }
     }
-    const u64 kept = !q.greedy && !filters && tid < a.chunks ? a.kept[(size_t)m * a.chunks + tid] : 0;
+    u64 kept[SAMPLE_SUBS];
+    load_kept(a, m, !q.greedy && !filters, kept);
     make_powers(sh.pow);
     float mine;
     const float top = top_of(a, m, mine, sh.wavef);
@@ -402,7 +457,9 @@ __global__ void __launch_bounds__(TH) sample_find_kernel(SampleArgs a) {
         }
         __syncthreads();
         if (!q.greedy) {
-            pick<F32>(a, m, q, top, none ? 0 : kept, nullptr, Cut{0, 0, 0}, 0, sh);
+            if (none)
+                for (u64 &k : kept) k = 0;
+            pick<F32>(a, m, q, top, kept, nullptr, Cut{0, 0, 0}, nullptr, 0, sh);
             return;
         }
         if (tid < a.chunks && mine == top) atomicMin(&sh.found32[0], (unsigned)a.top_at[(size_t)m * a.chunks + tid]);
@@ -484,11 +541,12 @@ __global__ void __launch_bounds__(TH) sample_list_kernel(SampleArgs a) {
     __shared__ unsigned first;
     const int c = blockIdx.x % a.chunks, m = blockIdx.x / a.chunks, tid = threadIdx.x;
     const SampleRow r = a.rows[m];
-    if (r.done) return;
+    if (!a.few && r.done) return;
     const Ask q = ask_of(a, m);
     float x[E], mine;
     load_logits<F32>(a.logits, (int64_t)m * a.stride, c * SAMPLE_CHUNK + tid * E, a.V, x);
     make_powers(pow);
+    if (r.done) return;
     const float top = top_of(a, m, mine, (float *)waves);
     u64 sum = 0;
     unsigned open = 0, n = 0;
@@ -504,11 +562,11 @@ __global__ void __launch_bounds__(TH) sample_list_kernel(SampleArgs a) {
             ++n;
         }
     }
-    sum = sum_all(sum, waves);
+    sum = scan_wave(sum);
+    if ((tid & 63) == 63) a.kept[((size_t)m * a.chunks + c) * SAMPLE_SUBS + tid / 64] = sum;
     unsigned all;
     unsigned place = scan_before(n, (unsigned *)waves, all);
     if (tid == 0) {
-        a.kept[(size_t)m * a.chunks + c] = sum;
         // (chunks come in any order: what is made of the list does not depend on it)
         if (all > 0) first = atomicAdd(&a.rows[m].listed, all);
     }
@@ -545,7 +603,8 @@ __global__ void __launch_bounds__(TH) sample_pick_kernel(SampleArgs a) {
 #pragma unroll 8
         for (unsigned i = tid; i < r.listed; i += TH) ls.list[i] = list[i];
     }
-    u64 kept = tid < a.chunks ? a.kept[(size_t)m * a.chunks + tid] : 0;
+    u64 kept[SAMPLE_SUBS];
+    load_kept(a, m, true, kept);
     make_powers(sh.pow);
     float mine;
     const float top = top_of(a, m, mine, sh.wavef);
@@ -576,27 +635,29 @@ __global__ void __launch_bounds__(TH) sample_pick_kernel(SampleArgs a) {
             keep &= b <= r.p_hi && before < max((u64)ceil(q.p * (double)mass), (u64)1);
         }
         __syncthreads();
-        sh.mass[tid] = 0;
+#pragma unroll
+        for (int i = 0; i < SAMPLE_SUBS; ++i) sh.mass[i * TH + tid] = 0;
         __syncthreads();
         // kept is what comes first, as far as the last of them
         u64 last = keep ? order : ~0ull;
 #pragma unroll
         for (int d = 32; d; d >>= 1) last = min(last, (u64)__shfl_xor(last, d));
         if ((tid & 63) == 0) atomicMin(&sh.found64[0], last);
-        if (keep && v >= q.minp) atomicAdd(&sh.mass[own[1] / SAMPLE_CHUNK], w);
+        if (keep && v >= q.minp) atomicAdd(&sh.mass[own[1] / SUB], w);
         __syncthreads();
         last = sh.found64[0];
-        if (tid < a.chunks) kept += sh.mass[tid];
-        pick<F32>(a, m, q, top, kept, &r, Cut{(unsigned)(last >> 32), ~(unsigned)last, ~0u}, 0, sh);
+#pragma unroll
+        for (int i = 0; i < SAMPLE_SUBS; ++i) kept[i] += sh.mass[tid * SAMPLE_SUBS + i];
+        pick<F32>(a, m, q, top, kept, &r, Cut{(unsigned)(last >> 32), ~(unsigned)last, ~0u}, nullptr, 0, sh);
         return;
     }
 
-    // f(key, bin, chunk) for each undecided token
+    // f(key, bin, part) for each undecided token
     const auto each = [&](auto f) {
         if (r.listed <= SAMPLE_LIST) {
             for (unsigned i = tid; i < r.listed; i += TH) {
                 const u32x2_t t = ls.list[i];
-                f(t[0], bin_of(logit_of(t[0]), top), (int)(t[1] / SAMPLE_CHUNK));
+                f(t[0], bin_of(logit_of(t[0]), top), (int)(t[1] / SUB));
             }
         } else {  // more than the list holds: from the logits again
             for (int i = tid; i < a.V; i += TH) {
@@ -604,7 +665,7 @@ __global__ void __launch_bounds__(TH) sample_pick_kernel(SampleArgs a) {
                 const float x = F32 ? ((const float *)a.logits)[at] : f32_of((unsigned)((const uint16_t *)a.logits)[at] << 16);
                 if (!(x == x)) continue;
                 const int b = bin_of(x, top);
-                if (undecided(r, b)) f(key_of(x), b, i / SAMPLE_CHUNK);
+                if (undecided(r, b)) f(key_of(x), b, i / SUB);
             }
         }
     };
@@ -702,28 +763,35 @@ __global__ void __launch_bounds__(TH) sample_pick_kernel(SampleArgs a) {
     }
     // what the chunks keep of their undecided tokens: those above the cut ...
     __syncthreads();
-    sh.mass[tid] = 0;
-    sh.count[tid] = 0;
+#pragma unroll
+    for (int i = 0; i < SAMPLE_SUBS; ++i) {
+        sh.mass[i * TH + tid] = 0;
+        sh.count[i * TH + tid] = 0;
+    }
     __syncthreads();
-    each([&](unsigned key, int, int c) {
+    each([&](unsigned key, int, int part) {
         if (key > cut.key) {
             const double v = weight(logit_of(key), top, q.c, sh.pow);
-            if (v >= q.minp) atomicAdd(&sh.mass[c], mass_of(v));
+            if (v >= q.minp) atomicAdd(&sh.mass[part], mass_of(v));
         } else if (key == cut.key) {
-            atomicAdd(&sh.count[c], 1u);
+            atomicAdd(&sh.count[part], 1u);
         }
     });
     __syncthreads();
     // ... and of the cut's key, the first tokens of the row
-    const unsigned ties = sh.count[tid];
-    unsigned all;
-    const unsigned ties_before = scan_before(ties, sh.wave32, all);
-    if (tid < a.chunks) {
-        const unsigned take = min(ties, ties_before < cut.ties ? cut.ties - ties_before : 0u);
-        const double v = take ? weight(logit_of(cut.key), top, q.c, sh.pow) : 0.0;
-        kept += sh.mass[tid] + (take && v >= q.minp ? take * mass_of(v) : 0);
+    unsigned ties[SAMPLE_SUBS], n = 0, all;
+#pragma unroll
+    for (int i = 0; i < SAMPLE_SUBS; ++i) n += ties[i] = sh.count[tid * SAMPLE_SUBS + i];
+    const unsigned ties_before = scan_before(n, sh.wave32, all);
+    const double v = weight(logit_of(cut.key), top, q.c, sh.pow);
+    const u64 each_tie = v >= q.minp ? mass_of(v) : 0;
+    n = ties_before;
+#pragma unroll
+    for (int i = 0; i < SAMPLE_SUBS; ++i) {
+        kept[i] += sh.mass[tid * SAMPLE_SUBS + i] + min(ties[i], n < cut.ties ? cut.ties - n : 0u) * each_tie;
+        n += ties[i];
     }
-    pick<F32>(a, m, q, top, kept, &r, cut, ties_before, sh);
+    pick<F32>(a, m, q, top, kept, &r, cut, ties, ties_before, sh);
 }
 
 template <bool F32>
