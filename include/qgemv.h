@@ -710,6 +710,52 @@ int kv_attention_run(const qg_kv_cache *cache, int64_t R, int64_t M, int64_t Hq,
                      void *workspace, size_t workspace_bytes, void *out, int64_t out_stride,
                      int out_dtype, void *stream);
 
+/* Bytes of workspace kv_prefix_attention_run needs (0 for arguments it would
+ * refuse, and for R or M of 0). */
+size_t qg_kv_prefix_attention_workspace_bytes(int64_t R, int64_t M, int64_t Hq, int64_t Hkv, int64_t D,
+                                              int64_t page, int64_t max_q, int64_t max_len,
+                                              int64_t max_prefix);
+
+/*
+ * kv_prefix_attention_run -- kv_attention_run for requests that share a prefix
+ * (a system prompt, a document): every query token sees all of the prefix's
+ * tokens, and its own request's as in kv_attention_run, under one softmax.  The
+ * prefix is read once for all rows of the call instead of once for each
+ * request.
+ *
+ *  The prefix is kept like a request: pages of the same cache, listed in
+ *  prefix_table, prefix_len tokens (for kv_tables_run, a request of its own that
+ *  gets no query tokens).  lens and table hold the requests' own tokens only,
+ *  so position 0 of a request is the one behind the prefix.
+ *
+ *  prefix_table device int32 [prefix_blocks]; a page id outside [0, pages) is
+ *               not attended to.  prefix_blocks >= 1, * page <= 2^30.
+ *  prefix_len   device int32 [1]: the prefix's tokens, 0 or more.
+ *  max_prefix   0..prefix_blocks * page: the prefix is not longer; if it is,
+ *               all rows become NaN.
+ *  tree_mask    as in kv_attention_run (over the request's own tokens).
+ *  workspace    device buffer, 16-B, of qg_kv_prefix_attention_workspace_bytes,
+ *               always.  Scratch: calls that may overlap, or graphs that may
+ *               run at once, need one each.
+ *  M            rows of q and out; M * Hq <= 2^26 - 8.  q_start[0] to q_start[R]
+ *               are the rows held against the prefix; the others are left as
+ *               they are.
+ *  other arguments, rounding and limits as in kv_attention_run, without window:
+ *               a part in the sense of its value scales is also a part of the
+ *               prefix.  (The products of row groups, heads and tokens / 32, of
+ *               the requests and of the prefix, have to stay below 2^31:
+ *               QG_ESHAPE.)  A row that sees nothing is 0.
+ * Errors: QG_EINVAL, QG_ESHAPE, QG_EALIGN, QG_ESIZE, QG_EUNSUPPORTED
+ * (QG_OUT_I32_GROUPS), QG_EHIP.
+ */
+int kv_prefix_attention_run(const qg_kv_cache *cache, int64_t R, int64_t M, int64_t Hq, const void *q,
+                            int64_t q_stride, const int32_t *q_start, const int32_t *lens,
+                            const int32_t *table, int64_t max_blocks, const int32_t *prefix_table,
+                            int64_t prefix_blocks, const int32_t *prefix_len,
+                            const uint32_t *tree_mask, float scale, int64_t max_q, int64_t max_len,
+                            int64_t max_prefix, void *workspace, size_t workspace_bytes, void *out,
+                            int64_t out_stride, int out_dtype, void *stream);
+
 /* Bytes of workspace sample_run needs (0 for arguments it would refuse). */
 size_t qg_sample_workspace_bytes(int64_t M, int64_t V);
 

@@ -13,7 +13,8 @@ from ._lib import (  # noqa: F401
     qgemm_skinny_run, qgemv_pack, qgemv_run, raw, status_string, qg_batch_plan_build,
     qg_batch_run, qg_batch_worklist_bytes, qg_plain_read, GemvDesc, BatchPlan, Plan,
     KV_INT8, KV_E4M3, KVCache, CacheDesc, rmsnorm_quant_run, qk_norm_rope_run, kv_tables_run, kv_append_run,
-    kv_attention_run, kv_attention_workspace_bytes, sample_run, sample_workspace_bytes,
+    kv_attention_run, kv_attention_workspace_bytes, kv_prefix_attention_run,
+    kv_prefix_attention_workspace_bytes, sample_run, sample_workspace_bytes,
 )
 
 __version__ = "0.1.0"

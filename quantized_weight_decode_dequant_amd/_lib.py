@@ -70,6 +70,8 @@ EXPORTS = (
     "kv_append_run",
     "qg_kv_attention_workspace_bytes",
     "kv_attention_run",
+    "qg_kv_prefix_attention_workspace_bytes",
+    "kv_prefix_attention_run",
     "qg_sample_workspace_bytes",
     "sample_run",
 )
@@ -167,6 +169,11 @@ def raw():
             lib.kv_attention_run.argtypes = [p, i64, i64, i64, p, i64, p, p, p, i64, p, i64,
                                              C.c_float, i64, i64, p, sz, p, i64, i, p]
             lib.kv_attention_run.restype = i
+            lib.qg_kv_prefix_attention_workspace_bytes.argtypes = [i64] * 9
+            lib.qg_kv_prefix_attention_workspace_bytes.restype = sz
+            lib.kv_prefix_attention_run.argtypes = [p, i64, i64, i64, p, i64, p, p, p, i64, p, i64, p, p, C.c_float,
+                                                    i64, i64, i64, p, sz, p, i64, i, p]
+            lib.kv_prefix_attention_run.restype = i
             lib.qg_sample_workspace_bytes.argtypes = [i64, i64]
             lib.qg_sample_workspace_bytes.restype = sz
             lib.sample_run.argtypes = [p, i, i64, i64, i64, p, p, p, p, p, p, sz, p, p, p]
@@ -673,6 +680,54 @@ def kv_attention_run(cache: KVCache, q, q_start, lens, table, max_q: int, max_le
           scale if scale is not None else D ** -0.5, max_q, max_len,
           _arg(workspace, workspace.dtype, workspace.shape, dev, "workspace") if nbytes else None, nbytes,
           op, os_, out_dtype)
+    return out
+
+
+def kv_prefix_attention_workspace_bytes(R: int, M: int, Hq: int, Hkv: int, D: int, page: int, max_q: int,
+                                        max_len: int, max_prefix: int) -> int:
+    return raw().qg_kv_prefix_attention_workspace_bytes(R, M, Hq, Hkv, D, page, max_q, max_len, max_prefix)
+
+
+def kv_prefix_attention_run(cache: KVCache, q, q_start, lens, table, prefix_table, prefix_len, max_q: int,
+                            max_len=None, max_prefix=None, tree_mask=None, scale=None, workspace=None, out=None,
+                            out_dtype: int = OUT_BF16, stream=None):
+    """kv_attention_run behind a prefix that all requests share: prefix_table
+    int32 [blocks] and prefix_len int32 [1] (its tokens); lens and table are
+    the requests' own tokens behind it.  max_prefix: the most tokens of the
+    prefix (its table's width by default).  Returns out [M, Hq, D]."""
+    torch = _torch()
+    i32 = torch.int32
+    if q.dim() != 3 or table.dim() != 2 or prefix_table.dim() != 1:
+        raise ValueError("q must be [M, Hq, D], table [R, max_blocks] and prefix_table [blocks]")
+    M, Hq, D = q.shape
+    R, nb = table.shape
+    pb = prefix_table.shape[0]
+    if max_len is None:
+        max_len = nb * cache.page
+    if max_prefix is None:
+        max_prefix = pb * cache.page
+    if out is None:
+        out = _empty((M, Hq, D), _out_torch_dtype(out_dtype), q.device, stream)
+    else:
+        out_dtype = _float_type(out, "out")
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    if M == 0 or R == 0:
+        return out
+    dev, D = cache.device, cache.D
+    qp, qs = _rows(q, Hq, D, torch.bfloat16, dev, "q")
+    op, os_ = _rows(out, Hq, D, out.dtype, dev, "out")
+    lib = raw()
+    if workspace is None:
+        nbytes = lib.qg_kv_prefix_attention_workspace_bytes(R, M, Hq, cache.Hkv, D, cache.page, max_q, max_len, max_prefix)
+        workspace = _empty(max(nbytes, 16), torch.uint8, q.device, stream)
+    nbytes = workspace.numel() * workspace.element_size()
+    _call(dev, stream, "kv_prefix_attention_run", lib.kv_prefix_attention_run, cache._ref, R, M, Hq, qp, qs,
+          _arg(q_start, i32, (R + 1,), dev, "q_start"), _arg(lens, i32, (R,), dev, "lens"),
+          _arg(table, i32, (R, nb), dev, "table"), nb, _arg(prefix_table, i32, (pb,), dev, "prefix_table"), pb,
+          _arg(prefix_len, i32, (1,), dev, "prefix_len"), _arg(tree_mask, i32, (M,), dev, "tree_mask"),
+          scale if scale is not None else D ** -0.5, max_q, max_len, max_prefix,
+          _arg(workspace, workspace.dtype, workspace.shape, dev, "workspace"), nbytes, op, os_, out_dtype)
     return out
 
 

@@ -92,6 +92,16 @@ bool attention_plan(int64_t R, int64_t M, int64_t Hq, int64_t Hkv, int64_t D, in
     return true;
 }
 
+// the same behind a shared prefix
+bool prefix_plan(int64_t R, int64_t M, int64_t Hq, int64_t Hkv, int64_t D, int64_t page, int64_t max_q,
+                 int64_t max_len, int64_t max_prefix, KvPrefixPlan *p) {
+    if (R < 0 || R > KV_R_MAX || M < 0 || Hkv < 1 || Hkv > 1024 || Hq < 1 || Hq > 8192 || Hq % Hkv ||
+        M > JOINS_MAX / Hq || !head_size(D) || !page_size(page) || max_q < 1 || max_q > KV_ROWS_MAX ||
+        max_len < 1 || max_len > LEN_MAX || max_prefix < 0 || max_prefix > LEN_MAX || R * max_q * Hq > JOINS_MAX)
+        return false;
+    return kv_prefix_plan(R, M, Hkv, Hq / Hkv, D, max_q, max_len, max_prefix, p);
+}
+
 }  // namespace
 
 extern "C" {
@@ -290,7 +300,7 @@ int kv_attention_run(const qg_kv_cache *cache, int64_t R, int64_t M, int64_t Hq,
             !aligned(tree_mask, 4) || !aligned(workspace, 16) || !aligned(out, 16))
             return QG_EALIGN;
         if (R == 0 || M == 0) return QG_OK;
-        KvAttnArgs a;
+        KvAttnArgs a{};
         a.k = reinterpret_cast<const uint8_t *>(cache->k);
         a.v = reinterpret_cast<const uint8_t *>(cache->v);
         a.k_scales = cache->k_scales;
@@ -331,7 +341,96 @@ int kv_attention_run(const qg_kv_cache *cache, int64_t R, int64_t M, int64_t Hq,
     } catch (...) {
         return QG_EINTERNAL;
     }
+}size_t qg_kv_prefix_attention_workspace_bytes(int64_t R, int64_t M, int64_t Hq, int64_t Hkv, int64_t D,
+                                              int64_t page, int64_t max_q, int64_t max_len,
+                                              int64_t max_prefix) {
+    KvPrefixPlan p;
+    return prefix_plan(R, M, Hq, Hkv, D, page, max_q, max_len, max_prefix, &p) && R > 0 && M > 0 ? p.bytes : 0;
 }
+
+int kv_prefix_attention_run(const qg_kv_cache *cache, int64_t R, int64_t M, int64_t Hq, const void *q,
+                            int64_t q_stride, const int32_t *q_start, const int32_t *lens,
+                            const int32_t *table, int64_t max_blocks, const int32_t *prefix_table,
+                            int64_t prefix_blocks, const int32_t *prefix_len,
+                            const uint32_t *tree_mask, float scale, int64_t max_q, int64_t max_len,
+                            int64_t max_prefix, void *workspace, size_t workspace_bytes, void *out,
+                            int64_t out_stride, int out_dtype, void *stream) {
+    try {
+        if (out_dtype != QG_OUT_BF16 && out_dtype != QG_OUT_F32 && out_dtype != QG_OUT_I32_GROUPS)
+            return QG_EINVAL;
+        if (out_dtype == QG_OUT_I32_GROUPS) return QG_EUNSUPPORTED;
+        const int st = check_cache(cache);
+        if (st != QG_OK) return st;
+        KvPrefixPlan p;
+        if (max_blocks < 1 || max_blocks > LEN_MAX / cache->page || max_len > max_blocks * cache->page ||
+            prefix_blocks < 1 || prefix_blocks > LEN_MAX / cache->page || max_prefix > prefix_blocks * cache->page ||
+            !prefix_plan(R, M, Hq, cache->Hkv, cache->D, cache->page, max_q, max_len, max_prefix, &p) ||
+            !row_stride(q_stride, Hq * cache->D) || !row_stride(out_stride, Hq * cache->D))
+            return QG_ESHAPE;
+        const float scale2 = scale * 1.44269504088896340736f;  // scores in powers of two
+        if (!std::isfinite(scale2)) return QG_EINVAL;
+        const bool none = R == 0 || M == 0;
+        if (!q || !q_start || !lens || !table || !prefix_table || !prefix_len || !out || (!none && !workspace))
+            return QG_EINVAL;
+        if (!none && workspace_bytes < p.bytes) return QG_ESIZE;
+        if (!aligned(q, 16) || !aligned(q_start, 4) || !aligned(lens, 4) || !aligned(table, 4) || !aligned(prefix_table, 4) ||
+            !aligned(prefix_len, 4) || !aligned(tree_mask, 4) || !aligned(workspace, 16) || !aligned(out, 16))
+            return QG_EALIGN;
+        if (none) return QG_OK;
+        KvAttnArgs a{};
+        a.k = reinterpret_cast<const uint8_t *>(cache->k);
+        a.v = reinterpret_cast<const uint8_t *>(cache->v);
+        a.k_scales = cache->k_scales;
+        a.v_scales = cache->v_scales;
+        a.q = reinterpret_cast<const uint16_t *>(q);
+        a.q_start = q_start;
+        a.lens = lens;
+        a.table = table;
+        a.tree = tree_mask;
+        a.out = out;
+        a.q_stride = q_stride;
+        a.out_stride = out_stride;
+        a.pages = cache->pages;
+        a.R = (int)R;
+        a.M = (int)M;
+        a.Hq = (int)Hq;
+        a.Hkv = cache->Hkv;
+        a.G = (int)(Hq / cache->Hkv);
+        a.page = cache->page;
+        a.max_blocks = (int)max_blocks;
+        a.max_q = (int)max_q;
+        a.max_len = (int)max_len;
+        a.scale = scale2;
+        a.out_f32 = out_dtype == QG_OUT_F32;
+        a.prefix_table = prefix_table;
+        a.prefix_len = prefix_len;
+        a.prefix_blocks = (int)prefix_blocks;
+        a.max_prefix = (int)max_prefix;
+        a.starts = p.own_starts;
+        a.cuts = p.cuts;
+        uint8_t *w = reinterpret_cast<uint8_t *>(workspace);
+        const auto line = [&](const KvAttnPlan &l, size_t head, size_t part) {
+            KvAttnArgs b = a;
+            b.head = reinterpret_cast<int32_t *>(w + head);
+            b.part = reinterpret_cast<float *>(w + part);
+            b.part_ml = b.part + (size_t)l.part_slots * (size_t)l.part_rows * (size_t)cache->D;
+            b.groups = l.groups;
+            b.slots = l.slots;
+            b.min_run = l.min_run;
+            b.part_rows = l.part_rows;
+            b.part_slots = (int)l.part_slots;
+            b.aligned = l.aligned;
+            return b;
+        };
+        return hip_status(launch_kv_prefix_attention(line(p.own, 0, p.own_part), line(p.pre, (size_t)p.own.head_bytes, p.pre_part),
+                                                     p, cache->D, cache->fmt == QG_KV_E4M3,
+                                                     reinterpret_cast<hipStream_t>(stream)));
+    } catch (...) {
+        return QG_EINTERNAL;
+    }
+}
+
+
 
 size_t qg_sample_workspace_bytes(int64_t M, int64_t V) {
     SampleLayout l;

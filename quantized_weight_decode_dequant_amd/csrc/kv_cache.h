@@ -52,6 +52,11 @@ struct KvAttnArgs {
     bool whole, aligned;
     float scale;     // softmax scale * log2(e)
     bool out_f32;
+    // with a shared prefix
+    const int32_t *prefix_table, *prefix_len;
+    int prefix_blocks, max_prefix;
+    int starts;      // (entry, head, row group)s of the line at most
+    int cuts;        // parts that the prefix is cut into, where it is a line by itself
 };
 
 struct KvTablesArgs {
@@ -77,6 +82,20 @@ struct KvAttnPlan {
     bool whole;          // nothing is cut: a workgroup for each (request, head, row group)
 };
 bool kv_attention_plan(int64_t R, int64_t Hkv, int64_t G, int64_t D, int64_t max_q, int64_t seen, KvAttnPlan *p);
+
+// The same behind a shared prefix: the requests' line, and the prefix's, or
+// both as one.
+struct KvPrefixPlan {
+    KvAttnPlan own, pre;
+    int cuts;
+    int own_starts;
+    bool both;      // one line, `own`
+    size_t own_part, pre_part, bytes;  // where the workspace holds the segments
+};
+bool kv_prefix_plan(int64_t R, int64_t M, int64_t Hkv, int64_t G, int64_t D, int64_t max_q, int64_t max_len,
+                    int64_t max_prefix, KvPrefixPlan *p);
+hipError_t launch_kv_prefix_attention(const KvAttnArgs &own, const KvAttnArgs &pre, const KvPrefixPlan &p, int D, bool e4m3,
+                                      hipStream_t s);
 
 constexpr int KV_R_MAX = 4096;       // requests of a call
 

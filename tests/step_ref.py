@@ -63,3 +63,51 @@ def sample(x, u, T=None, k=None, p=None, minp=None):
         i = min(i, int(np.searchsorted(c, c[-1])))
         tokens[m], logp[m] = i, np.log(w[i] / c[-1])
     return tokens, logp, keeps
+
+
+def prefix_attention(k, v, ks, vs, e4m3, q, q_start, lens, table, prefix, prefix_len, tree=None, scale=None):
+    """(out, sum of p |v| / l, largest sum |q k| scale) as cache_ref.attention's,
+    with the `prefix_len` tokens of the pages `prefix` before each request's
+    own; rows of no request are NaN.  k, v: row-major codes (uint8)."""
+    pages, H, page, D = k.shape
+    M, Hq = q.shape[:2]
+    G = Hq // H
+    scale = D ** -0.5 if scale is None else scale
+    dec = e4m3_value if e4m3 else (lambda b: b.view(np.int8).astype(np.float64))
+    out, A, S = np.full((M, Hq, D), np.nan), np.zeros((M, Hq, D)), np.zeros((M, Hq))
+
+    def tokens(ids, n, h):
+        ids = [int(i) for i in ids[: -(-n // page)]]
+        if not ids:
+            return np.zeros((0, D)), np.zeros((0, D)), np.zeros(0, bool)
+        safe = [i if 0 <= i < pages else 0 for i in ids]
+        there = np.repeat([0 <= i < pages for i in ids], page)[:n]
+        return tuple((dec(np.ascontiguousarray(c[safe, h])) * sc[safe, h][:, None, None]).reshape(-1, D)[:n] for c, sc in ((k, ks), (v, vs))) + (there,)
+
+    for h in range(H):
+        pk, pv, pt = tokens(prefix, prefix_len, h)
+        for r in range(len(lens)):
+            a, b, n = int(q_start[r]), int(q_start[r + 1]), int(lens[r])
+            T = b - a
+            if T <= 0:
+                continue
+            ok, ov, ot = tokens(table[r], n, h)
+            K, V, there = np.concatenate([pk, ok]), np.concatenate([pv, ov]), np.concatenate([pt, ot])
+            new = np.arange(-len(pk), n) - (n - T)
+            see = np.zeros((T, len(new)), bool)
+            for j in range(T):
+                see[j] = new <= j if tree is None else (new < 0) | (((int(tree[a + j]) >> np.clip(new, 0, 31)) & 1) > 0)
+            see &= there
+            for i in range(h * G, (h + 1) * G):
+                with np.errstate(invalid="ignore"):
+                    s = np.where(see, scale * (q[a:b, i] @ K.T), -np.inf)
+                    big = np.where(see, abs(scale) * (np.abs(q[a:b, i]) @ np.abs(K).T), 0.0)
+                top = s.max(1, keepdims=True) if s.shape[1] else np.full((T, 1), -np.inf)
+                p = np.where(see, np.exp(s - np.where(top == -np.inf, 0.0, top)), 0.0)
+                l = p.sum(1, keepdims=True)
+                some = l > 0
+                Vz = np.where(there[:, None], V, 0.0)
+                out[a:b, i] = np.where(some, p @ Vz / np.where(some, l, 1.0), 0.0)
+                A[a:b, i] = np.where(some, p @ np.abs(Vz) / np.where(some, l, 1.0), 0.0)
+                S[a:b, i] = big.max(1) if big.shape[1] else 0.0
+    return out, A, S
