@@ -171,8 +171,7 @@ __device__ __forceinline__ void load_codes(u32x4_t (&to)[N], const uint8_t *bloc
                                                 r, 16 * lane, (int)at + u * 1024, NT ? 2 : 0));
 }
 
-// CONV: the waves that share a step's codes through LDS put them there as f16.
-template <bool E4M3, int D, int NR, int RS, int WAVES, KvMode MODE = KV_PLAIN, bool CONV = false>
+template <bool E4M3, int D, int NR, int RS, int WAVES, KvMode MODE = KV_PLAIN>
 __global__ void __launch_bounds__(WAVES * 64, NR == 1 && D <= 128 && WAVES == 4 ? 3 : 2) kv_attn_kernel(KvAttnArgs) {
     constexpr int TS = WAVES / RS;      // waves that split the tokens
     constexpr int KS = D / 32;          // MFMA steps of Q K^T
@@ -185,9 +184,7 @@ __global__ void __launch_bounds__(WAVES * 64, NR == 1 && D <= 128 && WAVES == 4 
     // past the caches.
     constexpr bool SHARED = RS > 1;
     constexpr int PART = 2 * KB / RS;   // kilobytes each of them brings
-    constexpr int WIDE = CONV ? 2 : 1;  // kilobytes in LDS of one of codes
-    constexpr int STAGE = SHARED ? 2 * TS * 2 * KB * 64 * WIDE : 0;
-    static_assert(!CONV || SHARED, "a wave alone converts in its registers");
+    constexpr int STAGE = SHARED ? 2 * TS * 2 * KB * 64 : 0;
     constexpr int JOIN = TS > 1 ? (TS / 2) * RS * NR * SL * 16 : 0;
     __shared__ u32x4_t lds[STAGE > JOIN ? STAGE : JOIN > 0 ? JOIN : 1];
 
@@ -392,22 +389,6 @@ __global__ void __launch_bounds__(WAVES * 64, NR == 1 && D <= 128 && WAVES == 4 
     const f16x8_t ones = {(_Float16)1.f, (_Float16)1.f, (_Float16)1.f, (_Float16)1.f,
                           (_Float16)1.f, (_Float16)1.f, (_Float16)1.f, (_Float16)1.f};
 
-    // Masks for the values' codes of the step at t0: codes of slots behind the
-    // last token may be anything (an E4M3 NaN), and those of a page without a
-    // value scale are worth nothing.  `last`: the step may hold such slots.
-    const auto values_kept = [&](int t0, bool last, unsigned(&keep)[2]) {
-        const bool no_v = !(readlane_f(my_vs, (t0 >> shift) - page0) > 0.f);
-        keep[0] = keep[1] = ~0u;
-        if (no_v || (last && t0 + KV_STEP > rq.len)) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                keep[i] = 0u;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) keep[i] |= ((t0 + 16 * i + 4 * g + e < rq.len) & !no_v) ? 0xFFu << (8 * e) : 0u;
-            }
-        }
-    };
-
     // One step; MASK: some row may not see some of its tokens.  A wave alone
     // replaces its keys by the next step's once they are used, then its values: one buffer each, with loads in flight all the
     // time.  `buf`: where the shared codes lie.
@@ -417,6 +398,7 @@ __global__ void __launch_bounds__(WAVES * 64, NR == 1 && D <= 128 && WAVES == 4 
         const bool there = page_at(t0) >= 0;
         const int pi = (t0 >> shift) - page0;
         const float ks = readlane_f(my_ks, pi), lr = readlane_f(my_lr, pi), rr = readlane_f(my_rr, pi);
+        const bool no_v = !(readlane_f(my_vs, pi) > 0.f);
         // scores
         f32x4_t s[NR][2];
 #pragma unroll
@@ -428,13 +410,8 @@ __global__ void __launch_bounds__(WAVES * 64, NR == 1 && D <= 128 && WAVES == 4 
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int kb = i * (D / 64) + (k >> 1);
-                f16x8_t kf;
-                if constexpr (CONV) {
-                    kf = __builtin_bit_cast(f16x8_t, buf[(2 * kb + (k & 1)) * 64 + lane]);
-                } else {
-                    const u32x4_t w = SHARED ? buf[kb * 64 + lane] : kw[SHARED ? 0 : kb];
-                    kf = codes8<E4M3>(w[2 * (k & 1)], w[2 * (k & 1) + 1]);
-                }
+                const u32x4_t w = SHARED ? buf[kb * 64 + lane] : kw[SHARED ? 0 : kb];
+                const f16x8_t kf = codes8<E4M3>(w[2 * (k & 1)], w[2 * (k & 1) + 1]);
 #pragma unroll
                 for (int n = 0; n < NR; ++n)
                     s[n][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[n][k], s[n][i], 0, 0, 0);
@@ -442,8 +419,17 @@ __global__ void __launch_bounds__(WAVES * 64, NR == 1 && D <= 128 && WAVES == 4 
             if (k & 1) __builtin_amdgcn_sched_barrier(0);
         }
         if constexpr (!SHARED) load(kw, a.k, t0 + STRIDE, 0);
-        unsigned keep[2];
-        if constexpr (!CONV) values_kept(t0, MASK, keep);
+        // codes of slots behind the last token may be anything (an E4M3 NaN),
+        // and those of a page without a value scale are worth nothing
+        unsigned keep[2] = {~0u, ~0u};
+        if (no_v || (MASK && t0 + KV_STEP > rq.len)) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                keep[i] = 0u;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) keep[i] |= ((t0 + 16 * i + 4 * g + e < rq.len) & !no_v) ? 0xFFu << (8 * e) : 0u;
+            }
+        }
         const float off = there ? 0.f : NEG_INF;
         f16x8_t pf[NR];
 #pragma unroll
@@ -504,21 +490,14 @@ __global__ void __launch_bounds__(WAVES * 64, NR == 1 && D <= 128 && WAVES == 4 
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int u = 0; u < KB; ++u) {
-            u32x4_t w;
-            if constexpr (!CONV) {
-                w = SHARED ? buf[(KB + u) * 64 + lane] : vw[SHARED ? 0 : u];
-                w[0] &= keep[0];
-                w[1] &= keep[1];
-                w[2] &= keep[0];
-                w[3] &= keep[1];
-            }
+            u32x4_t w = SHARED ? buf[(KB + u) * 64 + lane] : vw[SHARED ? 0 : u];
+            w[0] &= keep[0];
+            w[1] &= keep[1];
+            w[2] &= keep[0];
+            w[3] &= keep[1];
 #pragma unroll
             for (int d = 0; d < 2; ++d) {
-                f16x8_t vf;
-                if constexpr (CONV)
-                    vf = __builtin_bit_cast(f16x8_t, buf[(2 * (KB + u) + d) * 64 + lane]);
-                else
-                    vf = codes8<E4M3>(w[2 * d], w[2 * d + 1]);
+                const f16x8_t vf = codes8<E4M3>(w[2 * d], w[2 * d + 1]);
 #pragma unroll
                 for (int n = 0; n < NR; ++n)
                     o[n][2 * u + d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, pf[n], o[n][2 * u + d], 0, 0, 0);
@@ -559,30 +538,14 @@ __global__ void __launch_bounds__(WAVES * 64, NR == 1 && D <= 128 && WAVES == 4 
             // LDS while the next one's loads run, and one barrier a step tells
             // that all parts are there (and that the step before the last is
             // used up)
-            u32x4_t *mine = lds + ((ts * 2 * KB + (st_v ? KB : 0)) * 64 + (st_skip / 16)) * WIDE + lane;
+            u32x4_t *mine = lds + (ts * 2 * KB + (st_v ? KB : 0)) * 64 + (st_skip / 16) + lane;
             const auto stage = [&](auto masked, u32x4_t(&st)[PART], int t, int b) {
-                u32x4_t *to = mine + b * (TS * 2 * KB * 64 * WIDE);
-                if constexpr (CONV) {
-                    if (st_v && t < t_hi) {
-                        unsigned keep[2];
-                        values_kept(t, decltype(masked)::value, keep);
+                u32x4_t *to = mine + b * (TS * 2 * KB * 64);
 #pragma unroll
-                        for (int u = 0; u < PART; ++u)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) st[u][e] &= keep[e & 1];
-                    }
-#pragma unroll
-                    for (int u = 0; u < PART; ++u) {
-                        to[2 * u * 64] = __builtin_bit_cast(u32x4_t, codes8<E4M3>(st[u][0], st[u][1]));
-                        to[(2 * u + 1) * 64] = __builtin_bit_cast(u32x4_t, codes8<E4M3>(st[u][2], st[u][3]));
-                    }
-                } else {
-#pragma unroll
-                    for (int u = 0; u < PART; ++u) to[u * 64] = st[u];
-                }
+                for (int u = 0; u < PART; ++u) to[u * 64] = st[u];
                 load(st, st_codes, t + 2 * STRIDE, st_skip);
                 __syncthreads();
-                if (t < t_hi) compute(masked, t, lds + (b * TS + ts) * 2 * KB * 64 * WIDE);
+                if (t < t_hi) compute(masked, t, lds + (b * TS + ts) * 2 * KB * 64);
             };
             int t0 = t_lo;
             for (; t0 + 2 * STRIDE <= t_clear; t0 += 2 * STRIDE) {

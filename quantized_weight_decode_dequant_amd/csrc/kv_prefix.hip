@@ -144,43 +144,338 @@ __global__ void __launch_bounds__(512) kv_prefix_join_kernel(KvPrefixJoinArgs p)
         *reinterpret_cast<u32x2_t *>((uint16_t *)a.out + to) = bf16x4(o);
 }
 
+// The prefix against many rows: a workgroup of WAVES waves takes 16 NR WAVES
+// rows of a KV head and one of the prefix's parts.  The waves convert a step's
+// codes (32 tokens) to f16 once for all of them, into LDS, keys one step ahead
+// of values: a step's scores are made by the matrix cores while the softmax of
+// the step before is on the vector unit.  Nothing is masked but what lies
+// behind the prefix's last token.
+constexpr int ROWS_PAGES = 512;  // pages whose scales are held at once
+
+template <bool E4M3, int D, int NR, int WAVES>
+__global__ void __launch_bounds__(WAVES * 64, 2) kv_prefix_rows_kernel(KvAttnArgs) {
+    constexpr int KS = D / 32, DT = D / 16, KB = D / 32, TH = WAVES * 64;
+    constexpr int PW = 2 * KB / WAVES;  // kilobytes of codes that a wave brings of a step
+    static_assert(PW >= 1 && PW * WAVES == 2 * KB, "half of the waves bring keys, half values");
+    constexpr float UNIT = Code<E4M3>::unit, BIAS = Code<E4M3>::bias;
+    __shared__ u32x4_t kbuf[2][2 * KB * 64], vbuf[2][2 * KB * 64];
+    __shared__ f32x4_t info[ROWS_PAGES];  // of a page: key scale, log2 of the value scale's part, its inverse, id
+    __shared__ float wmax[WAVES];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int g = lane >> 4, c = lane & 15;
+    constexpr int RW = 16 * NR * WAVES;
+    Args &a = args();
+    const Req rq = req_of<RW, KV_PREFIX>(a, 0);
+    const int rows = rq.T * a.G;
+    // heads fastest: the workgroups of a head, which read the same codes, run
+    // on one XCD where there are eight heads
+    const int h = blockIdx.x % a.Hkv, cut = blockIdx.x / a.Hkv % a.cuts, rg = blockIdx.x / a.Hkv / a.cuts;
+    const int len = (rq.units + a.cuts - 1) / a.cuts;
+    if (blockIdx.x == 0 && tid == 0) {
+        a.head[0] = len;
+        a.head[1] = 0;
+    }
+    if (rg >= rq.groups || cut * len >= rq.units) return;
+    const int shift = __builtin_ctz(a.page);
+    const int t_begin = cut * len * KV_STEP, t_end = rq.too_long ? 0 : min((cut + 1) * len * KV_STEP, rq.len);
+    const int row0 = rg * RW + 16 * NR * wave;
+
+    // Q, as f16 in the K tiles' order of dimensions
+    f16x8_t qf[NR][KS];
+    float cs[NR], k0[NR];  // factor and start of the scores
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+        const int row = row0 + 16 * n + c;
+        const bool valid = row < rows;
+        const int j = valid ? row / a.G : 0;
+        const int hq = h * a.G + (valid ? row - j * a.G : 0);
+        const uint16_t *q = a.q + (size_t)(rq.q0 + j) * a.q_stride + (size_t)hq * D;
+        u32x4_t w[KS];
+        float top = 0.f;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            w[s] = *reinterpret_cast<const u32x4_t *>(q + 64 * (s >> 1) + 16 * g + 8 * (s & 1));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const unsigned u = w[s][e];
+                top = fmaxf(top, fmaxf(fabsf(bf16_lo(u)), fabsf(bf16_hi(u))));
+            }
+        }
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        // the row's largest magnitude to [2^13, 2^14), the scale's sign with it
+        const int e2 = top > 0.f ? 13 - ((int)(__builtin_bit_cast(unsigned, top) >> 23) - 127) : 0;
+        float sum = 0.f;
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const unsigned u = w[s][e >> 1];
+                const float x = ldexpf(e & 1 ? bf16_hi(u) : bf16_lo(u), e2);
+                const _Float16 hx = (_Float16)(a.scale < 0.f ? -x : x);
+                qf[n][s][e] = hx;
+                sum += (float)hx;
+            }
+        if (BIAS != 0.f) {
+            sum += __shfl_xor(sum, 16);
+            sum += __shfl_xor(sum, 32);
+        }
+        k0[n] = -(BIAS / UNIT) * sum;
+        cs[n] = ldexpf(fabsf(a.scale), -e2);
+    }
+
+    f32x4_t o[NR][DT], s[NR][2];
+    float m[NR], nm[NR], l[NR], ps[NR], vref = 0.f;
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+        m[n] = NEG_INF;
+        nm[n] = l[n] = ps[n] = 0.f;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) o[n][d] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    }
+    const f16x8_t ones = {(_Float16)1.f, (_Float16)1.f, (_Float16)1.f, (_Float16)1.f,
+                          (_Float16)1.f, (_Float16)1.f, (_Float16)1.f, (_Float16)1.f};
+    const bool brings_v = wave >= WAVES / 2;
+    const unsigned skip = 1024u * PW * (wave % (WAVES / 2));
+    const uint8_t *codes = brings_v ? a.v : a.k;
+
+    for (int w0 = t_begin; w0 < t_end;) {  // windows of pages
+        const int page0 = w0 >> shift;
+        const int w1 = (int)min((int64_t)t_end, (int64_t)(page0 + ROWS_PAGES) << shift);
+        const int pages = ((w1 - 1) >> shift) - page0 + 1, steps = (w1 - w0 + KV_STEP - 1) / KV_STEP;
+        float up = 0.f;
+        __syncthreads();
+        for (int i = tid; i < pages; i += TH) {
+            int id = a.prefix_table[page0 + i];
+            if (id < 0 || id >= a.pages) id = -1;
+            const float ks = id < 0 ? 0.f : a.k_scales[(size_t)id * a.Hkv + h] * UNIT;
+            const float vs = id < 0 ? 0.f : a.v_scales[(size_t)id * a.Hkv + h];
+            up = fmaxf(up, vs);
+            info[i] = f32x4_t{ks, vs, 1.f, __builtin_bit_cast(float, id)};
+        }
+#pragma unroll
+        for (int d = 32; d; d >>= 1) up = fmaxf(up, __shfl_xor(up, d));
+        if (lane == 0) wmax[wave] = up;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) up = fmaxf(up, wmax[w]);
+        up = readlane_f(up, 0);
+        // vref: a power of two at least as large as every value scale so far
+        if (up > vref) {
+            up = pow2_above(up);
+            const float f = vref / up;
+            vref = up;
+#pragma unroll
+            for (int n = 0; n < NR; ++n) {
+                ps[n] *= f;
+#pragma unroll
+                for (int d = 0; d < DT; ++d) o[n][d] *= f;
+            }
+        }
+        for (int i = tid; i < pages; i += TH) {
+            const float vs = info[i][1];
+            info[i][1] = (vs > 0.f ? __builtin_amdgcn_logf(vs / vref) : 0.f) + P_EXP;
+            info[i][2] = vs > 0.f ? vref / vs : 0.f;  // (0: no value scale)
+        }
+        __syncthreads();
+        const auto info_of = [&](int i) { return info[((w0 + i * KV_STEP) >> shift) - page0]; };
+        // this wave's part of step i
+        const auto load = [&](u32x4_t(&to)[PW], int i) {
+            const int t = w0 + i * KV_STEP;
+            const int page = i < steps ? __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, (float)info_of(i)[3])) : -1;
+            const size_t at = ((size_t)max(page, 0) * a.Hkv + h) * ((size_t)a.page * D);
+            load_codes<PW, false>(to, uniform_ptr(codes + at), page < 0 ? 0u : (unsigned)a.page * D, (unsigned)(t & (a.page - 1)) * D + skip, lane);
+        };
+        const auto store = [&](u32x4_t(&st)[PW], int i, int b) {
+            if (brings_v && i < steps) {
+                // codes of slots behind the last token may be anything (an E4M3
+                // NaN), those of a page without a value scale are worth nothing
+                const int t = w0 + i * KV_STEP + 4 * g;
+                const bool no_v = info_of(i)[2] == 0.f;
+                if (no_v || t - 4 * g + KV_STEP > rq.len) {
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        unsigned keep = 0u;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) keep |= ((t + 16 * half + e < rq.len) & !no_v) ? 0xFFu << (8 * e) : 0u;
+#pragma unroll
+                        for (int u = 0; u < PW; ++u) {
+                            st[u][half] &= keep;
+                            st[u][2 + half] &= keep;
+                        }
+                    }
+                }
+            }
+            u32x4_t *to = (brings_v ? vbuf[b] : kbuf[b]) + skip / 8 + lane;  // (1024 bytes of codes: 128 operands)
+#pragma unroll
+            for (int u = 0; u < PW; ++u) {
+                to[2 * u * 64] = __builtin_bit_cast(u32x4_t, codes8<E4M3>(st[u][0], st[u][1]));
+                to[(2 * u + 1) * 64] = __builtin_bit_cast(u32x4_t, codes8<E4M3>(st[u][2], st[u][3]));
+            }
+        };
+        const auto scores = [&](const u32x4_t *buf) {
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const f16x8_t kf = __builtin_bit_cast(f16x8_t, buf[(2 * (i * (D / 64) + (k >> 1)) + (k & 1)) * 64 + lane]);
+#pragma unroll
+                    for (int n = 0; n < NR; ++n)
+                        s[n][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                            kf, qf[n][k], k == 0 ? f32x4_t{k0[n], k0[n], k0[n], k0[n]} : s[n][i], 0, 0, 0);
+                }
+        };
+        // step i: keys of i + 1 and values of i are in LDS, scores of i in s.
+        // What the wave brings next (keys of i + 2, values of i + 1) goes there
+        // meanwhile, and what comes two steps later is asked for.
+        const auto step = [&](auto masked, u32x4_t(&st)[PW], int i) {
+            constexpr bool MASK = decltype(masked)::value;
+            const f32x4_t in = info_of(i);
+            const float ks = readlane_f(in[0], 0), lr = readlane_f(in[1], 0);
+            const float rr = readlane_f(in[2], 0), id = readlane_f(in[3], 0);
+            const float off = __builtin_bit_cast(int, id) < 0 ? NEG_INF : 0.f;
+            __syncthreads();
+            const int ahead = brings_v ? i + 1 : i + 2;
+            store(st, ahead, ahead & 1);
+            load(st, ahead + 2);
+            float x[NR][8];
+#pragma unroll
+            for (int n = 0; n < NR; ++n) {
+                const float f = ks * cs[n];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    x[n][e] = fmaf(s[n][e >> 2][e & 3], f, off);
+                    if (MASK) x[n][e] = w0 + i * KV_STEP + 4 * g + 16 * (e >> 2) + (e & 3) < rq.len ? x[n][e] : NEG_INF;
+                }
+            }
+            bool rise = false;
+            float top[NR];
+#pragma unroll
+            for (int n = 0; n < NR; ++n) {
+                top[n] = fmaxf(fmaxf(fmaxf(x[n][0], x[n][1]), fmaxf(x[n][2], x[n][3])), fmaxf(fmaxf(x[n][4], x[n][5]), fmaxf(x[n][6], x[n][7])));
+                rise |= top[n] > m[n] + 8.f;
+            }
+            if (__any(rise)) {
+#pragma unroll
+                for (int n = 0; n < NR; ++n) {
+                    top[n] = fmaxf(top[n], __shfl_xor(top[n], 16));
+                    top[n] = fmaxf(top[n], __shfl_xor(top[n], 32));
+                    // only the rows concerned: a row does not depend on its neighbours
+                    const float mn = top[n] > m[n] + 8.f ? top[n] : m[n];
+                    const float down = mn == NEG_INF ? 1.f : __builtin_amdgcn_exp2f(m[n] - mn);
+                    m[n] = mn;
+                    nm[n] = mn == NEG_INF ? 0.f : -mn;
+                    l[n] *= down;
+                    ps[n] *= down;
+#pragma unroll
+                    for (int d = 0; d < DT; ++d) o[n][d] *= down;
+                }
+            }
+            scores(kbuf[(i + 1) & 1]);
+            f16x8_t pf[NR];
+#pragma unroll
+            for (int n = 0; n < NR; ++n) {
+                const float nr = nm[n] + lr;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) pf[n][e] = (_Float16)__builtin_amdgcn_exp2f(x[n][e] + nr);
+            }
+            const u32x4_t *buf = vbuf[i & 1];
+#pragma unroll
+            for (int d = 0; d < DT; ++d) {
+                const f16x8_t vf = __builtin_bit_cast(f16x8_t, buf[d * 64 + lane]);
+#pragma unroll
+                for (int n = 0; n < NR; ++n) o[n][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, pf[n], o[n][d], 0, 0, 0);
+            }
+#pragma unroll
+            for (int n = 0; n < NR; ++n) {
+                // the sum of the step's p, as rounded, in every lane of the row
+                const f32x4_t t = __builtin_amdgcn_mfma_f32_16x16x32_f16(ones, pf[n], f32x4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+                ps[n] += t[0];
+                if (rr > 0.f && rr <= 8.f) {
+                    l[n] = fmaf(t[0], rr, l[n]);
+                } else if (rr == 0.f) {
+                    l[n] += t[0];
+                } else {
+                    // values far smaller than the largest: p vs / vref may have
+                    // left f16's range, so p is summed by itself
+                    float sum = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) sum += __builtin_amdgcn_exp2f(x[n][e] + nm[n]);
+                    sum += __shfl_xor(sum, 16);
+                    l[n] = fmaf(sum + __shfl_xor(sum, 32), P_UNIT, l[n]);
+                }
+            }
+        };
+        u32x4_t st0[PW], st1[PW];
+        load(st0, 0);
+        load(st1, 1);
+        store(st0, 0, 0);
+        if (!brings_v) store(st1, 1, 1);
+        load(st0, brings_v ? 1 : 2);
+        load(st1, brings_v ? 2 : 3);
+        __syncthreads();
+        scores(kbuf[0]);
+        const int clear = (w1 - w0) / KV_STEP;  // whole steps
+        int i = 0;
+        for (; i + 2 <= clear; i += 2) {
+            step(std::false_type(), st0, i);
+            step(std::false_type(), st1, i + 1);
+        }
+        for (; i < steps; i += 2) {
+            step(std::true_type(), st0, i);
+            if (i + 1 < steps) step(std::true_type(), st1, i + 1);
+        }
+        w0 = w1;
+    }
+    // o in OUT_UNITs
+    const float out_unit = vref * OUT_UNIT;
+    const int n_cuts = (rq.units + len - 1) / len;
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+        const int row = row0 + 16 * n + c;
+        if (row >= rows) continue;
+        const float back = -BIAS * ps[n];
+        const float sum = rq.too_long ? __builtin_nanf("") : l[n] * OUT_UNIT;
+        const size_t at = (size_t)((h * rq.groups + rg) * n_cuts + cut) * a.part_rows + (row - rg * RW);
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+            f32x4_t v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = fmaf(o[n][d][e], UNIT, back) * out_unit;
+            *reinterpret_cast<f32x4_t *>(a.part + at * D + 16 * d + 4 * g) = v;
+        }
+        if (g == 0) *reinterpret_cast<f32x2_t *>(a.part_ml + 2 * at) = f32x2_t{m[n], sum};
+    }
+}
+
 // The prefix's variant for M * G rows to a KV head: as a request's up to 128
 // rows; more go to 8 waves that share the converted codes.
 struct PrefixShape {
-    int NR, RS, waves;
-    bool conv;
+    int NR, RS;  // row tiles of a wave, waves that take different rows
+    bool many;   // kv_prefix_rows_kernel
 };
 
 constexpr PrefixShape prefix_shape(int D, int64_t rows) {
-    if (D == 64 && rows > 128) return {4, 4, 4, true};
-    if (D == 128 && rows > 128) return {2, 8, 8, true};
-    if (D == 256 && rows > 64) return {1, 8, 8, true};
+    if (D == 64 && rows > 128) return {2, 4, true};
+    if (D == 128 && rows > 128) return {2, 8, true};
+    if (D == 256 && rows > 64) return {1, 8, true};
     const Shape v = shape_of(D, rows);
-    return {v.NR, v.RS, 4, false};
+    return {v.NR, v.RS, false};
 }
 
-template <bool E4M3, int D, int NR, int RS, int WAVES, KvMode MODE, bool CONV>
+template <bool E4M3, int D, int NR, int RS, KvMode MODE>
 void run_line(const KvAttnArgs &a, hipStream_t s) {
-    hipLaunchKernelGGL((kv_attn_kernel<E4M3, D, NR, RS, WAVES, MODE, CONV>), dim3((unsigned)a.slots), dim3(WAVES * 64), 0, s, a);
+    hipLaunchKernelGGL((kv_attn_kernel<E4M3, D, NR, RS, 4, MODE>), dim3((unsigned)a.slots), dim3(256), 0, s, a);
 }
 
 template <bool E4M3, int D, KvMode MODE>
 void pick_line(const KvAttnArgs &a, int NR, int RS, hipStream_t s) {
-    if (NR == 1 && RS == 1) run_line<E4M3, D, 1, 1, 4, MODE, false>(a, s);
-    if constexpr (D == 256) {
-        if (RS == 2) run_line<E4M3, D, 1, 2, 4, MODE, false>(a, s);
-        if (RS == 4) run_line<E4M3, D, 1, 4, 4, MODE, false>(a, s);
-        if constexpr (MODE == KV_PREFIX)
-            if (RS == 8) run_line<E4M3, D, 1, 8, 8, MODE, true>(a, s);
-    } else {
-        if (NR == 2 && RS == 1) run_line<E4M3, D, 2, 1, 4, MODE, false>(a, s);
-        if (RS == 2) run_line<E4M3, D, 2, 2, 4, MODE, false>(a, s);
-        if (NR == 2 && RS == 4) run_line<E4M3, D, 2, 4, 4, MODE, false>(a, s);
-        if constexpr (MODE == KV_PREFIX && D == 128)
-            if (RS == 8) run_line<E4M3, D, 2, 8, 8, MODE, true>(a, s);
-        if constexpr (MODE == KV_PREFIX && D == 64)
-            if (NR == 4) run_line<E4M3, D, 4, 4, 4, MODE, true>(a, s);
-    }
+    if constexpr (D == 256)
+        RS == 1 ? run_line<E4M3, D, 1, 1, MODE>(a, s) : RS == 2 ? run_line<E4M3, D, 1, 2, MODE>(a, s) : run_line<E4M3, D, 1, 4, MODE>(a, s);
+    else if (NR == 1)
+        run_line<E4M3, D, 1, 1, MODE>(a, s);
+    else
+        RS == 1 ? run_line<E4M3, D, 2, 1, MODE>(a, s) : RS == 2 ? run_line<E4M3, D, 2, 2, MODE>(a, s) : run_line<E4M3, D, 2, 4, MODE>(a, s);
 }
 
 template <bool E4M3, int D>
@@ -188,9 +483,14 @@ void run(const KvAttnArgs &own, const KvAttnArgs &pre, const KvPrefixPlan &p, hi
     const Shape v = shape_of(D, (int64_t)own.max_q * own.G);
     const PrefixShape w = prefix_shape(D, (int64_t)own.M * own.G);
     if (p.both) {
-        run_line<E4M3, D, 1, 1, 4, KV_BOTH, false>(own, s);
+        run_line<E4M3, D, 1, 1, KV_BOTH>(own, s);
     } else {
-        pick_line<E4M3, D, KV_PREFIX>(pre, w.NR, w.RS, s);
+        if (w.many) {
+            constexpr PrefixShape big = prefix_shape(D, 1 << 20);
+            hipLaunchKernelGGL((kv_prefix_rows_kernel<E4M3, D, big.NR, big.RS>), dim3((unsigned)pre.slots), dim3(big.RS * 64), 0, s, pre);
+        } else {
+            pick_line<E4M3, D, KV_PREFIX>(pre, w.NR, w.RS, s);
+        }
         pick_line<E4M3, D, KV_OWN>(own, v.NR, v.RS, s);
     }
     KvPrefixJoinArgs j;
@@ -233,7 +533,7 @@ bool kv_prefix_plan(int64_t R, int64_t M, int64_t Hkv, int64_t G, int64_t D, int
     p->own_starts = (int)starts;
     // the prefix's: parts of at least 8 steps, as many as fill the GPU best
     KvAttnPlan &q = p->pre;
-    const int64_t pairs = Hkv * pgroups, fit = 256 * (w.conv ? 1 : w.NR == 1 && D <= 128 ? 3 : 2);
+    const int64_t pairs = Hkv * pgroups, fit = 256 * (w.many ? 8 / w.RS : w.NR == 1 && D <= 128 ? 3 : 2);
     if (pairs * (steps + 1) >= (int64_t(1) << 31) - 65536) return false;
     const int64_t longest = steps / 8 > 1 ? steps / 8 : 1, upto = longest < 4 * fit / pairs ? longest : 4 * fit / pairs;
     int64_t best = 1;
@@ -250,7 +550,7 @@ bool kv_prefix_plan(int64_t R, int64_t M, int64_t Hkv, int64_t G, int64_t D, int
     q.groups = (int)pgroups;
     q.whole = false;
     q.slots = (int)(p->both ? 0 : pairs * best);
-    q.min_run = w.conv ? 1 : 4 / w.RS;
+    q.min_run = w.many ? 1 : 4 / w.RS;
     q.part_rows = (int)(all < PW ? all : PW);
     q.aligned = true;
     q.part_slots = q.slots;
