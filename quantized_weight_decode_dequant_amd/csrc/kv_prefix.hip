@@ -150,8 +150,6 @@ __global__ void __launch_bounds__(512) kv_prefix_join_kernel(KvPrefixJoinArgs p)
 // of values: a step's scores are made by the matrix cores while the softmax of
 // the step before is on the vector unit.  Nothing is masked but what lies
 // behind the prefix's last token.
-constexpr int ROWS_PAGES = 512;  // pages whose scales are held at once
-
 template <bool E4M3, int D, int NR, int WAVES>
 __global__ void __launch_bounds__(WAVES * 64, 2) kv_prefix_rows_kernel(KvAttnArgs) {
     constexpr int KS = D / 32, DT = D / 16, KB = D / 32, TH = WAVES * 64;
@@ -159,8 +157,6 @@ __global__ void __launch_bounds__(WAVES * 64, 2) kv_prefix_rows_kernel(KvAttnArg
     static_assert(PW >= 1 && PW * WAVES == 2 * KB, "half of the waves bring keys, half values");
     constexpr float UNIT = Code<E4M3>::unit, BIAS = Code<E4M3>::bias;
     __shared__ u32x4_t kbuf[2][2 * KB * 64], vbuf[2][2 * KB * 64];
-    __shared__ f32x4_t info[ROWS_PAGES];  // of a page: key scale, log2 of the value scale's part, its inverse, id
-    __shared__ float wmax[WAVES];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g = lane >> 4, c = lane & 15;
     constexpr int RW = 16 * NR * WAVES;
@@ -239,50 +235,46 @@ __global__ void __launch_bounds__(WAVES * 64, 2) kv_prefix_rows_kernel(KvAttnArg
     const unsigned skip = 1024u * PW * (wave % (WAVES / 2));
     const uint8_t *codes = brings_v ? a.v : a.k;
 
-    for (int w0 = t_begin; w0 < t_end;) {  // windows of pages
+    for (int w0 = t_begin; w0 < t_end;) {  // windows of 64 pages, one a lane
         const int page0 = w0 >> shift;
-        const int w1 = (int)min((int64_t)t_end, (int64_t)(page0 + ROWS_PAGES) << shift);
-        const int pages = ((w1 - 1) >> shift) - page0 + 1, steps = (w1 - w0 + KV_STEP - 1) / KV_STEP;
-        float up = 0.f;
-        __syncthreads();
-        for (int i = tid; i < pages; i += TH) {
-            int id = a.prefix_table[page0 + i];
-            if (id < 0 || id >= a.pages) id = -1;
-            const float ks = id < 0 ? 0.f : a.k_scales[(size_t)id * a.Hkv + h] * UNIT;
-            const float vs = id < 0 ? 0.f : a.v_scales[(size_t)id * a.Hkv + h];
-            up = fmaxf(up, vs);
-            info[i] = f32x4_t{ks, vs, 1.f, __builtin_bit_cast(float, id)};
+        const int w1 = (int)min((int64_t)t_end, (int64_t)(page0 + 64) << shift);
+        const int steps = (w1 - w0 + KV_STEP - 1) / KV_STEP;
+        int my_page = -1;
+        float my_ks = 0.f, my_vs = 0.f;
+        if (page0 + lane <= (w1 - 1) >> shift) {
+            my_page = a.prefix_table[page0 + lane];
+            if (my_page < 0 || my_page >= a.pages) my_page = -1;
+            if (my_page >= 0) {
+                my_ks = a.k_scales[(size_t)my_page * a.Hkv + h] * UNIT;
+                my_vs = a.v_scales[(size_t)my_page * a.Hkv + h];
+            }
         }
+        // vref: a power of two at least as large as every value scale so far
+        float up = fmaxf(my_vs, 0.f);
 #pragma unroll
         for (int d = 32; d; d >>= 1) up = fmaxf(up, __shfl_xor(up, d));
-        if (lane == 0) wmax[wave] = up;
-        __syncthreads();
-#pragma unroll
-        for (int w = 0; w < WAVES; ++w) up = fmaxf(up, wmax[w]);
         up = readlane_f(up, 0);
-        // vref: a power of two at least as large as every value scale so far
         if (up > vref) {
             up = pow2_above(up);
-            const float f = vref / up;
+            const float down = vref / up;
             vref = up;
 #pragma unroll
             for (int n = 0; n < NR; ++n) {
-                ps[n] *= f;
+                ps[n] *= down;
 #pragma unroll
-                for (int d = 0; d < DT; ++d) o[n][d] *= f;
+                for (int d = 0; d < DT; ++d) o[n][d] *= down;
             }
         }
-        for (int i = tid; i < pages; i += TH) {
-            const float vs = info[i][1];
-            info[i][1] = (vs > 0.f ? __builtin_amdgcn_logf(vs / vref) : 0.f) + P_EXP;
-            info[i][2] = vs > 0.f ? vref / vs : 0.f;  // (0: no value scale)
-        }
-        __syncthreads();
-        const auto info_of = [&](int i) { return info[((w0 + i * KV_STEP) >> shift) - page0]; };
+        // of a page: log2 of the value scale's part of vref (-infinity where there
+        // is no page), and its inverse (0: no value scale)
+        const float my_lr = my_page < 0 ? NEG_INF : (my_vs > 0.f ? __builtin_amdgcn_logf(my_vs / vref) : 0.f) + P_EXP;
+        const float my_rr = my_vs > 0.f ? vref / my_vs : 0.f;
+        const auto page_of = [&](int i) { return ((w0 + i * KV_STEP) >> shift) - page0; };
+        __syncthreads();  // LDS is free of the last window
         // this wave's part of step i
         const auto load = [&](u32x4_t(&to)[PW], int i) {
             const int t = w0 + i * KV_STEP;
-            const int page = i < steps ? __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, (float)info_of(i)[3])) : -1;
+            const int page = i < steps ? __builtin_amdgcn_readlane(my_page, page_of(i)) : -1;
             const size_t at = ((size_t)max(page, 0) * a.Hkv + h) * ((size_t)a.page * D);
             load_codes<PW, false>(to, uniform_ptr(codes + at), page < 0 ? 0u : (unsigned)a.page * D, (unsigned)(t & (a.page - 1)) * D + skip, lane);
         };
@@ -291,7 +283,7 @@ __global__ void __launch_bounds__(WAVES * 64, 2) kv_prefix_rows_kernel(KvAttnArg
                 // codes of slots behind the last token may be anything (an E4M3
                 // NaN), those of a page without a value scale are worth nothing
                 const int t = w0 + i * KV_STEP + 4 * g;
-                const bool no_v = info_of(i)[2] == 0.f;
+                const bool no_v = readlane_f(my_rr, page_of(i)) == 0.f;
                 if (no_v || t - 4 * g + KV_STEP > rq.len) {
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
@@ -313,48 +305,48 @@ __global__ void __launch_bounds__(WAVES * 64, 2) kv_prefix_rows_kernel(KvAttnArg
                 to[(2 * u + 1) * 64] = __builtin_bit_cast(u32x4_t, codes8<E4M3>(st[u][2], st[u][3]));
             }
         };
-        const auto scores = [&](const u32x4_t *buf) {
+        // operand q of the step's keys, and of its values
+        const auto key = [&](const u32x4_t *buf, int q) { return __builtin_bit_cast(f16x8_t, buf[q * 64 + lane]); };
+        const auto start = [&](int n) { return f32x4_t{k0[n], k0[n], k0[n], k0[n]}; };
+        // of step i, whose scores are in s: the factor to them, and a
+        // lane's largest of each row
+        float f[NR], top[NR];
+        const auto sees = [&](int i, int e) { return w0 + i * KV_STEP + 4 * g + 16 * (e >> 2) + (e & 3) < rq.len; };
+        const auto largest = [&](auto masked, int i) {
+            const int page = page_of(min(i, steps - 1));
+            const bool there = __builtin_amdgcn_readlane(my_page, page) >= 0;
+            const float ks = readlane_f(my_ks, page);
 #pragma unroll
-            for (int k = 0; k < KS; ++k)
+            for (int n = 0; n < NR; ++n) {
+                f[n] = ks * cs[n];
+                float v[8];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const f16x8_t kf = __builtin_bit_cast(f16x8_t, buf[(2 * (i * (D / 64) + (k >> 1)) + (k & 1)) * 64 + lane]);
-#pragma unroll
-                    for (int n = 0; n < NR; ++n)
-                        s[n][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-                            kf, qf[n][k], k == 0 ? f32x4_t{k0[n], k0[n], k0[n], k0[n]} : s[n][i], 0, 0, 0);
-                }
+                for (int e = 0; e < 8; ++e) v[e] = !decltype(masked)::value || sees(i, e) ? s[n][e >> 2][e & 3] : NEG_INF;
+                const float most = fmaxf(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])), fmaxf(fmaxf(v[4], v[5]), fmaxf(v[6], v[7])));
+                top[n] = there && most > NEG_INF ? most * f[n] : NEG_INF;
+            }
         };
         // step i: keys of i + 1 and values of i are in LDS, scores of i in s.
         // What the wave brings next (keys of i + 2, values of i + 1) goes there
-        // meanwhile, and what comes two steps later is asked for.
+        // meanwhile, and what comes two steps later is asked for.  Matrix
+        // instructions take four times a vector instruction's time, so they are
+        // spread: the next scores among the powers, the sums among the next
+        // scores' maxima.  `masked`: step i + 1 may end behind the last token.
         const auto step = [&](auto masked, u32x4_t(&st)[PW], int i) {
-            constexpr bool MASK = decltype(masked)::value;
-            const f32x4_t in = info_of(i);
-            const float ks = readlane_f(in[0], 0), lr = readlane_f(in[1], 0);
-            const float rr = readlane_f(in[2], 0), id = readlane_f(in[3], 0);
-            const float off = __builtin_bit_cast(int, id) < 0 ? NEG_INF : 0.f;
+            const float lr = readlane_f(my_lr, page_of(i)), rr = readlane_f(my_rr, page_of(i));
             __syncthreads();
+            constexpr int NK = 2 * KS, HELD = NK < 8 ? NK : 8;  // operands of keys; as many are read ahead
+            const u32x4_t *kb = kbuf[(i + 1) & 1], *vb = vbuf[i & 1];
+            f16x8_t kf[HELD], vf[HELD];
+#pragma unroll
+            for (int q = 0; q < HELD; ++q) kf[q] = key(kb, q);
+            __builtin_amdgcn_sched_barrier(0);
             const int ahead = brings_v ? i + 1 : i + 2;
             store(st, ahead, ahead & 1);
             load(st, ahead + 2);
-            float x[NR][8];
-#pragma unroll
-            for (int n = 0; n < NR; ++n) {
-                const float f = ks * cs[n];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    x[n][e] = fmaf(s[n][e >> 2][e & 3], f, off);
-                    if (MASK) x[n][e] = w0 + i * KV_STEP + 4 * g + 16 * (e >> 2) + (e & 3) < rq.len ? x[n][e] : NEG_INF;
-                }
-            }
             bool rise = false;
-            float top[NR];
 #pragma unroll
-            for (int n = 0; n < NR; ++n) {
-                top[n] = fmaxf(fmaxf(fmaxf(x[n][0], x[n][1]), fmaxf(x[n][2], x[n][3])), fmaxf(fmaxf(x[n][4], x[n][5]), fmaxf(x[n][6], x[n][7])));
-                rise |= top[n] > m[n] + 8.f;
-            }
+            for (int n = 0; n < NR; ++n) rise |= top[n] > m[n] + 8.f;
             if (__any(rise)) {
 #pragma unroll
                 for (int n = 0; n < NR; ++n) {
@@ -371,39 +363,73 @@ __global__ void __launch_bounds__(WAVES * 64, 2) kv_prefix_rows_kernel(KvAttnArg
                     for (int d = 0; d < DT; ++d) o[n][d] *= down;
                 }
             }
-            scores(kbuf[(i + 1) & 1]);
+            if (rr > 8.f) {
+                // values far smaller than the largest: p vs / vref may have left
+                // f16's range, so p is summed by itself
+#pragma unroll
+                for (int n = 0; n < NR; ++n) {
+                    float sum = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        sum += !decltype(masked)::value || sees(i, e) ? __builtin_amdgcn_exp2f(fmaf(s[n][e >> 2][e & 3], f[n], nm[n])) : 0.f;
+                    sum += __shfl_xor(sum, 16);
+                    l[n] = fmaf(sum + __shfl_xor(sum, 32), P_UNIT, l[n]);
+                }
+            }
+            f32x4_t was[NR][2];  // scores of step i
+#pragma unroll
+            for (int n = 0; n < NR; ++n) {
+                was[n][0] = s[n][0];
+                was[n][1] = s[n][1];
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            // operand q: token tile (q / 2) / (D / 64), MFMA step the rest
+#pragma unroll
+            for (int q = 0; q < NK; ++q) {
+                const int t = q / KS, k = q % KS;
+#pragma unroll
+                for (int n = 0; n < NR; ++n)
+                    s[n][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf[q % HELD], qf[n][k], k == 0 ? start(n) : s[n][t], 0, 0, 0);
+                if (q + HELD < NK) kf[q % HELD] = key(kb, q + HELD);
+                if (q >= NK - HELD) vf[q - (NK - HELD)] = key(vb, q - (NK - HELD));
+            }
             f16x8_t pf[NR];
 #pragma unroll
             for (int n = 0; n < NR; ++n) {
                 const float nr = nm[n] + lr;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) pf[n][e] = (_Float16)__builtin_amdgcn_exp2f(x[n][e] + nr);
+                for (int e = 0; e < 8; ++e) {
+                    const float x = fmaf(was[n][e >> 2][e & 3], f[n], nr);
+                    pf[n][e] = (_Float16)__builtin_amdgcn_exp2f(!decltype(masked)::value || sees(i, e) ? x : NEG_INF);
+                }
             }
-            const u32x4_t *buf = vbuf[i & 1];
+#pragma unroll
+            for (int r = 0; r < NK; ++r) {
+                __builtin_amdgcn_sched_group_barrier(0x008, NR, 0);
+                __builtin_amdgcn_sched_group_barrier(0x400, 8 * NR / NK, 0);
+                __builtin_amdgcn_sched_group_barrier(0x002, 12 * NR / NK, 0);
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            }
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int d = 0; d < DT; ++d) {
-                const f16x8_t vf = __builtin_bit_cast(f16x8_t, buf[d * 64 + lane]);
 #pragma unroll
-                for (int n = 0; n < NR; ++n) o[n][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, pf[n], o[n][d], 0, 0, 0);
+                for (int n = 0; n < NR; ++n) o[n][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[d % HELD], pf[n], o[n][d], 0, 0, 0);
+                if (d + HELD < DT) vf[d % HELD] = key(vb, d + HELD);
+            }
+            f32x4_t t[NR];  // the sum of the step's p, as rounded, in every lane of the row
+#pragma unroll
+            for (int n = 0; n < NR; ++n) t[n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ones, pf[n], f32x4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+            largest(masked, i + 1);
+#pragma unroll
+            for (int r = 0; r < DT; ++r) {
+                __builtin_amdgcn_sched_group_barrier(0x008, NR, 0);
+                __builtin_amdgcn_sched_group_barrier(0x002, 2 * NR, 0);
             }
 #pragma unroll
             for (int n = 0; n < NR; ++n) {
-                // the sum of the step's p, as rounded, in every lane of the row
-                const f32x4_t t = __builtin_amdgcn_mfma_f32_16x16x32_f16(ones, pf[n], f32x4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
-                ps[n] += t[0];
-                if (rr > 0.f && rr <= 8.f) {
-                    l[n] = fmaf(t[0], rr, l[n]);
-                } else if (rr == 0.f) {
-                    l[n] += t[0];
-                } else {
-                    // values far smaller than the largest: p vs / vref may have
-                    // left f16's range, so p is summed by itself
-                    float sum = 0.f;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) sum += __builtin_amdgcn_exp2f(x[n][e] + nm[n]);
-                    sum += __shfl_xor(sum, 16);
-                    l[n] = fmaf(sum + __shfl_xor(sum, 32), P_UNIT, l[n]);
-                }
+                ps[n] += t[n][0];
+                if (rr <= 8.f) l[n] = fmaf(t[n][0], rr == 0.f ? 1.f : rr, l[n]);
             }
         };
         u32x4_t st0[PW], st1[PW];
@@ -414,8 +440,13 @@ __global__ void __launch_bounds__(WAVES * 64, 2) kv_prefix_rows_kernel(KvAttnArg
         load(st0, brings_v ? 1 : 2);
         load(st1, brings_v ? 2 : 3);
         __syncthreads();
-        scores(kbuf[0]);
-        const int clear = (w1 - w0) / KV_STEP;  // whole steps
+#pragma unroll
+        for (int q = 0; q < 2 * KS; ++q)
+#pragma unroll
+            for (int n = 0; n < NR; ++n)
+                s[n][q / KS] = __builtin_amdgcn_mfma_f32_16x16x32_f16(key(kbuf[0], q), qf[n][q % KS], q % KS == 0 ? start(n) : s[n][q / KS], 0, 0, 0);
+        largest(std::true_type(), 0);
+        const int clear = (w1 - w0) / KV_STEP - 1;  // steps before a whole one
         int i = 0;
         for (; i + 2 <= clear; i += 2) {
             step(std::false_type(), st0, i);
@@ -457,7 +488,7 @@ struct PrefixShape {
 
 constexpr PrefixShape prefix_shape(int D, int64_t rows) {
     if (D == 64 && rows > 128) return {2, 4, true};
-    if (D == 128 && rows > 128) return {2, 8, true};
+    if (D == 128 && rows > 128) return {2, 4, true};
     if (D == 256 && rows > 64) return {1, 8, true};
     const Shape v = shape_of(D, rows);
     return {v.NR, v.RS, false};
