@@ -269,36 +269,43 @@ __global__ void __launch_bounds__(WAVES * 64, 2) kv_prefix_rows_kernel(KvAttnArg
         // is no page), and its inverse (0: no value scale)
         const float my_lr = my_page < 0 ? NEG_INF : (my_vs > 0.f ? __builtin_amdgcn_logf(my_vs / vref) : 0.f) + P_EXP;
         const float my_rr = my_vs > 0.f ? vref / my_vs : 0.f;
-        const auto page_of = [&](int i) { return ((w0 + i * KV_STEP) >> shift) - page0; };
+        // where a wave's part of the page lies, and how much of it there is
+        const uint64_t my_at = reinterpret_cast<uint64_t>(codes) + ((size_t)max(my_page, 0) * a.Hkv + h) * ((size_t)a.page * D) + skip;
+        const unsigned my_lo = (unsigned)my_at, my_hi = (unsigned)(my_at >> 32), my_bytes = my_page < 0 ? 0u : (unsigned)a.page * D - skip;
+        // whether every page is there, has a value scale, and one whose part of
+        // vref leaves p in f16's range
+        const bool plain = !__any(page0 + lane <= (w1 - 1) >> shift && !(my_rr > 0.f && my_rr <= 8.f));
+        const auto page_of = [&](int i) { return ((w0 + min(i, steps - 1) * KV_STEP) >> shift) - page0; };
         __syncthreads();  // LDS is free of the last window
-        // this wave's part of step i
+        // this wave's part of step i (of the last one again where i is past it)
         const auto load = [&](u32x4_t(&to)[PW], int i) {
-            const int t = w0 + i * KV_STEP;
-            const int page = i < steps ? __builtin_amdgcn_readlane(my_page, page_of(i)) : -1;
-            const size_t at = ((size_t)max(page, 0) * a.Hkv + h) * ((size_t)a.page * D);
-            load_codes<PW, false>(to, uniform_ptr(codes + at), page < 0 ? 0u : (unsigned)a.page * D, (unsigned)(t & (a.page - 1)) * D + skip, lane);
+            const int page = page_of(i), t = w0 + min(i, steps - 1) * KV_STEP;
+            const uint64_t at = (uint64_t)(unsigned)__builtin_amdgcn_readlane((int)my_lo, page) |
+                                ((uint64_t)(unsigned)__builtin_amdgcn_readlane((int)my_hi, page) << 32);
+            load_codes<PW, false>(to, reinterpret_cast<const uint8_t *>(at), (unsigned)__builtin_amdgcn_readlane((int)my_bytes, page),
+                                  (unsigned)(t & (a.page - 1)) * D, lane);
         };
-        const auto store = [&](u32x4_t(&st)[PW], int i, int b) {
-            if (brings_v && i < steps) {
+        // its codes, converted, to LDS
+        u32x4_t *const home = (brings_v ? vbuf[0] : kbuf[0]) + skip / 8 + lane;  // (1024 bytes of codes: 128 operands)
+        const auto store = [&](auto masked, u32x4_t(&st)[PW], int i) {
+            if (decltype(masked)::value && brings_v) {
                 // codes of slots behind the last token may be anything (an E4M3
                 // NaN), those of a page without a value scale are worth nothing
                 const int t = w0 + i * KV_STEP + 4 * g;
                 const bool no_v = readlane_f(my_rr, page_of(i)) == 0.f;
-                if (no_v || t - 4 * g + KV_STEP > rq.len) {
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        unsigned keep = 0u;
+                for (int half = 0; half < 2; ++half) {
+                    unsigned keep = 0u;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) keep |= ((t + 16 * half + e < rq.len) & !no_v) ? 0xFFu << (8 * e) : 0u;
+                    for (int e = 0; e < 4; ++e) keep |= ((t + 16 * half + e < rq.len) & !no_v) ? 0xFFu << (8 * e) : 0u;
 #pragma unroll
-                        for (int u = 0; u < PW; ++u) {
-                            st[u][half] &= keep;
-                            st[u][2 + half] &= keep;
-                        }
+                    for (int u = 0; u < PW; ++u) {
+                        st[u][half] &= keep;
+                        st[u][2 + half] &= keep;
                     }
                 }
             }
-            u32x4_t *to = (brings_v ? vbuf[b] : kbuf[b]) + skip / 8 + lane;  // (1024 bytes of codes: 128 operands)
+            u32x4_t *to = home + (i & 1) * (2 * KB * 64);
 #pragma unroll
             for (int u = 0; u < PW; ++u) {
                 to[2 * u * 64] = __builtin_bit_cast(u32x4_t, codes8<E4M3>(st[u][0], st[u][1]));
@@ -313,9 +320,8 @@ __global__ void __launch_bounds__(WAVES * 64, 2) kv_prefix_rows_kernel(KvAttnArg
         float f[NR], top[NR];
         const auto sees = [&](int i, int e) { return w0 + i * KV_STEP + 4 * g + 16 * (e >> 2) + (e & 3) < rq.len; };
         const auto largest = [&](auto masked, int i) {
-            const int page = page_of(min(i, steps - 1));
-            const bool there = __builtin_amdgcn_readlane(my_page, page) >= 0;
-            const float ks = readlane_f(my_ks, page);
+            const float ks = readlane_f(my_ks, page_of(i));
+            const bool there = !decltype(masked)::value || __builtin_amdgcn_readlane(my_page, page_of(i)) >= 0;
 #pragma unroll
             for (int n = 0; n < NR; ++n) {
                 f[n] = ks * cs[n];
@@ -323,7 +329,7 @@ __global__ void __launch_bounds__(WAVES * 64, 2) kv_prefix_rows_kernel(KvAttnArg
 #pragma unroll
                 for (int e = 0; e < 8; ++e) v[e] = !decltype(masked)::value || sees(i, e) ? s[n][e >> 2][e & 3] : NEG_INF;
                 const float most = fmaxf(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])), fmaxf(fmaxf(v[4], v[5]), fmaxf(v[6], v[7])));
-                top[n] = there && most > NEG_INF ? most * f[n] : NEG_INF;
+                top[n] = !decltype(masked)::value || (there && most > NEG_INF) ? most * f[n] : NEG_INF;
             }
         };
         // step i: keys of i + 1 and values of i are in LDS, scores of i in s.
@@ -341,9 +347,6 @@ __global__ void __launch_bounds__(WAVES * 64, 2) kv_prefix_rows_kernel(KvAttnArg
 #pragma unroll
             for (int q = 0; q < HELD; ++q) kf[q] = key(kb, q);
             __builtin_amdgcn_sched_barrier(0);
-            const int ahead = brings_v ? i + 1 : i + 2;
-            store(st, ahead, ahead & 1);
-            load(st, ahead + 2);
             bool rise = false;
 #pragma unroll
             for (int n = 0; n < NR; ++n) rise |= top[n] > m[n] + 8.f;
@@ -363,7 +366,7 @@ __global__ void __launch_bounds__(WAVES * 64, 2) kv_prefix_rows_kernel(KvAttnArg
                     for (int d = 0; d < DT; ++d) o[n][d] *= down;
                 }
             }
-            if (rr > 8.f) {
+            if (decltype(masked)::value && !(rr > 0.f && rr <= 8.f) && lr > NEG_INF) {
                 // values far smaller than the largest: p vs / vref may have left
                 // f16's range, so p is summed by itself
 #pragma unroll
@@ -382,6 +385,8 @@ __global__ void __launch_bounds__(WAVES * 64, 2) kv_prefix_rows_kernel(KvAttnArg
                 was[n][0] = s[n][0];
                 was[n][1] = s[n][1];
             }
+            const int ahead = brings_v ? i + 1 : i + 2;
+            if (decltype(masked)::value) store(masked, st, ahead);
             __builtin_amdgcn_sched_barrier(0);
             // operand q: token tile (q / 2) / (D / 64), MFMA step the rest
 #pragma unroll
@@ -393,6 +398,8 @@ __global__ void __launch_bounds__(WAVES * 64, 2) kv_prefix_rows_kernel(KvAttnArg
                 if (q + HELD < NK) kf[q % HELD] = key(kb, q + HELD);
                 if (q >= NK - HELD) vf[q - (NK - HELD)] = key(vb, q - (NK - HELD));
             }
+            if (!decltype(masked)::value) store(masked, st, ahead);
+            load(st, ahead + 2);
             f16x8_t pf[NR];
 #pragma unroll
             for (int n = 0; n < NR; ++n) {
@@ -405,9 +412,12 @@ __global__ void __launch_bounds__(WAVES * 64, 2) kv_prefix_rows_kernel(KvAttnArg
             }
 #pragma unroll
             for (int r = 0; r < NK; ++r) {
-                __builtin_amdgcn_sched_group_barrier(0x008, NR, 0);
-                __builtin_amdgcn_sched_group_barrier(0x400, 8 * NR / NK, 0);
-                __builtin_amdgcn_sched_group_barrier(0x002, 12 * NR / NK, 0);
+#pragma unroll
+                for (int n = 0; n < NR; ++n) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x002, 3, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x400, 8 / NK, 0);
+                }
                 __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
             }
             __builtin_amdgcn_sched_barrier(0);
@@ -429,14 +439,14 @@ __global__ void __launch_bounds__(WAVES * 64, 2) kv_prefix_rows_kernel(KvAttnArg
 #pragma unroll
             for (int n = 0; n < NR; ++n) {
                 ps[n] += t[n][0];
-                if (rr <= 8.f) l[n] = fmaf(t[n][0], rr == 0.f ? 1.f : rr, l[n]);
+                if (!decltype(masked)::value || (rr > 0.f && rr <= 8.f)) l[n] = fmaf(t[n][0], rr, l[n]);
             }
         };
         u32x4_t st0[PW], st1[PW];
         load(st0, 0);
         load(st1, 1);
-        store(st0, 0, 0);
-        if (!brings_v) store(st1, 1, 1);
+        store(std::true_type(), st0, 0);
+        if (!brings_v) store(std::true_type(), st1, 1);
         load(st0, brings_v ? 1 : 2);
         load(st1, brings_v ? 2 : 3);
         __syncthreads();
@@ -446,7 +456,7 @@ __global__ void __launch_bounds__(WAVES * 64, 2) kv_prefix_rows_kernel(KvAttnArg
             for (int n = 0; n < NR; ++n)
                 s[n][q / KS] = __builtin_amdgcn_mfma_f32_16x16x32_f16(key(kbuf[0], q), qf[n][q % KS], q % KS == 0 ? start(n) : s[n][q / KS], 0, 0, 0);
         largest(std::true_type(), 0);
-        const int clear = (w1 - w0) / KV_STEP - 1;  // steps before a whole one
+        const int clear = plain ? (w1 - w0) / KV_STEP - 1 : 0;  // steps before a whole one
         int i = 0;
         for (; i + 2 <= clear; i += 2) {
             step(std::false_type(), st0, i);
