@@ -422,8 +422,15 @@ int kv_prefix_attention_run(const qg_kv_cache *cache, int64_t R, int64_t M, int6
             b.aligned = l.aligned;
             return b;
         };
-        return hip_status(launch_kv_prefix_attention(line(p.own, 0, p.own_part), line(p.pre, (size_t)p.own.head_bytes, p.pre_part),
-                                                     p, cache->D, cache->fmt == QG_KV_E4M3,
+        KvAttnArgs own = line(p.own, 0, p.own_part);
+        const KvAttnArgs pre = line(p.pre, (size_t)p.own.head_bytes, p.pre_part);
+        own.pre_part = pre.part;
+        own.pre_ml = pre.part_ml;
+        own.pre_head = pre.head;
+        own.pre_rw = p.pre_rw;
+        own.pre_rows = pre.part_rows;
+        own.pre_slots = pre.part_slots;
+        return hip_status(launch_kv_prefix_attention(own, pre, p, cache->D, cache->fmt == QG_KV_E4M3,
                                                      reinterpret_cast<hipStream_t>(stream)));
     } catch (...) {
         return QG_EINTERNAL;

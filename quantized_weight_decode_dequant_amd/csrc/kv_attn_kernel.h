@@ -14,7 +14,9 @@ namespace qg {
 //   KV_BOTH    the requests and, as one more entry, the prefix that they share:
 //              all rows of the call against it, without masks; segments only
 //   KV_PREFIX  the prefix alone; segments only
-enum KvMode { KV_PLAIN, KV_OWN, KV_BOTH, KV_PREFIX };
+//   KV_LAST    the requests, not cut, with the prefix's segments joined to them;
+//              the output
+enum KvMode { KV_PLAIN, KV_OWN, KV_BOTH, KV_PREFIX, KV_LAST };
 
 namespace {
 
@@ -198,7 +200,7 @@ __global__ void __launch_bounds__(WAVES * 64, NR == 1 && D <= 128 && WAVES == 4 
 
     // this workgroup's run [x, end) of the line, and the request it starts in
     int r, x, end, before;
-    const bool whole = MODE == KV_PLAIN && args().whole;
+    const bool whole = MODE == KV_LAST || (MODE == KV_PLAIN && args().whole);
     if (whole) {
         r = blockIdx.x / per;
         x = end = before = 0;
@@ -576,6 +578,35 @@ __global__ void __launch_bounds__(WAVES * 64, NR == 1 && D <= 128 && WAVES == 4 
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[n][d][e] = fmaf(o[n][d][e], UNIT, back) * out_unit;
     }
+    // the prefix's segments, spread over the waves that split the tokens
+    if constexpr (MODE == KV_LAST) {
+        Args &a = args();
+        const Req pq = req_of<RW, KV_PREFIX>(a, 0);
+        const int cut = max(a.pre_head[0], 1), segs = pq.units > 0 ? (pq.units + cut - 1) / cut : 0;
+        const int pgroups = (pq.T * a.G + a.pre_rw - 1) / a.pre_rw;
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+            const int row = (rq.q0 - pq.q0) * a.G + min(row0 + 16 * (rsi * NR + n) + c, rows - 1);
+            const int slot = (h * pgroups + row / a.pre_rw) * segs;
+            // (never so, unless another call wrote to the workspace in between)
+            if (slot < 0 || segs > a.pre_slots || slot > a.pre_slots - segs) continue;
+            const size_t at = (size_t)slot * a.pre_rows + row % a.pre_rw;
+            for (int i = ts; i < segs; i += TS) {
+                const size_t from = at + (size_t)i * a.pre_rows;
+                const f32x2_t ml = *reinterpret_cast<const f32x2_t *>(a.pre_ml + 2 * from);
+                f32x4_t v[DT];
+#pragma unroll
+                for (int d = 0; d < DT; ++d) v[d] = *reinterpret_cast<const f32x4_t *>(a.pre_part + from * D + 16 * d + 4 * g);
+                const float mn = fmaxf(m[n], ml[0]);
+                const float f1 = mn == NEG_INF ? 0.f : __builtin_amdgcn_exp2f(m[n] - mn);
+                const float f2 = mn == NEG_INF ? 0.f : __builtin_amdgcn_exp2f(ml[0] - mn);
+                m[n] = mn;
+                l[n] = l[n] * f1 + ml[1] * f2;
+#pragma unroll
+                for (int d = 0; d < DT; ++d) o[n][d] = o[n][d] * f1 + v[d] * f2;
+            }
+        }
+    }
     // join the waves that split the tokens, half of them at a time
     if constexpr (TS > 1) {
 #pragma unroll
@@ -620,7 +651,7 @@ __global__ void __launch_bounds__(WAVES * 64, NR == 1 && D <= 128 && WAVES == 4 
         for (int n = 0; n < NR; ++n) {
             const int row = row0 + 16 * (rsi * NR + n) + c;
             if (row >= rows) continue;
-            if (MODE == KV_PLAIN && all) {
+            if (MODE == KV_LAST || (MODE == KV_PLAIN && all)) {
                 const float f = rq.too_long ? __builtin_nanf("") : l[n] == 0.f ? 0.f : 1.f / l[n];
                 const int j = row / a.G;
                 const size_t at = (size_t)(rq.q0 + j) * a.out_stride + (size_t)(h * a.G + row - j * a.G) * D + 4 * g;

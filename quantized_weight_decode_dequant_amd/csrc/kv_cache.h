@@ -57,6 +57,9 @@ struct KvAttnArgs {
     int prefix_blocks, max_prefix;
     int starts;      // (entry, head, row group)s of the line at most
     int cuts;        // parts that the prefix is cut into, where it is a line by itself
+    const float *pre_part, *pre_ml;  // the prefix's segments, for the last kernel
+    const int32_t *pre_head;
+    int pre_rw, pre_rows, pre_slots;  // rows of a group, of a segment; places
 };
 
 struct KvTablesArgs {
@@ -90,6 +93,8 @@ struct KvPrefixPlan {
     int cuts;
     int own_starts;
     bool both;      // one line, `own`
+    bool last;      // the requests are not cut: their kernel joins the prefix's segments
+    int pre_rw;     // rows of a group of the prefix's line
     size_t own_part, pre_part, bytes;  // where the workspace holds the segments
 };
 bool kv_prefix_plan(int64_t R, int64_t M, int64_t Hkv, int64_t G, int64_t D, int64_t max_q, int64_t max_len,

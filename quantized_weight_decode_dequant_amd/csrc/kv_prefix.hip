@@ -489,34 +489,37 @@ __global__ void __launch_bounds__(WAVES * 64, 2) kv_prefix_rows_kernel(KvAttnArg
     }
 }
 
-// The prefix's variant for M * G rows to a KV head: as a request's up to 128
-// rows; more go to 8 waves that share the converted codes.
+// The prefix's variant for M * G rows to a KV head.
 struct PrefixShape {
     int NR, RS;  // row tiles of a wave, waves that take different rows
     bool many;   // kv_prefix_rows_kernel
 };
 
 constexpr PrefixShape prefix_shape(int D, int64_t rows) {
-    if (D == 64 && rows > 128) return {2, 4, true};
-    if (D == 128 && rows > 128) return {2, 4, true};
-    if (D == 256 && rows > 64) return {1, 8, true};
-    const Shape v = shape_of(D, rows);
-    return {v.NR, v.RS, false};
+    if (D == 256) return rows <= 16 ? PrefixShape{1, 1, false} : rows <= 64 ? PrefixShape{1, 4, true} : PrefixShape{1, 8, true};
+    if (rows <= 32) return {rows <= 16 ? 1 : 2, 1, false};
+    return {D == 128 && rows <= 192 ? 1 : 2, 4, true};
 }
 
-template <bool E4M3, int D, int NR, int RS, KvMode MODE>
+template <bool E4M3, int D, int NR, int RS, KvMode MODE, int WAVES = 4>
 void run_line(const KvAttnArgs &a, hipStream_t s) {
-    hipLaunchKernelGGL((kv_attn_kernel<E4M3, D, NR, RS, 4, MODE>), dim3((unsigned)a.slots), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((kv_attn_kernel<E4M3, D, NR, RS, WAVES, MODE>), dim3((unsigned)a.slots), dim3(WAVES * 64), 0, s, a);
 }
 
+// the requests' own tokens
 template <bool E4M3, int D, KvMode MODE>
-void pick_line(const KvAttnArgs &a, int NR, int RS, hipStream_t s) {
+void pick_own(const KvAttnArgs &a, const Shape &v, hipStream_t s) {
     if constexpr (D == 256)
-        RS == 1 ? run_line<E4M3, D, 1, 1, MODE>(a, s) : RS == 2 ? run_line<E4M3, D, 1, 2, MODE>(a, s) : run_line<E4M3, D, 1, 4, MODE>(a, s);
-    else if (NR == 1)
-        run_line<E4M3, D, 1, 1, MODE>(a, s);
+        v.RS == 1 ? run_line<E4M3, D, 1, 1, MODE>(a, s) : v.RS == 2 ? run_line<E4M3, D, 1, 2, MODE>(a, s) : run_line<E4M3, D, 1, 4, MODE>(a, s);
+    else if (v.NR == 1)
+        run_line<E4M3, D, 1, 1, MODE, MODE == KV_LAST ? 8 : 4>(a, s);
     else
-        RS == 1 ? run_line<E4M3, D, 2, 1, MODE>(a, s) : RS == 2 ? run_line<E4M3, D, 2, 2, MODE>(a, s) : run_line<E4M3, D, 2, 4, MODE>(a, s);
+        v.RS == 1 ? run_line<E4M3, D, 2, 1, MODE>(a, s) : v.RS == 2 ? run_line<E4M3, D, 2, 2, MODE>(a, s) : run_line<E4M3, D, 2, 4, MODE>(a, s);
+}
+
+template <bool E4M3, int D, int NR, int WAVES>
+void run_rows(const KvAttnArgs &a, hipStream_t s) {
+    hipLaunchKernelGGL((kv_prefix_rows_kernel<E4M3, D, NR, WAVES>), dim3((unsigned)a.slots), dim3(WAVES * 64), 0, s, a);
 }
 
 template <bool E4M3, int D>
@@ -526,19 +529,25 @@ void run(const KvAttnArgs &own, const KvAttnArgs &pre, const KvPrefixPlan &p, hi
     if (p.both) {
         run_line<E4M3, D, 1, 1, KV_BOTH>(own, s);
     } else {
-        if (w.many) {
-            constexpr PrefixShape big = prefix_shape(D, 1 << 20);
-            hipLaunchKernelGGL((kv_prefix_rows_kernel<E4M3, D, big.NR, big.RS>), dim3((unsigned)pre.slots), dim3(big.RS * 64), 0, s, pre);
-        } else {
-            pick_line<E4M3, D, KV_PREFIX>(pre, w.NR, w.RS, s);
+        if constexpr (D == 256)
+            !w.many ? run_line<E4M3, D, 1, 1, KV_PREFIX>(pre, s) : w.RS == 4 ? run_rows<E4M3, D, 1, 4>(pre, s) : run_rows<E4M3, D, 1, 8>(pre, s);
+        else if (!w.many)
+            w.NR == 1 ? run_line<E4M3, D, 1, 1, KV_PREFIX>(pre, s) : run_line<E4M3, D, 2, 1, KV_PREFIX>(pre, s);
+        else if (D == 128 && w.NR == 1)
+            run_rows<E4M3, D, D == 128 ? 1 : 2, 4>(pre, s);
+        else
+            run_rows<E4M3, D, 2, 4>(pre, s);
+        if (p.last) {
+            pick_own<E4M3, D, KV_LAST>(own, v, s);
+            return;
         }
-        pick_line<E4M3, D, KV_OWN>(own, v.NR, v.RS, s);
+        pick_own<E4M3, D, KV_OWN>(own, v, s);
     }
     KvPrefixJoinArgs j;
     j.own = own;
     j.pre = pre;
     j.own_rw = 16 * v.NR * v.RS;
-    j.pre_rw = 16 * w.NR * w.RS;
+    j.pre_rw = p.pre_rw;
     j.both = p.both;
     const int64_t joins = (int64_t)own.R * own.max_q * own.Hq;
     if (joins >= 1024)
@@ -562,6 +571,8 @@ bool kv_prefix_plan(int64_t R, int64_t M, int64_t Hkv, int64_t G, int64_t D, int
     const int64_t starts = R * Hkv * groups + (p->both ? Hkv * pgroups : 0);
     int64_t most = R * Hkv * groups * units + (p->both ? Hkv * pgroups * (steps + 1) : 0);
     if (most >= (int64_t(1) << 31) - 65536) return false;
+    p->last = !p->both && max_len <= 1024;
+    p->pre_rw = (int)PW;
     o.groups = (int)groups;
     o.whole = false;
     o.slots = 256 * (v.NR == 1 && D <= 128 ? 3 : 2);
@@ -571,10 +582,14 @@ bool kv_prefix_plan(int64_t R, int64_t M, int64_t Hkv, int64_t G, int64_t D, int
     if (!o.aligned) o.slots *= 2;
     o.part_slots = o.slots + (o.aligned ? 0 : starts);
     o.head_bytes = PART_HEAD;
+    if (p->last) {
+        o.slots = (int)starts;  // a workgroup for each (request, head, row group)
+        o.part_slots = o.head_bytes = 0;
+    }
     p->own_starts = (int)starts;
     // the prefix's: parts of at least 8 steps, as many as fill the GPU best
     KvAttnPlan &q = p->pre;
-    const int64_t pairs = Hkv * pgroups, fit = 256 * (w.many ? 8 / w.RS : w.NR == 1 && D <= 128 ? 3 : 2);
+    const int64_t pairs = Hkv * pgroups, fit = 256 * (w.many ? (w.NR == 1 && D == 128 ? 3 : 8 / w.RS) : w.NR == 1 && D <= 128 ? 3 : 2);
     if (pairs * (steps + 1) >= (int64_t(1) << 31) - 65536) return false;
     const int64_t longest = steps / 8 > 1 ? steps / 8 : 1, upto = longest < 4 * fit / pairs ? longest : 4 * fit / pairs;
     int64_t best = 1;
