@@ -571,7 +571,6 @@ bool kv_prefix_plan(int64_t R, int64_t M, int64_t Hkv, int64_t G, int64_t D, int
     const int64_t starts = R * Hkv * groups + (p->both ? Hkv * pgroups : 0);
     int64_t most = R * Hkv * groups * units + (p->both ? Hkv * pgroups * (steps + 1) : 0);
     if (most >= (int64_t(1) << 31) - 65536) return false;
-    p->last = !p->both && max_len <= 1024;
     p->pre_rw = (int)PW;
     o.groups = (int)groups;
     o.whole = false;
@@ -582,24 +581,37 @@ bool kv_prefix_plan(int64_t R, int64_t M, int64_t Hkv, int64_t G, int64_t D, int
     if (!o.aligned) o.slots *= 2;
     o.part_slots = o.slots + (o.aligned ? 0 : starts);
     o.head_bytes = PART_HEAD;
-    if (p->last) {
-        o.slots = (int)starts;  // a workgroup for each (request, head, row group)
-        o.part_slots = o.head_bytes = 0;
-    }
     p->own_starts = (int)starts;
-    // the prefix's: parts of at least 8 steps, as many as fill the GPU best
+    // the prefix's: parts of at least 3 steps, as many as cost least: rounds of
+    // workgroups, each of its steps and of about 12 more of first loads and
+    // last sums (6 or 20 made no difference).  Requests that are not cut join the
+    // prefix's segments themselves, a launch and a pass over segments less,
+    // where contexts are short, or many requests of one row tile fill the GPU:
+    // about two steps for each segment of a wave, against 28.
+    // Measured, 8 heads of 128 behind 2048 tokens, this against a line of the
+    // requests' own and a join: 32 requests of 40 tokens 20.1 us against 30.6,
+    // 48 of 1000 39.8 against 49.1, 48 of 4000 86.8 against 95, 48 of 8192 158
+    // against 151, 256 of 40 97 against 86; 16 of 16 drafts and 500 tokens 51.6
+    // against 60.9, 2000 80.8 against 72.4; 8 of 300, heads of 256, behind
+    // 131072 tokens (128 segments) 55 us against 25.
     KvAttnPlan &q = p->pre;
     const int64_t pairs = Hkv * pgroups, fit = 256 * (w.many ? (w.NR == 1 && D == 128 ? 3 : 8 / w.RS) : w.NR == 1 && D <= 128 ? 3 : 2);
     if (pairs * (steps + 1) >= (int64_t(1) << 31) - 65536) return false;
-    const int64_t longest = steps / 8 > 1 ? steps / 8 : 1, upto = longest < 4 * fit / pairs ? longest : 4 * fit / pairs;
+    const int split = v.NR == 1 && D <= 128 ? 8 : 4 / v.RS;  // waves that share a request's segments
+    const bool whole = !p->both && starts <= 1024 && (max_len <= 1024 || (split == 8 && starts >= 128 && max_len <= 4096));
+    const int64_t longest = steps / 3 > 1 ? steps / 3 : 1, upto = longest < 4 * fit / pairs ? longest : 4 * fit / pairs;
     int64_t best = 1;
     double least = 1e30;
-    for (int64_t k = 1; k <= upto; ++k) {
-        // rounds of workgroups, each of its steps and of about 12 more of first loads and last sums
-        const double cost = (double)((pairs * k + fit - 1) / fit) * ((double)((steps + k - 1) / k) + 12.0);
-        if (cost < least) {
-            least = cost;
+    p->last = false;
+    for (int64_t k = 1; k <= (upto > 1 ? upto : 1); ++k) {
+        const double cost = (double)((pairs * k + fit - 1) / fit) * ((double)((steps + k - 1) / k) + 12.0) +
+                            (double)(Hkv * all * k * D) * 8.0 / 5e6;
+        const double fold = 2.0 + 2.0 * (double)k / split;
+        const bool last = whole && fold < 28.0;
+        if (cost + (last ? fold : 28.0) < least) {
+            least = cost + (last ? fold : 28.0);
             best = k;
+            p->last = last;
         }
     }
     p->cuts = (int)best;
@@ -611,6 +623,10 @@ bool kv_prefix_plan(int64_t R, int64_t M, int64_t Hkv, int64_t G, int64_t D, int
     q.aligned = true;
     q.part_slots = q.slots;
     q.head_bytes = p->both ? 0 : PART_HEAD;
+    if (p->last) {
+        o.slots = (int)starts;  // a workgroup for each (request, head, row group)
+        o.part_slots = o.head_bytes = 0;
+    }
     const auto bytes = [&](const KvAttnPlan &l) { return (size_t)l.part_slots * (size_t)l.part_rows * (size_t)(D + 2) * 4; };
     const auto up = [](size_t n) { return (n + 255) / 256 * 256; };
     p->own_part = up((size_t)(o.head_bytes + q.head_bytes));
