@@ -560,7 +560,7 @@ void run(const KvAttnArgs &own, const KvAttnArgs &pre, const KvPrefixPlan &p, hi
 
 bool kv_prefix_plan(int64_t R, int64_t M, int64_t Hkv, int64_t G, int64_t D, int64_t max_q, int64_t max_len,
                     int64_t max_prefix, KvPrefixPlan *p) {
-    const int64_t rows = max_q * G, all = M * G, steps = (max_prefix + KV_STEP - 1) / KV_STEP;
+    const int64_t rows = max_q * G, all = M > 0 ? M * G : 1, steps = (max_prefix + KV_STEP - 1) / KV_STEP;
     const Shape v = shape_of((int)D, rows);
     const PrefixShape w = prefix_shape((int)D, all);
     const int64_t RW = 16 * v.NR * v.RS, PW = 16 * w.NR * w.RS;
