@@ -235,6 +235,7 @@ __global__ void __launch_bounds__(TH) sample_top_kernel(SampleArgs a) {
             a.counts[(size_t)m * NB + i] = 0;
         }
     }
+    if (c == 0 && tid == 0) a.rows[m].listed = 0;
     float top = NEG_INF;
 #pragma unroll
     for (int e = 0; e < E; ++e) top = fmaxf(top, x[e]);  // (past NaN)
@@ -425,58 +426,29 @@ __device__ __forceinline__ void load_kept(const SampleArgs &a, int m, bool there
         kept[i] = there && (int)threadIdx.x < a.chunks ? a.kept[((size_t)m * a.chunks + threadIdx.x) * SAMPLE_SUBS + i] : 0;
 }
 
-template <bool F32>
-__global__ void __launch_bounds__(TH) sample_find_kernel(SampleArgs a) {
-    __shared__ Shared sh;
-    constexpr int PER = NB / TH;
-    const int m = blockIdx.x, tid = threadIdx.x;
-    SampleRow *row = a.rows + m;
-    const Ask q = ask_of(a, m);
-    const bool filters = !q.greedy && q.filters();
-    u64 mass[PER], sum = 0;  // of PER consecutive bins
+// Finds the bins of a row's borders, by the whole workgroup; false where there
+// are none to find: the row's token is its largest, or hangs on its kept masses
+// alone.
+__device__ __forceinline__ bool find_borders(const SampleArgs &a, int m, const Ask &q, float top, SampleRow &r, Shared &sh) {
+    constexpr int PER = NB / TH;  // consecutive bins a thread
+    const int tid = threadIdx.x;
+    if (q.greedy || !q.filters() || top == NEG_INF) return false;
+    u64 mass[PER], sum = 0;
     unsigned count[PER], n = 0;
-    if (filters) {
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            mass[i] = a.masses[(size_t)m * NB + tid * PER + i];
-            count[i] = a.counts[(size_t)m * NB + tid * PER + i];
-            sum += mass[i];
-            n += count[i];
-        }
-    }
-    u64 kept[SAMPLE_SUBS];
-    load_kept(a, m, !q.greedy && !filters, kept);
-    make_powers(sh.pow);
-    float mine;
-    const float top = top_of(a, m, mine, sh.wavef);
-    const bool none = top == NEG_INF;  // of finite or infinite logits
-    if (q.greedy || none || !filters) {
-        if (tid == 0) {
-            sh.found32[0] = 0x7FFFFFFF;
-            row->done = 1;
-        }
-        __syncthreads();
-        if (!q.greedy) {
-            if (none)
-                for (u64 &k : kept) k = 0;
-            pick<F32>(a, m, q, top, kept, nullptr, Cut{0, 0, 0}, nullptr, 0, sh);
-            return;
-        }
-        if (tid < a.chunks && mine == top) atomicMin(&sh.found32[0], (unsigned)a.top_at[(size_t)m * a.chunks + tid]);
-        __syncthreads();
-        if (tid == 0) {
-            a.tokens[m] = none ? -1 : (int)sh.found32[0];
-            if (a.logprobs) a.logprobs[m] = none ? __builtin_nanf("") : 0.f;
-        }
-        return;
+    for (int i = 0; i < PER; ++i) {
+        mass[i] = a.masses[(size_t)m * NB + tid * PER + i];
+        count[i] = a.counts[(size_t)m * NB + tid * PER + i];
+        sum += mass[i];
+        n += count[i];
     }
     u64 total;
     unsigned tokens;
     const u64 mass_before = scan_before(sum, sh.wave64, total);
     const unsigned count_before = scan_before(n, sh.wave32, tokens);
     if (tid == 0) {
-        sh.found64[0] = sh.found64[1] = total;  // mass before top-k's bin, and with it
-        sh.found32[2] = sh.found32[3] = NB - 1;      // top-p's bins
+        sh.found64[0] = sh.found64[1] = total;   // mass before top-k's bin, and with it
+        sh.found32[2] = sh.found32[3] = NB - 1;  // top-p's bins
     }
     __syncthreads();
     const bool by_k = q.k > 0 && (unsigned)q.k < tokens;  // (tokens: without NaN)
@@ -497,9 +469,9 @@ __global__ void __launch_bounds__(TH) sample_find_kernel(SampleArgs a) {
     }
     __syncthreads();
     const u64 lo = sh.found64[0], hi = sh.found64[1];  // top-k's mass lies between
-    const int k_bin = by_k ? (int)sh.found32[0] : -1;
-    const unsigned k_left = sh.found32[1];
     const bool by_p = q.p < 1.0;
+    r.k_bin = by_k ? (int)sh.found32[0] : -1;
+    r.k_left = by_k ? sh.found32[1] : 0;
     __syncthreads();
     if (by_p) {
         const u64 want_lo = max((u64)ceil(q.p * (double)lo), (u64)1), want_hi = max((u64)ceil(q.p * (double)hi), (u64)1);
@@ -515,39 +487,94 @@ __global__ void __launch_bounds__(TH) sample_find_kernel(SampleArgs a) {
         }
     }
     __syncthreads();
+    r.done = 0;
+    r.listed = r.pad = 0;
+    r.pad2 = 0;
+    r.p_lo = by_p ? (int)sh.found32[2] : NB;
+    r.p_hi = by_p ? (int)sh.found32[3] : -1;
+    r.full = by_p ? r.p_lo : by_k ? r.k_bin : NB;
+    r.p_mass = sh.found64[0];
+    r.k_mass = lo;
+    r.mass = total;
+    return true;
+}
+
+// A row without borders: its token.
+template <bool F32>
+__device__ __forceinline__ void finish_row(const SampleArgs &a, int m, const Ask &q, float top, float mine, Shared &sh) {
+    const int tid = threadIdx.x;
+    const bool none = top == NEG_INF;  // of finite or infinite logits
     if (tid == 0) {
-        SampleRow r;
-        r.done = 0;
-        r.p_lo = by_p ? (int)sh.found32[2] : NB;
-        r.p_hi = by_p ? (int)sh.found32[3] : -1;
-        r.full = by_p ? r.p_lo : by_k ? k_bin : NB;
-        r.k_bin = k_bin;
-        r.k_left = k_left;
-        r.listed = 0;
-        r.pad = 0;
-        r.p_mass = sh.found64[0];
-        r.k_mass = lo;
-        r.mass = total;
-        r.pad2 = 0;
-        *row = r;
+        sh.found32[0] = 0x7FFFFFFF;
+        a.rows[m].done = 1;
+    }
+    __syncthreads();
+    if (!q.greedy) {
+        u64 kept[SAMPLE_SUBS];
+        load_kept(a, m, !none, kept);
+        pick<F32>(a, m, q, top, kept, nullptr, Cut{0, 0, 0}, nullptr, 0, sh);
+        return;
+    }
+    if (tid < a.chunks && mine == top) atomicMin(&sh.found32[0], (unsigned)a.top_at[(size_t)m * a.chunks + tid]);
+    __syncthreads();
+    if (tid == 0) {
+        a.tokens[m] = none ? -1 : (int)sh.found32[0];
+        if (a.logprobs) a.logprobs[m] = none ? __builtin_nanf("") : 0.f;
+    }
+}
+
+template <bool F32>
+__global__ void __launch_bounds__(TH) sample_find_kernel(SampleArgs a) {
+    __shared__ Shared sh;
+    const int m = blockIdx.x;
+    const Ask q = ask_of(a, m);
+    make_powers(sh.pow);
+    float mine;
+    const float top = top_of(a, m, mine, sh.wavef);
+    SampleRow r;
+    if (!find_borders(a, m, q, top, r, sh)) {
+        finish_row<F32>(a, m, q, top, mine, sh);
+    } else if (threadIdx.x == 0) {
+        a.rows[m] = r;
     }
 }
 
 // ------------------------------------------------------------------ the list
-template <bool F32>
+// FIND: the borders' bins are found by each of a row's workgroups for itself,
+// and left for the next kernel by the first, which also ends rows without.
+template <bool F32, bool FIND>
 __global__ void __launch_bounds__(TH) sample_list_kernel(SampleArgs a) {
-    __shared__ double pow[32];
-    __shared__ u64 waves[TH / 64];
+    __shared__ Shared sh;
     __shared__ unsigned first;
     const int c = blockIdx.x % a.chunks, m = blockIdx.x / a.chunks, tid = threadIdx.x;
-    const SampleRow r = a.rows[m];
-    if (!a.few && r.done) return;
+    SampleRow r;
+    if (!FIND) {
+        r = a.rows[m];
+        if (r.done) return;
+    }
     const Ask q = ask_of(a, m);
     float x[E], mine;
     load_logits<F32>(a.logits, (int64_t)m * a.stride, c * SAMPLE_CHUNK + tid * E, a.V, x);
-    make_powers(pow);
-    if (r.done) return;
-    const float top = top_of(a, m, mine, (float *)waves);
+    make_powers(sh.pow);
+    const float top = top_of(a, m, mine, sh.wavef);
+    if (FIND) {
+        if (!find_borders(a, m, q, top, r, sh)) {
+            if (c == 0) finish_row<F32>(a, m, q, top, mine, sh);
+            return;
+        }
+        if (c == 0 && tid == 0) {
+            SampleRow *to = a.rows + m;  // (its count of the list is the others' already)
+            to->done = 0;
+            to->full = r.full;
+            to->p_lo = r.p_lo;
+            to->p_hi = r.p_hi;
+            to->k_bin = r.k_bin;
+            to->k_left = r.k_left;
+            to->p_mass = r.p_mass;
+            to->k_mass = r.k_mass;
+            to->mass = r.mass;
+        }
+    }
     u64 sum = 0;
     unsigned open = 0, n = 0;
 #pragma unroll
@@ -555,7 +582,7 @@ __global__ void __launch_bounds__(TH) sample_list_kernel(SampleArgs a) {
         if (!(x[e] == x[e])) continue;
         const int b = bin_of(x[e], top);
         if (b < r.full) {
-            const double v = weight(x[e], top, q.c, pow);
+            const double v = weight(x[e], top, q.c, sh.pow);
             sum += v >= q.minp ? mass_of(v) : 0;
         } else if (undecided(r, b)) {
             open |= 1u << e;
@@ -565,7 +592,7 @@ __global__ void __launch_bounds__(TH) sample_list_kernel(SampleArgs a) {
     sum = scan_wave(sum);
     if ((tid & 63) == 63) a.kept[((size_t)m * a.chunks + c) * SAMPLE_SUBS + tid / 64] = sum;
     unsigned all;
-    unsigned place = scan_before(n, (unsigned *)waves, all);
+    unsigned place = scan_before(n, sh.wave32, all);
     if (tid == 0) {
         // (chunks come in any order: what is made of the list does not depend on it)
         if (all > 0) first = atomicAdd(&a.rows[m].listed, all);
@@ -583,25 +610,44 @@ __global__ void __launch_bounds__(TH) sample_list_kernel(SampleArgs a) {
 }
 
 // ------------------------------------------------------------------ the borders, and the token
+// So many tokens are taken by rank, each against all others (of 256, that took
+// 6 us; a descent takes 5).
+constexpr unsigned BRIEF = 128;
+static_assert(BRIEF <= TH, "a token a thread");
+
+// Number and mass of the n tokens before `order`; few[] is filled up to a
+// multiple of four with tokens that come last.
+__device__ __forceinline__ u64 before_of(u64 order, const ulonglong2 *few, unsigned n, unsigned &rank) {
+    u64 mass = 0;
+    rank = 0;
+    for (unsigned j = 0; j < n; j += 4) {
+#pragma unroll
+        for (unsigned e = 0; e < 4; ++e) {
+            const ulonglong2 t = few[j + e];
+            rank += t.x > order;
+            mass += t.x > order ? t.y : 0;
+        }
+    }
+    return mass;
+}
+
 template <bool F32>
 __global__ void __launch_bounds__(TH) sample_pick_kernel(SampleArgs a) {
     __shared__ Shared sh;
-    __shared__ union {
-        u32x2_t list[SAMPLE_LIST];
-        u64 order[TH];  // of a short list
-    } ls;
+    __shared__ u32x2_t held[SAMPLE_LIST];
+    __shared__ ulonglong2 few[BRIEF + 4];  // a few tokens' order (larger: earlier) and mass
     const int m = blockIdx.x, tid = threadIdx.x;
     const SampleRow r = a.rows[m];
     if (r.done) return;
     const Ask q = ask_of(a, m);
     const u32x2_t *list = a.lists + (size_t)m * SAMPLE_LIST;
-    const bool brief = r.listed <= TH;  // a token of the list for each thread
+    const bool brief = r.listed <= BRIEF;  // a token of the list for each thread
     u32x2_t own = {0u, 0u};
     if (brief) {
         if ((unsigned)tid < r.listed) own = list[tid];
     } else if (r.listed <= SAMPLE_LIST) {
 #pragma unroll 8
-        for (unsigned i = tid; i < r.listed; i += TH) ls.list[i] = list[i];
+        for (unsigned i = tid; i < r.listed; i += TH) held[i] = list[i];
     }
     u64 kept[SAMPLE_SUBS];
     load_kept(a, m, true, kept);
@@ -616,18 +662,11 @@ __global__ void __launch_bounds__(TH) sample_pick_kernel(SampleArgs a) {
         const double v = valid ? weight(logit_of(own[0]), top, q.c, sh.pow) : 0.0;
         const u64 w = mass_of(v), order = ((u64)own[0] << 32) | ~own[1];  // larger: earlier
         const int b = valid ? bin_of(logit_of(own[0]), top) : NB;
-        ls.order[tid] = order;
-        sh.mass[tid] = w;
+        if (tid < (int)BRIEF + 4) few[tid] = valid ? ulonglong2{order, w} : ulonglong2{0, 0};
         if (tid == 0) sh.found64[0] = ~0ull;
         const unsigned sooner = (unsigned)__syncthreads_count(b < r.k_bin);  // listed, before top-k's bin
-        unsigned rank = 0;
-        u64 before = r.p_mass;
-        if (valid)
-            for (unsigned j = 0; j < r.listed; ++j) {
-                const bool first = ls.order[j] > order;
-                rank += first;
-                before += first ? sh.mass[j] : 0;
-            }
+        unsigned rank;
+        const u64 before = r.p_mass + before_of(order, few, r.listed, rank);
         bool keep = valid && (r.k_bin < 0 || rank < r.k_left + sooner);
         if (q.p < 1.0) {
             u64 mass = r.mass;  // what top-k keeps
@@ -652,12 +691,12 @@ __global__ void __launch_bounds__(TH) sample_pick_kernel(SampleArgs a) {
         return;
     }
 
-    // f(key, bin, part) for each undecided token
+    // f(key, bin, token) for each undecided token
     const auto each = [&](auto f) {
         if (r.listed <= SAMPLE_LIST) {
             for (unsigned i = tid; i < r.listed; i += TH) {
-                const u32x2_t t = ls.list[i];
-                f(t[0], bin_of(logit_of(t[0]), top), (int)(t[1] / SUB));
+                const u32x2_t t = held[i];
+                f(t[0], bin_of(logit_of(t[0]), top), t[1]);
             }
         } else {  // more than the list holds: from the logits again
             for (int i = tid; i < a.V; i += TH) {
@@ -665,18 +704,20 @@ __global__ void __launch_bounds__(TH) sample_pick_kernel(SampleArgs a) {
                 const float x = F32 ? ((const float *)a.logits)[at] : f32_of((unsigned)((const uint16_t *)a.logits)[at] << 16);
                 if (!(x == x)) continue;
                 const int b = bin_of(x, top);
-                if (undecided(r, b)) f(key_of(x), b, i / SUB);
+                if (undecided(r, b)) f(key_of(x), b, (unsigned)i);
             }
         }
     };
 
     // Among the undecided tokens that `in` takes, the largest first: where
     // `want` of them are together (or, by mass, where the mass with them reaches
-    // `want`).  Digits of 8 bits, from the first in which keys differ.
+    // `want`).  Digits of 8 bits, from the first in which keys differ, until
+    // a workgroup's threads can take a token each: those by rank and the mass
+    // before them.
     const auto descend = [&](auto by_mass, u64 want, auto in) {
         constexpr bool MASS = decltype(by_mass)::value;
         unsigned least = ~0u, most = 0;
-        each([&](unsigned key, int b, int) {
+        each([&](unsigned key, int b, unsigned) {
             if (in(key, b)) {
                 least = min(least, key);
                 most = max(most, key);
@@ -709,7 +750,7 @@ __global__ void __launch_bounds__(TH) sample_pick_kernel(SampleArgs a) {
             sh.mass[tid] = 0;
             sh.count[tid] = 0;
             __syncthreads();
-            each([&](unsigned key, int b, int) {
+            each([&](unsigned key, int b, unsigned) {
                 if (!in(key, b) || (bits < 32 && (key >> bits) != (prefix >> bits))) return;
                 const unsigned d = (DIGITS - 1) - ((key >> shift) & ((1u << (bits - shift)) - 1));
                 atomicAdd(&sh.count[d], 1u);
@@ -735,7 +776,32 @@ __global__ void __launch_bounds__(TH) sample_pick_kernel(SampleArgs a) {
             above = sh.found64[0];
             bits = shift;
             __syncthreads();
-        } while (bits > 0);
+        } while (bits > 0 && here > BRIEF);
+        if (bits > 0) {
+            if (tid == 0) {
+                sh.found32[0] = 0;
+                sh.found64[0] = ~0ull;
+            }
+            if (tid < (int)BRIEF + 4) few[tid] = ulonglong2{0, 0};
+            __syncthreads();
+            each([&](unsigned key, int b, unsigned token) {
+                if (!in(key, b) || key >> bits != prefix >> bits) return;
+                few[atomicAdd(&sh.found32[0], 1u)] = ulonglong2{((u64)key << 32) | ~token, MASS ? mass_at(key) : 1};
+            });
+            __syncthreads();
+            u64 last = ~0ull;
+            if ((unsigned)tid < here) {
+                const u64 order = few[tid].x;
+                unsigned rank;
+                if (above + before_of(order, few, here, rank) < want) last = order;
+            }
+#pragma unroll
+            for (int d = 32; d; d >>= 1) last = min(last, (u64)__shfl_xor(last, d));
+            if ((tid & 63) == 0) atomicMin(&sh.found64[0], last);
+            __syncthreads();
+            last = sh.found64[0];
+            return Cut{(unsigned)(last >> 32), ~(unsigned)last, ~0u};
+        }
         u64 ties = want - above;
         if (MASS) {
             const u64 w = mass_at(prefix);
@@ -751,15 +817,19 @@ __global__ void __launch_bounds__(TH) sample_pick_kernel(SampleArgs a) {
         cut = descend(std::false_type(), r.k_left, [&](unsigned, int b) { return b == r.k_bin; });
         if (q.p < 1.0) {
             u64 s = 0;
-            each([&](unsigned key, int b, int) { s += key > cut.key && b == r.k_bin ? mass_at(key) : 0; });
-            mass = r.k_mass + sum_all(s, sh.wave64) + (u64)cut.ties * mass_at(cut.key);
+            const bool by_token = cut.ties == ~0u;
+            each([&](unsigned key, int b, unsigned token) {
+                s += b == r.k_bin && (key > cut.key || (by_token && key == cut.key && token <= cut.token)) ? mass_at(key) : 0;
+            });
+            mass = r.k_mass + sum_all(s, sh.wave64) + (by_token ? 0 : (u64)cut.ties * mass_at(cut.key));
         }
     }
     if (q.p < 1.0) {
         const Cut k = cut;
         const u64 want = max((u64)ceil(q.p * (double)mass), (u64)1) - r.p_mass;
         cut = descend(std::true_type(), want, [&](unsigned key, int b) { return b >= r.p_lo && b <= r.p_hi && key >= k.key; });
-        if (r.k_bin >= 0 && cut.key <= k.key) cut = Cut{k.key, ~0u, cut.key == k.key ? min(cut.ties, k.ties) : k.ties};
+        if (r.k_bin >= 0 && cut.key <= k.key)
+            cut = cut.key == k.key ? Cut{k.key, min(cut.token, k.token), min(cut.ties, k.ties)} : k;
     }
     // what the chunks keep of their undecided tokens: those above the cut ...
     __syncthreads();
@@ -769,12 +839,12 @@ __global__ void __launch_bounds__(TH) sample_pick_kernel(SampleArgs a) {
         sh.count[i * TH + tid] = 0;
     }
     __syncthreads();
-    each([&](unsigned key, int, int part) {
+    each([&](unsigned key, int, unsigned token) {
         if (key > cut.key) {
             const double v = weight(logit_of(key), top, q.c, sh.pow);
-            if (v >= q.minp) atomicAdd(&sh.mass[part], mass_of(v));
-        } else if (key == cut.key) {
-            atomicAdd(&sh.count[part], 1u);
+            if (v >= q.minp) atomicAdd(&sh.mass[token / SUB], mass_of(v));
+        } else if (key == cut.key && token <= cut.token) {
+            atomicAdd(&sh.count[token / SUB], 1u);
         }
     });
     __syncthreads();
@@ -797,11 +867,15 @@ __global__ void __launch_bounds__(TH) sample_pick_kernel(SampleArgs a) {
 template <bool F32>
 void run(const SampleArgs &a, hipStream_t s) {
     const dim3 chunks((unsigned)((int64_t)a.M * a.chunks)), rows((unsigned)a.M);
+    const bool borders = a.top_k || a.top_p;
     hipLaunchKernelGGL((sample_top_kernel<F32>), chunks, dim3(TH), 0, s, a);
     hipLaunchKernelGGL((sample_bins_kernel<F32>), chunks, dim3(TH), 0, s, a);
-    hipLaunchKernelGGL((sample_find_kernel<F32>), rows, dim3(TH), 0, s, a);
-    if (!a.top_k && !a.top_p) return;
-    hipLaunchKernelGGL((sample_list_kernel<F32>), chunks, dim3(TH), 0, s, a);
+    if (!borders || !a.few) hipLaunchKernelGGL((sample_find_kernel<F32>), rows, dim3(TH), 0, s, a);
+    if (!borders) return;
+    if (a.few)
+        hipLaunchKernelGGL((sample_list_kernel<F32, true>), chunks, dim3(TH), 0, s, a);
+    else
+        hipLaunchKernelGGL((sample_list_kernel<F32, false>), chunks, dim3(TH), 0, s, a);
     hipLaunchKernelGGL((sample_pick_kernel<F32>), rows, dim3(TH), 0, s, a);
 }
 
