@@ -72,8 +72,8 @@ bool sample_layout(int64_t M, int64_t V, SampleLayout *l) {
     l->masses = take(8 * SAMPLE_BINS);
     l->counts = take(4 * SAMPLE_BINS);
     l->kept = take(8 * C * SAMPLE_SUBS);
-    l->tops = take(4 * C);
-    l->top_at = take(4 * C);
+    l->tops = take(4 * C * SAMPLE_SUBS);
+    l->top_at = take(4 * C * SAMPLE_SUBS);
     l->lists = take(8 * SAMPLE_LIST);
     l->bytes = at;
     return true;

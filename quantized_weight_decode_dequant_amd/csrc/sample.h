@@ -23,7 +23,7 @@ struct SampleRow {
     int k_bin;                  // the bin of top-k's border (-1: none)
     unsigned k_left;            // tokens of k_bin that top-k keeps
     unsigned listed;            // undecided tokens (those in the border's bins)
-    unsigned pad;
+    float top;                  // the row's largest logit
     unsigned long long p_mass;  // mass of the bins below p_lo
     unsigned long long k_mass;  // mass of the bins below k_bin
     unsigned long long mass;    // of all bins
@@ -42,8 +42,8 @@ struct SampleArgs {
     unsigned long long *masses;  // [M][SAMPLE_BINS]
     unsigned *counts;            // [M][SAMPLE_BINS]
     unsigned long long *kept;    // [M][chunks][SAMPLE_SUBS]: mass that is kept for sure
-    float *tops;                 // [M][chunks]: largest logit
-    int32_t *top_at;             // [M][chunks]: the first token that has it
+    float *tops;                 // [M][chunks][SAMPLE_SUBS]: largest logit
+    int32_t *top_at;             // [M][chunks][SAMPLE_SUBS]: the first token that has it (-1: all are NaN)
     u32x2_t *lists;              // [M][SAMPLE_LIST]: (key, token) of undecided tokens
     int M, V, chunks;
     bool few;  // workgroups than fill the GPU: read ahead of a row's settings

@@ -198,14 +198,19 @@ __device__ __forceinline__ float max_lane(float v) {
     return fmaxf(v, f32_of((unsigned)__builtin_amdgcn_update_dpp(u, u, CTRL, 0xF, 0xF, false)));
 }
 
-__device__ __forceinline__ float max_all(float v, float *waves) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+// The wave's largest, in its last lane.
+__device__ __forceinline__ float max_wave(float v) {
     v = max_lane<0x111>(v);
     v = max_lane<0x112>(v);
     v = max_lane<0x114>(v);
     v = max_lane<0x118>(v);
     v = max_lane<0x142>(v);
-    v = max_lane<0x143>(v);  // lane 63 has the wave's
+    return max_lane<0x143>(v);
+}
+
+__device__ __forceinline__ float max_all(float v, float *waves) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    v = max_wave(v);
     __syncthreads();
     if (lane == 63) waves[wave] = v;
     __syncthreads();
@@ -217,15 +222,17 @@ __device__ __forceinline__ float max_all(float v, float *waves) {
 
 // A row's largest logit, from its chunks'.
 __device__ __forceinline__ float top_of(const SampleArgs &a, int m, float &mine, float *waves) {
-    mine = (int)threadIdx.x < a.chunks ? a.tops[(size_t)m * a.chunks + threadIdx.x] : NEG_INF;
+    mine = NEG_INF;
+    if ((int)threadIdx.x < a.chunks) {
+        const f32x4_t t = *reinterpret_cast<const f32x4_t *>(a.tops + ((size_t)m * a.chunks + threadIdx.x) * SAMPLE_SUBS);
+        mine = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+    }
     return max_all(mine, waves);
 }
 
 // ------------------------------------------------------------------ the chunks' largest
 template <bool F32>
 __global__ void __launch_bounds__(TH) sample_top_kernel(SampleArgs a) {
-    __shared__ float waves[TH / 64];
-    __shared__ unsigned first;
     const int c = blockIdx.x % a.chunks, m = blockIdx.x / a.chunks, tid = threadIdx.x;
     float x[E];
     load_logits<F32>(a.logits, (int64_t)m * a.stride, c * SAMPLE_CHUNK + tid * E, a.V, x);
@@ -239,17 +246,16 @@ __global__ void __launch_bounds__(TH) sample_top_kernel(SampleArgs a) {
     float top = NEG_INF;
 #pragma unroll
     for (int e = 0; e < E; ++e) top = fmaxf(top, x[e]);  // (past NaN)
-    if (tid == 0) first = 0x7FFFFFFF;
-    top = max_all(top, waves);
-    int at = 0x7FFFFFFF;
+    top = f32_of((unsigned)__builtin_amdgcn_readlane((int)bits_of(max_wave(top)), 63));
+    int at = -1;
 #pragma unroll
     for (int e = E - 1; e >= 0; --e)
         if (x[e] == top) at = c * SAMPLE_CHUNK + tid * E + e;
-    if (at != 0x7FFFFFFF) atomicMin(&first, (unsigned)at);
-    __syncthreads();
-    if (tid == 0) {
-        a.tops[(size_t)m * a.chunks + c] = top;
-        a.top_at[(size_t)m * a.chunks + c] = (int)first;
+    const unsigned long long has = __ballot(at >= 0);
+    if ((tid & 63) == (has ? (int)__builtin_ctzll(has) : 0)) {
+        const size_t part = ((size_t)m * a.chunks + c) * SAMPLE_SUBS + tid / 64;
+        a.tops[part] = top;
+        a.top_at[part] = at;
     }
 }
 
@@ -488,7 +494,8 @@ __device__ __forceinline__ bool find_borders(const SampleArgs &a, int m, const A
     }
     __syncthreads();
     r.done = 0;
-    r.listed = r.pad = 0;
+    r.listed = 0;
+    r.top = top;
     r.pad2 = 0;
     r.p_lo = by_p ? (int)sh.found32[2] : NB;
     r.p_hi = by_p ? (int)sh.found32[3] : -1;
@@ -515,7 +522,13 @@ __device__ __forceinline__ void finish_row(const SampleArgs &a, int m, const Ask
         pick<F32>(a, m, q, top, kept, nullptr, Cut{0, 0, 0}, nullptr, 0, sh);
         return;
     }
-    if (tid < a.chunks && mine == top) atomicMin(&sh.found32[0], (unsigned)a.top_at[(size_t)m * a.chunks + tid]);
+    if (tid < a.chunks && mine == top) {
+#pragma unroll
+        for (int i = SAMPLE_SUBS - 1; i >= 0; --i) {
+            const size_t part = ((size_t)m * a.chunks + tid) * SAMPLE_SUBS + i;
+            if (a.tops[part] == top && a.top_at[part] >= 0) atomicMin(&sh.found32[0], (unsigned)a.top_at[part]);
+        }
+    }
     __syncthreads();
     if (tid == 0) {
         a.tokens[m] = none ? -1 : (int)sh.found32[0];
@@ -548,15 +561,41 @@ __global__ void __launch_bounds__(TH) sample_list_kernel(SampleArgs a) {
     __shared__ unsigned first;
     const int c = blockIdx.x % a.chunks, m = blockIdx.x / a.chunks, tid = threadIdx.x;
     SampleRow r;
-    if (!FIND) {
+    Ask q;
+    float x[E], top, mine;
+    if (FIND) {
+        q = ask_of(a, m);
+        load_logits<F32>(a.logits, (int64_t)m * a.stride, c * SAMPLE_CHUNK + tid * E, a.V, x);
+        top = top_of(a, m, mine, sh.wavef);
+    } else {
         r = a.rows[m];
         if (r.done) return;
+        q = ask_of(a, m);
+        top = r.top;
+        // a wave, or a workgroup, whose largest lies behind all borders has nothing
+        // to read
+        const size_t part = ((size_t)m * a.chunks + c) * SAMPLE_SUBS;
+        const int last = max(max(r.p_hi, r.k_bin), r.full - 1);
+        bool any = false, mine_any = false;
+#pragma unroll
+        for (int i = 0; i < SAMPLE_SUBS; ++i) {
+            const bool has = bin_of(a.tops[part + i], top) <= last;
+            any |= has;
+            if (i == __builtin_amdgcn_readfirstlane(tid / 64)) mine_any = has;
+        }
+        if (!any) {
+            if (tid < SAMPLE_SUBS) a.kept[part + tid] = 0;
+            return;
+        }
+        if (mine_any) {
+            load_logits<F32>(a.logits, (int64_t)m * a.stride, c * SAMPLE_CHUNK + tid * E, a.V, x);
+        } else {
+#pragma unroll
+            for (int e = 0; e < E; ++e) x[e] = __builtin_nanf("");
+        }
     }
-    const Ask q = ask_of(a, m);
-    float x[E], mine;
-    load_logits<F32>(a.logits, (int64_t)m * a.stride, c * SAMPLE_CHUNK + tid * E, a.V, x);
     make_powers(sh.pow);
-    const float top = top_of(a, m, mine, sh.wavef);
+    __syncthreads();
     if (FIND) {
         if (!find_borders(a, m, q, top, r, sh)) {
             if (c == 0) finish_row<F32>(a, m, q, top, mine, sh);
@@ -565,6 +604,7 @@ __global__ void __launch_bounds__(TH) sample_list_kernel(SampleArgs a) {
         if (c == 0 && tid == 0) {
             SampleRow *to = a.rows + m;  // (its count of the list is the others' already)
             to->done = 0;
+            to->top = top;
             to->full = r.full;
             to->p_lo = r.p_lo;
             to->p_hi = r.p_hi;
@@ -652,8 +692,8 @@ __global__ void __launch_bounds__(TH) sample_pick_kernel(SampleArgs a) {
     u64 kept[SAMPLE_SUBS];
     load_kept(a, m, true, kept);
     make_powers(sh.pow);
-    float mine;
-    const float top = top_of(a, m, mine, sh.wavef);
+    const float top = r.top;
+    __syncthreads();
     const auto mass_at = [&](unsigned key) { return mass_of(weight(logit_of(key), top, q.c, sh.pow)); };
 
     if (brief) {
