@@ -109,11 +109,37 @@ __device__ __forceinline__ void make_powers(double *pow) {
     if (threadIdx.x < 32) pow[threadIdx.x] = exp2(-(double)threadIdx.x * 0.03125);
 }
 
+// Logits as a row sees them, relative to its largest: `top`, what makes them
+// finite where that is infinite, and from which distance on (in halves, which
+// cannot overflow) a weight is below half of its unit: such tokens, NaN and
+// -infinity among them, are dead, they are never drawn and do not count.
+struct Scale {
+    float top, half_top, reach;
+    bool infinite;
+    __device__ __forceinline__ float distance(float x) const { return fmaf(-0.5f, x, half_top); }
+    __device__ __forceinline__ bool dead(float d) const { return !(d <= reach); }
+    template <int n>
+    __device__ __forceinline__ void settle(float (&x)[n]) const {
+        if (infinite) {
+#pragma unroll
+            for (int e = 0; e < n; ++e) x[e] = x[e] == -NEG_INF ? 0.f : NEG_INF;
+        }
+    }
+};
+
+__device__ __forceinline__ Scale scale_of(float top, const Ask &q) {
+    Scale s;
+    s.infinite = top == -NEG_INF;
+    s.top = s.infinite ? 0.f : top;
+    s.half_top = 0.5f * s.top;
+    s.reach = fminf((float)(22.0 / q.c), 3.4e38f);
+    return s;
+}
+
 // exp((x - top) / T): 2^-t by t = (32 n + j) / 32 + rest, |rest| <= 1/64, the
 // rest's power by its series to the fifth order (2e-15).  0 of NaN.
 __device__ __forceinline__ double weight(float x, float top, double c, const double *pow) {
-    const double d = x == top ? 0.0 : (double)top - (double)x;
-    const double t = fmin(d * c, 1100.0);
+    const double t = fmin(((double)top - (double)x) * c, 1100.0);
     constexpr double MAGIC = 0x1.8p52, S = -0.69314718055994530942 / 32;
     const double y = fma(t, 32.0, MAGIC);
     const int n = (int)(unsigned)__builtin_bit_cast(u64, y);
@@ -138,11 +164,8 @@ __device__ __forceinline__ unsigned key_of(float x) {
 }
 __device__ __forceinline__ float logit_of(unsigned key) { return f32_of(key & 0x80000000u ? key ^ 0x80000000u : ~key); }
 
-// 128 bins to an octave of the distance from the top, from 1/16 on.
-__device__ __forceinline__ int bin_of(float x, float top) {
-    const float d = x == top ? 0.f : top - x;
-    return min(max((int)(bits_of(d) >> 16) - ((127 - 4) << 7), 0), NB - 1);
-}
+// 128 bins to an octave of the distance from the top, from 1/32 of halves on.
+__device__ __forceinline__ int bin_of(float d) { return min(max((int)(bits_of(d) >> 16) - ((127 - 5) << 7), 0), NB - 1); }
 
 // v of the lane that a DPP control names; 0 where it names none.
 template <int CTRL, int ROWS>
@@ -278,12 +301,14 @@ __global__ void __launch_bounds__(TH) sample_bins_kernel(SampleArgs a) {
         counts[i * TH + tid] = 0;
     }
     if (q.greedy) return;
-    const float top = top_of(a, m, mine, (float *)waves);
+    const Scale t = scale_of(top_of(a, m, mine, (float *)waves), q);
+    t.settle(x);
     if (!q.filters()) {
         u64 sum = 0;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            const double v = weight(x[e], top, q.c, pow);
+            if (t.dead(t.distance(x[e]))) continue;
+            const double v = weight(x[e], t.top, q.c, pow);
             sum += v >= q.minp ? mass_of(v) : 0;
         }
         sum = scan_wave(sum);
@@ -292,10 +317,11 @@ __global__ void __launch_bounds__(TH) sample_bins_kernel(SampleArgs a) {
     }
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-        if (x[e] == x[e]) {
-            const int b = bin_of(x[e], top);
+        const float d = t.distance(x[e]);
+        if (!t.dead(d)) {
+            const int b = bin_of(d);
             if (q.k > 0) atomicAdd(&counts[b], 1u);
-            if (q.p < 1.0) atomicAdd(&masses[b], mass_of(weight(x[e], top, q.c, pow)));
+            if (q.p < 1.0) atomicAdd(&masses[b], mass_of(weight(x[e], t.top, q.c, pow)));
         }
     }
     __syncthreads();
@@ -345,7 +371,7 @@ __device__ __forceinline__ bool undecided(const SampleRow &r, int b) {
 // and, where there are filters (`row`), their numbers of the cut key's tokens
 // (`ties`; `ties_before`: before chunk tid).
 template <bool F32>
-__device__ __forceinline__ void pick(const SampleArgs &a, int m, const Ask &q, float top, const u64 (&mine)[SAMPLE_SUBS], const SampleRow *row,
+__device__ __forceinline__ void pick(const SampleArgs &a, int m, const Ask &q, const Scale &s, const u64 (&mine)[SAMPLE_SUBS], const SampleRow *row,
                                      Cut cut, const unsigned *ties, unsigned ties_before, Shared &sh) {
     constexpr int PE = SUB / TH;
     const int tid = threadIdx.x;
@@ -379,11 +405,15 @@ __device__ __forceinline__ void pick(const SampleArgs &a, int m, const Ask &q, f
     r = sh.found64[0];
     float x[PE];
     load_logits<F32>(a.logits, (int64_t)m * a.stride, at, a.V, x);
+    s.settle(x);
     unsigned place = 0;  // of this thread's first token of the cut key among all
     if (by_ties) {
         unsigned n = 0, all;
 #pragma unroll
-        for (int e = 0; e < PE; ++e) n += x[e] == x[e] && key_of(x[e]) == cut.key && undecided(*row, bin_of(x[e], top));
+        for (int e = 0; e < PE; ++e) {
+            const float d = s.distance(x[e]);
+            n += !s.dead(d) && key_of(x[e]) == cut.key && undecided(*row, bin_of(d));
+        }
         place = sh.found32[1];
         place += scan_before(n, sh.wave32, all);
     }
@@ -392,20 +422,21 @@ __device__ __forceinline__ void pick(const SampleArgs &a, int m, const Ask &q, f
     sum = 0;
 #pragma unroll
     for (int e = 0; e < PE; ++e) {
-        v[e] = weight(x[e], top, q.c, sh.pow);
-        bool keep = v[e] >= q.minp;
-        if (row && x[e] == x[e]) {
-            const int b = bin_of(x[e], top);
+        v[e] = weight(x[e], s.top, q.c, sh.pow);
+        const float d = s.distance(x[e]);
+        bool keep = v[e] >= q.minp && !s.dead(d);
+        if (row && keep) {
+            const int b = bin_of(d);
             const unsigned key = key_of(x[e]);
             if (undecided(*row, b)) {
                 const bool tie = key == cut.key;
-                keep &= key > cut.key || (tie && (unsigned)(at + e) <= cut.token && place < cut.ties);
+                keep = key > cut.key || (tie && (unsigned)(at + e) <= cut.token && place < cut.ties);
                 place += by_ties && tie;
             } else {
-                keep &= b < row->full;
+                keep = b < row->full;
             }
         }
-        w[e] = keep && x[e] == x[e] ? mass_of(v[e]) : 0;
+        w[e] = keep ? mass_of(v[e]) : 0;
         sum += w[e];
     }
     u64 from = scan_before(sum, sh.wave64, sum);
@@ -457,7 +488,7 @@ __device__ __forceinline__ bool find_borders(const SampleArgs &a, int m, const A
         sh.found32[2] = sh.found32[3] = NB - 1;  // top-p's bins
     }
     __syncthreads();
-    const bool by_k = q.k > 0 && (unsigned)q.k < tokens;  // (tokens: without NaN)
+    const bool by_k = q.k > 0 && (unsigned)q.k < tokens;  // (of those that are not dead)
     if (by_k) {
         u64 s = mass_before;
         unsigned k = count_before;
@@ -519,7 +550,7 @@ __device__ __forceinline__ void finish_row(const SampleArgs &a, int m, const Ask
     if (!q.greedy) {
         u64 kept[SAMPLE_SUBS];
         load_kept(a, m, !none, kept);
-        pick<F32>(a, m, q, top, kept, nullptr, Cut{0, 0, 0}, nullptr, 0, sh);
+        pick<F32>(a, m, q, scale_of(top, q), kept, nullptr, Cut{0, 0, 0}, nullptr, 0, sh);
         return;
     }
     if (tid < a.chunks && mine == top) {
@@ -574,12 +605,14 @@ __global__ void __launch_bounds__(TH) sample_list_kernel(SampleArgs a) {
         top = r.top;
         // a wave, or a workgroup, whose largest lies behind all borders has nothing
         // to read
+        const Scale t = scale_of(top, q);
         const size_t part = ((size_t)m * a.chunks + c) * SAMPLE_SUBS;
         const int last = max(max(r.p_hi, r.k_bin), r.full - 1);
         bool any = false, mine_any = false;
 #pragma unroll
         for (int i = 0; i < SAMPLE_SUBS; ++i) {
-            const bool has = bin_of(a.tops[part + i], top) <= last;
+            const float d = t.infinite ? (a.tops[part + i] == top ? 0.f : -NEG_INF) : t.distance(a.tops[part + i]);
+            const bool has = !t.dead(d) && bin_of(d) <= last;
             any |= has;
             if (i == __builtin_amdgcn_readfirstlane(tid / 64)) mine_any = has;
         }
@@ -615,14 +648,17 @@ __global__ void __launch_bounds__(TH) sample_list_kernel(SampleArgs a) {
             to->mass = r.mass;
         }
     }
+    const Scale t = scale_of(top, q);
+    t.settle(x);
     u64 sum = 0;
     unsigned open = 0, n = 0;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-        if (!(x[e] == x[e])) continue;
-        const int b = bin_of(x[e], top);
+        const float d = t.distance(x[e]);
+        if (t.dead(d)) continue;
+        const int b = bin_of(d);
         if (b < r.full) {
-            const double v = weight(x[e], top, q.c, sh.pow);
+            const double v = weight(x[e], t.top, q.c, sh.pow);
             sum += v >= q.minp ? mass_of(v) : 0;
         } else if (undecided(r, b)) {
             open |= 1u << e;
@@ -692,16 +728,17 @@ __global__ void __launch_bounds__(TH) sample_pick_kernel(SampleArgs a) {
     u64 kept[SAMPLE_SUBS];
     load_kept(a, m, true, kept);
     make_powers(sh.pow);
-    const float top = r.top;
+    const Scale t = scale_of(r.top, q);
     __syncthreads();
-    const auto mass_at = [&](unsigned key) { return mass_of(weight(logit_of(key), top, q.c, sh.pow)); };
+    const auto mass_at = [&](unsigned key) { return mass_of(weight(logit_of(key), t.top, q.c, sh.pow)); };
+    const auto bin_at = [&](unsigned key) { return bin_of(t.distance(logit_of(key))); };
 
     if (brief) {
         // every token's rank and the mass before it, against all others
         const bool valid = (unsigned)tid < r.listed;
-        const double v = valid ? weight(logit_of(own[0]), top, q.c, sh.pow) : 0.0;
+        const double v = valid ? weight(logit_of(own[0]), t.top, q.c, sh.pow) : 0.0;
         const u64 w = mass_of(v), order = ((u64)own[0] << 32) | ~own[1];  // larger: earlier
-        const int b = valid ? bin_of(logit_of(own[0]), top) : NB;
+        const int b = valid ? bin_at(own[0]) : NB;
         if (tid < (int)BRIEF + 4) few[tid] = valid ? ulonglong2{order, w} : ulonglong2{0, 0};
         if (tid == 0) sh.found64[0] = ~0ull;
         const unsigned sooner = (unsigned)__syncthreads_count(b < r.k_bin);  // listed, before top-k's bin
@@ -727,7 +764,7 @@ __global__ void __launch_bounds__(TH) sample_pick_kernel(SampleArgs a) {
         last = sh.found64[0];
 #pragma unroll
         for (int i = 0; i < SAMPLE_SUBS; ++i) kept[i] += sh.mass[tid * SAMPLE_SUBS + i];
-        pick<F32>(a, m, q, top, kept, &r, Cut{(unsigned)(last >> 32), ~(unsigned)last, ~0u}, nullptr, 0, sh);
+        pick<F32>(a, m, q, t, kept, &r, Cut{(unsigned)(last >> 32), ~(unsigned)last, ~0u}, nullptr, 0, sh);
         return;
     }
 
@@ -735,16 +772,16 @@ __global__ void __launch_bounds__(TH) sample_pick_kernel(SampleArgs a) {
     const auto each = [&](auto f) {
         if (r.listed <= SAMPLE_LIST) {
             for (unsigned i = tid; i < r.listed; i += TH) {
-                const u32x2_t t = held[i];
-                f(t[0], bin_of(logit_of(t[0]), top), t[1]);
+                const u32x2_t one = held[i];
+                f(one[0], bin_at(one[0]), one[1]);
             }
         } else {  // more than the list holds: from the logits again
             for (int i = tid; i < a.V; i += TH) {
                 const int64_t at = (int64_t)m * a.stride + i;
-                const float x = F32 ? ((const float *)a.logits)[at] : f32_of((unsigned)((const uint16_t *)a.logits)[at] << 16);
-                if (!(x == x)) continue;
-                const int b = bin_of(x, top);
-                if (undecided(r, b)) f(key_of(x), b, (unsigned)i);
+                float x[1] = {F32 ? ((const float *)a.logits)[at] : f32_of((unsigned)((const uint16_t *)a.logits)[at] << 16)};
+                t.settle(x);
+                const float d = t.distance(x[0]);
+                if (!t.dead(d) && undecided(r, bin_of(d))) f(key_of(x[0]), bin_of(d), (unsigned)i);
             }
         }
     };
@@ -881,7 +918,7 @@ __global__ void __launch_bounds__(TH) sample_pick_kernel(SampleArgs a) {
     __syncthreads();
     each([&](unsigned key, int, unsigned token) {
         if (key > cut.key) {
-            const double v = weight(logit_of(key), top, q.c, sh.pow);
+            const double v = weight(logit_of(key), t.top, q.c, sh.pow);
             if (v >= q.minp) atomicAdd(&sh.mass[token / SUB], mass_of(v));
         } else if (key == cut.key && token <= cut.token) {
             atomicAdd(&sh.count[token / SUB], 1u);
@@ -893,7 +930,7 @@ __global__ void __launch_bounds__(TH) sample_pick_kernel(SampleArgs a) {
 #pragma unroll
     for (int i = 0; i < SAMPLE_SUBS; ++i) n += ties[i] = sh.count[tid * SAMPLE_SUBS + i];
     const unsigned ties_before = scan_before(n, sh.wave32, all);
-    const double v = weight(logit_of(cut.key), top, q.c, sh.pow);
+    const double v = weight(logit_of(cut.key), t.top, q.c, sh.pow);
     const u64 each_tie = v >= q.minp ? mass_of(v) : 0;
     n = ties_before;
 #pragma unroll
@@ -901,7 +938,7 @@ __global__ void __launch_bounds__(TH) sample_pick_kernel(SampleArgs a) {
         kept[i] += sh.mass[tid * SAMPLE_SUBS + i] + min(ties[i], n < cut.ties ? cut.ties - n : 0u) * each_tie;
         n += ties[i];
     }
-    pick<F32>(a, m, q, top, kept, &r, cut, ties, ties_before, sh);
+    pick<F32>(a, m, q, t, kept, &r, cut, ties, ties_before, sh);
 }
 
 template <bool F32>

@@ -240,3 +240,29 @@ def test_the_binding_refuses():
     with pytest.raises(pkg.QGError) as e:
         pkg.sample_run(x, u, workspace=torch.empty(64, dtype=torch.uint8, device=DEV))
     assert e.value.status == pkg.QG_ESIZE
+
+
+@pytest.mark.parametrize("fill", [float("-inf"), -3e38, -1e4])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_masks_that_leave_fewer_tokens_than_a_filter_asks_for(fill, dtype):
+    """A grammar's mask: 30 of 40001 tokens left, top-k 50: they all stay in, and nothing masked is drawn."""
+    M, V = 6, 40001
+    x = torch.full((M, V), fill).to(dtype)
+    g = torch.Generator().manual_seed(2)
+    at = torch.stack([torch.randperm(V, generator=g)[:30] for _ in range(M)])
+    x.scatter_(1, at, (3 * torch.randn(M, 30, generator=g)).to(dtype))
+    u = np.random.default_rng(5).random(M)
+    u[0] = 0.9999999
+    for kw in (dict(k=[50] * M), dict(k=[50] * M, p=[0.9] * M), dict(p=[0.999999] * M), dict(), dict(k=[30] * M, p=[0.5] * M), dict(k=[31] * M, minp=[0.01] * M)):
+        got, _ = check(x.to(DEV), u, **kw)
+        assert all(int(got[m]) in at[m] for m in range(M))
+
+
+def test_tokens_far_below_the_largest():
+    """Weights around the last one that counts, 2^-44 of the largest, at many temperatures."""
+    x = torch.linspace(0, -60, 5000)[None].repeat(6, 1).to(DEV)
+    u = np.array([0.0, 0.5, 0.9, 0.99999, 0.9999999, 1.0])
+    for T in (0.05, 0.5, 1.0, 1.9, 3.0):
+        for kw in (dict(), dict(k=[4900] * 6), dict(k=[4900] * 6, p=[0.9999] * 6), dict(p=[0.99] * 6)):
+            # (what lies below changes no sum by more than 2^-31 of it)
+            check(x, np.minimum(u, 1 - 2.0 ** -22), T=[T] * 6, **kw)
