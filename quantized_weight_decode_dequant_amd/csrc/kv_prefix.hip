@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(WAVES * 64, 2) kv_prefix_rows_kernel(KvAttnArg
         // meanwhile, and what comes two steps later is asked for.  Matrix
         // instructions take four times a vector instruction's time, so they are
         // spread: the next scores among the powers, the sums among the next
-        // scores' maxima.  `masked`: step i + 1 may end behind the last token.
+        // scores' maxima and the conversions.  `masked`: step i + 1 may end behind the last token.
         const auto step = [&](auto masked, u32x4_t(&st)[PW], int i) {
             const float lr = readlane_f(my_lr, page_of(i)), rr = readlane_f(my_rr, page_of(i));
             __syncthreads();
@@ -398,8 +398,6 @@ __global__ void __launch_bounds__(WAVES * 64, 2) kv_prefix_rows_kernel(KvAttnArg
                 if (q + HELD < NK) kf[q % HELD] = key(kb, q + HELD);
                 if (q >= NK - HELD) vf[q - (NK - HELD)] = key(vb, q - (NK - HELD));
             }
-            if (!decltype(masked)::value) store(masked, st, ahead);
-            load(st, ahead + 2);
             f16x8_t pf[NR];
 #pragma unroll
             for (int n = 0; n < NR; ++n) {
@@ -421,6 +419,8 @@ __global__ void __launch_bounds__(WAVES * 64, 2) kv_prefix_rows_kernel(KvAttnArg
                 __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
             }
             __builtin_amdgcn_sched_barrier(0);
+            if (!decltype(masked)::value) store(masked, st, ahead);
+            load(st, ahead + 2);
 #pragma unroll
             for (int d = 0; d < DT; ++d) {
 #pragma unroll
