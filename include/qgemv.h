@@ -739,7 +739,8 @@ size_t qg_kv_prefix_attention_workspace_bytes(int64_t R, int64_t M, int64_t Hq, 
  *               run at once, need one each.
  *  M            rows of q and out; M * Hq <= 2^26 - 8.  q_start[0] to q_start[R]
  *               are the rows held against the prefix; the others are left as
- *               they are.
+ *               they are.  (Rows outside that a q_start out of order gives to
+ *               a request see its own tokens only.)
  *  other arguments, rounding and limits as in kv_attention_run, without window:
  *               a part in the sense of its value scales is also a part of the
  *               prefix.  (The products of row groups, heads and tokens / 32, of

@@ -588,8 +588,8 @@ __global__ void __launch_bounds__(WAVES * 64, NR == 1 && D <= 128 && WAVES == 4 
         for (int n = 0; n < NR; ++n) {
             const int row = (rq.q0 - pq.q0) * a.G + min(row0 + 16 * (rsi * NR + n) + c, rows - 1);
             const int slot = (h * pgroups + row / a.pre_rw) * segs;
-            // (never so, unless another call wrote to the workspace in between)
-            if (slot < 0 || segs > a.pre_slots || slot > a.pre_slots - segs) continue;
+            // (so of q_start out of order only, or if another call wrote to the workspace)
+            if (row < 0 || row >= pq.T * a.G || segs > a.pre_slots || slot > a.pre_slots - segs) continue;
             const size_t at = (size_t)slot * a.pre_rows + row % a.pre_rw;
             for (int i = ts; i < segs; i += TS) {
                 const size_t from = at + (size_t)i * a.pre_rows;

@@ -29,7 +29,8 @@ struct Segments {
 __device__ __forceinline__ Segments segments_of(const KvAttnArgs &a, const Req &rq, int entry, int before, int len, int rw,
                                                 int head, int row, bool aligned, int per) {
     Segments s{0, 0, (size_t)a.part_rows};
-    if (rq.units <= 0) return s;
+    // (rows out of the entry's: of q_start out of order only)
+    if (rq.units <= 0 || row < 0 || row >= rq.T * a.G) return s;
     const int groups = (rq.T * a.G + rw - 1) / rw, pair = head * groups + row / rw;
     int slot;
     if (aligned) {
@@ -66,7 +67,7 @@ __global__ void __launch_bounds__(512) kv_prefix_join_kernel(KvPrefixJoinArgs p)
     const int head = hq / a.G, g = hq % a.G, prow = (rq.q0 - pq.q0 + j) * a.G + g;
     const Segments s = segments_of(p.own, rq, r, a.head[1 + r], max(a.head[0], 1), p.own_rw, head, j * a.G + g, a.aligned, a.Hkv * a.groups);
     Segments t = p.both ? segments_of(p.own, pq, a.R, a.head[1 + a.R], max(a.head[0], 1), p.own_rw, head, prow, a.aligned, a.Hkv * a.groups)
-                        : pq.units > 0 ? segments_of(p.pre, pq, 0, 0, max(b.head[0], 1), p.pre_rw, head, prow, true, 0) : Segments{0, 0, 0};
+                        : segments_of(p.pre, pq, 0, 0, pq.units > 0 ? max(b.head[0], 1) : 1, p.pre_rw, head, prow, true, 0);
     const float *part = p.both ? a.part : b.part, *part_ml = p.both ? a.part_ml : b.part_ml;
     const int n = s.n + t.n;
     float mx = NEG_INF;

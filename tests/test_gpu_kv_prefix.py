@@ -294,6 +294,54 @@ def test_a_large_call_by_some_of_its_rows():
     c.check(got[torch.tensor(pick, device=DEV)])
 
 
+# the one line of work; the requests' own kernel joins; a kernel joins
+PLANS = [dict(lens=[1, 40, 7], T=[1, 1, 1], G=4), dict(lens=[5 + i for i in range(40)], T=[1] * 40, G=4),
+         dict(lens=[3000] * 3 + [5] * 3, T=[3] * 6, G=8, D=256)]
+
+
+@pytest.mark.parametrize("plan", range(3))
+@pytest.mark.parametrize("off", [1, 5])
+def test_rows_around_the_requests_are_left(plan, off):
+    """q_start[0] above 0, rows behind q_start[R]."""
+    c = Case(off, 700, **PLANS[plan])
+    a = c.args()
+    q = torch.randn((c.M + 2 * off,) + c.q.shape[1:], device=DEV).to(torch.bfloat16)
+    q[off: off + c.M] = a["q"]
+    out = torch.full(q.shape, 7.0, device=DEV)
+    pkg.kv_prefix_attention_run(c.cache(), **dict(a, q=q, q_start=a["q_start"] + off), out=out)
+    torch.cuda.synchronize()
+    c.check(out[off: off + c.M], f32=True)
+    assert torch.all(out[:off] == 7) and torch.all(out[off + c.M:] == 7)
+
+
+@pytest.mark.parametrize("plan", range(3))
+@pytest.mark.parametrize("q_start_of", ["first", "last"])
+def test_rows_out_of_order_see_no_prefix(plan, q_start_of):
+    """q_start that does not ascend: rows outside q_start[0]..q_start[R] are not held
+    against the prefix, and read nothing of its segments."""
+    c = Case(plan, 700, **PLANS[plan])
+    bad = c.q_start.copy()
+    if q_start_of == "first":
+        bad[0] = bad[2]  # request 0 has no rows, request 1 lies before the prefix's
+        lone, none = [1], [0]
+    else:
+        bad[-1] = bad[1]  # the last has no rows, those behind the first lie behind the prefix's
+        lone, none = list(range(1, len(c.T) - 1)), [len(c.T) - 1]
+    out = torch.full(c.q.shape, 7.0, device=DEV)
+    pkg.kv_prefix_attention_run(c.cache(), **dict(c.args(), q_start=i32(bad)), out=out)
+    torch.cuda.synchronize()
+    rows = lambda rs: torch.cat([torch.arange(c.q_start[r], c.q_start[r + 1]) for r in rs]).to(DEV)  # noqa: E731
+    assert torch.all(out[rows(none)] == 7)
+    def held(rs, P):
+        k = rows(rs)
+        d = Case(plan, 700, **PLANS[plan])
+        d.lens, d.table, d.T, d.q, d.P = c.lens[rs], c.table[rs], c.T[rs], c.q[k.cpu().numpy()], P
+        d.q_start = np.concatenate([[0], np.cumsum(d.T)])
+        d.check(out[k], f32=True)
+    held(lone, 0)
+    held([r for r in range(len(c.T)) if r not in lone + none], 700)
+
+
 def test_the_binding_refuses():
     c = Case(1, 100, [5, 6], [1, 1])
     cache, a = c.cache(), c.args()
