@@ -13,7 +13,7 @@ namespace qg {
 //   KV_OWN     the requests; segments only, to be joined with the prefix's
 //   KV_BOTH    the requests and, as one more entry, the prefix that they share:
 //              all rows of the call against it, without masks; segments only
-//   KV_PREFIX  the prefix alone; segments only
+//   KV_PREFIX  the prefix alone, of kv_prefix_rows_kernel; segments only
 //   KV_LAST    the requests, not cut, with the prefix's segments joined to them;
 //              the output
 enum KvMode { KV_PLAIN, KV_OWN, KV_BOTH, KV_PREFIX, KV_LAST };
@@ -102,7 +102,7 @@ __device__ __forceinline__ Args &args() {
 // entries of the line
 template <KvMode MODE>
 __device__ __forceinline__ int entries_of(Args &a) {
-    return MODE == KV_PREFIX ? 1 : a.R + (MODE == KV_BOTH ? 1 : 0);
+    return a.R + (MODE == KV_BOTH ? 1 : 0);
 }
 
 template <int RW, KvMode MODE = KV_PLAIN>
@@ -208,11 +208,7 @@ __global__ void __launch_bounds__(WAVES * 64, NR == 1 && D <= 128 && WAVES == 4 
         Args &a = args();
         int len = 0, unit = 1;  // steps are counted in `unit`s
         const int entries = entries_of<MODE>(a);
-        if (MODE == KV_PREFIX)
-            len = (req_of<RW, MODE>(a, 0).units + a.cuts * a.min_run - 1) / (a.cuts * a.min_run) * a.min_run;
-        else
-            len = run_length<MODE>(a, work_before<RW, MODE>(a, entries, lane));
-        if (len == 0) return;  // (a prefix of nothing)
+        len = run_length<MODE>(a, work_before<RW, MODE>(a, entries, lane));
         if (a.aligned) {
             unit = len;
             len = 1;

@@ -6,8 +6,19 @@
 // the prefix all query tokens of all requests are rows of one product, so what
 // is memory's work for one request becomes the matrix cores' for many.  Up to
 // 16 rows to a KV head the prefix is one more entry on the requests' line of
-// work, in one launch; above it is a line of its own, of groups of up to 256
-// rows times equal parts of the prefix.
+// work, in one launch; above it is a line of its own, of groups of up to 128
+// rows times equal parts of the prefix.  What joins the segments is a kernel, or
+// the requests' own one (KV_LAST), whichever costs less (kv_prefix_plan).
+//
+// Measured (passes, 8 KV heads of 128 unless said): 4 requests of 4 rows behind
+// 8192 tokens 21.5 us (14.8 the line, 6.2 the join: latency, a chain of loads
+// before the first step and after the last); 48 behind 32768 73 us (47.9 the
+// prefix, 510 TFLOP/s; 27.5 the requests, up to 2000 own tokens); 256 drafts of
+// 16 requests, 1024 rows a head, behind 20011 113 us (93 the prefix, 720
+// TFLOP/s); 8 requests, 4 heads of 256, E4M3, behind 131072 87 us (62.5 the
+// prefix, 4.3 TB/s and 550 TFLOP/s; 11.6 and 13 the rest); 32 requests behind
+// 333 tokens 17.8 us.  Read for each request by kv_attention_run, 48 times
+// 32768 tokens are 3.2 GB.
 #include "kv_attn_kernel.h"
 
 namespace qg {
@@ -151,6 +162,16 @@ __global__ void __launch_bounds__(512) kv_prefix_join_kernel(KvPrefixJoinArgs p)
 // of values: a step's scores are made by the matrix cores while the softmax of
 // the step before is on the vector unit.  Nothing is masked but what lies
 // behind the prefix's last token.
+//
+// Four waves of 32 rows, two workgroups a CU (1024 rows a head 95.4 us, one of
+// eight waves 99.6: all of them wait at every step's barrier); 16 rows a wave
+// where rows are few (prefix_shape); 64 rows a wave leave one wave a SIMD
+// (196 us).  What an unmasked step does besides its products
+// was most of its time: staging with branches 105 us, without 95; before the
+// first product 97, under the second 93.  A step of the two waves of a SIMD then
+// takes about 2050 clocks, of which the matrix unit is busy for half, and the clock is
+// near 1.5 GHz under such work (a library product of 8192 cubed reaches 1.4 of
+// the 2.5 PFLOP/s); keys read a step earlier changed nothing.
 template <bool E4M3, int D, int NR, int WAVES>
 __global__ void __launch_bounds__(WAVES * 64, 2) kv_prefix_rows_kernel(KvAttnArgs) {
     constexpr int KS = D / 32, DT = D / 16, KB = D / 32, TH = WAVES * 64;
@@ -490,17 +511,31 @@ __global__ void __launch_bounds__(WAVES * 64, 2) kv_prefix_rows_kernel(KvAttnArg
     }
 }
 
-// The prefix's variant for M * G rows to a KV head.
+// kv_prefix_rows_kernel's variant for more than 16 rows (M * G) to a KV head.
 struct PrefixShape {
-    int NR, RS;  // row tiles of a wave, waves that take different rows
-    bool many;   // kv_prefix_rows_kernel
+    int NR, WAVES;  // row tiles of a wave, waves
 };
-
+// One row tile a wave, three workgroups a CU, for heads of 128 up to 192 rows
+// (8 heads behind 4096 / 32768 tokens: 64 rows 27.3 / 41.4 us against 30.0 / 47.5
+// of two tiles, 128 rows 35.4 / 57.8 against 38.9 / 60.6; behind 32768 192 rows
+// 68.3 against 72.0, 256 rows 79.8 against 74.5, 512 rows 129 against 110).  Heads
+// of 256 have registers for one tile: four waves up to 64 rows, which is what
+// they hold (49.7 us against 50.4 of eight), eight above (4 heads, 96 rows 54.3
+// against 56.8, 512 rows 113 against 128).  The requests' kernel, a wave for all
+// rows of a step, takes 22.8 us for 24 rows behind 4096 tokens (here 18.8), 25.9
+// for 32 behind 8192 (21.6), 47.7 for 64 behind 32768; heads of 64, 32 rows
+// 19.4 (18.5).
 constexpr PrefixShape prefix_shape(int D, int64_t rows) {
-    if (D == 256) return rows <= 16 ? PrefixShape{1, 1, false} : rows <= 64 ? PrefixShape{1, 4, true} : PrefixShape{1, 8, true};
-    if (rows <= 32) return {rows <= 16 ? 1 : 2, 1, false};
-    return {D == 128 && rows <= 192 ? 1 : 2, 4, true};
+    if (D == 256) return {1, rows <= 64 ? 4 : 8};
+    return {D == 128 && rows <= 192 ? 1 : 2, 4};
 }
+// Up to 16 rows the prefix lies on the requests' line, in one launch (4
+// requests, 8 heads of 128 behind 8192 tokens 19.6 us against 21.2 in a launch
+// of its own, 32768 tokens 27.4 against 38.7).
+constexpr bool on_one_line(int64_t rows) { return rows <= 16; }
+
+// The requests' variant, for the rows that one of them can have.
+Shape own_shape(int64_t D, int64_t M, int64_t max_q, int64_t G) { return shape_of((int)D, (max_q < M ? max_q : M) * G); }
 
 template <bool E4M3, int D, int NR, int RS, KvMode MODE, int WAVES = 4>
 void run_line(const KvAttnArgs &a, hipStream_t s) {
@@ -525,15 +560,13 @@ void run_rows(const KvAttnArgs &a, hipStream_t s) {
 
 template <bool E4M3, int D>
 void run(const KvAttnArgs &own, const KvAttnArgs &pre, const KvPrefixPlan &p, hipStream_t s) {
-    const Shape v = shape_of(D, (int64_t)own.max_q * own.G);
+    const Shape v = own_shape(D, own.M, own.max_q, own.G);
     const PrefixShape w = prefix_shape(D, (int64_t)own.M * own.G);
     if (p.both) {
         run_line<E4M3, D, 1, 1, KV_BOTH>(own, s);
     } else {
         if constexpr (D == 256)
-            !w.many ? run_line<E4M3, D, 1, 1, KV_PREFIX>(pre, s) : w.RS == 4 ? run_rows<E4M3, D, 1, 4>(pre, s) : run_rows<E4M3, D, 1, 8>(pre, s);
-        else if (!w.many)
-            w.NR == 1 ? run_line<E4M3, D, 1, 1, KV_PREFIX>(pre, s) : run_line<E4M3, D, 2, 1, KV_PREFIX>(pre, s);
+            w.WAVES == 4 ? run_rows<E4M3, D, 1, 4>(pre, s) : run_rows<E4M3, D, 1, 8>(pre, s);
         else if (D == 128 && w.NR == 1)
             run_rows<E4M3, D, D == 128 ? 1 : 2, 4>(pre, s);
         else
@@ -550,6 +583,9 @@ void run(const KvAttnArgs &own, const KvAttnArgs &pre, const KvPrefixPlan &p, hi
     j.own_rw = 16 * v.NR * v.RS;
     j.pre_rw = p.pre_rw;
     j.both = p.both;
+    // a wave a join where they fill the GPU, eight below (8 heads of 128, requests of
+    // 6000 tokens: 48 requests, 1536 joins, 120 us against 128.5; 16, 512 joins, 66.8
+    // against 70.3)
     const int64_t joins = (int64_t)own.R * own.max_q * own.Hq;
     if (joins >= 1024)
         hipLaunchKernelGGL((kv_prefix_join_kernel<D, 1>), dim3((unsigned)((joins + 7) / 8)), dim3(512), 0, s, j);
@@ -561,12 +597,13 @@ void run(const KvAttnArgs &own, const KvAttnArgs &pre, const KvPrefixPlan &p, hi
 
 bool kv_prefix_plan(int64_t R, int64_t M, int64_t Hkv, int64_t G, int64_t D, int64_t max_q, int64_t max_len,
                     int64_t max_prefix, KvPrefixPlan *p) {
-    const int64_t rows = max_q * G, all = M > 0 ? M * G : 1, steps = (max_prefix + KV_STEP - 1) / KV_STEP;
-    const Shape v = shape_of((int)D, rows);
+    M = M > 0 ? M : 1;
+    const int64_t rows = (max_q < M ? max_q : M) * G, all = M * G, steps = (max_prefix + KV_STEP - 1) / KV_STEP;
+    const Shape v = own_shape(D, M, max_q, G);
     const PrefixShape w = prefix_shape((int)D, all);
-    const int64_t RW = 16 * v.NR * v.RS, PW = 16 * w.NR * w.RS;
+    p->both = on_one_line(all);
+    const int64_t RW = 16 * v.NR * v.RS, PW = p->both ? RW : 16 * w.NR * w.WAVES;
     const int64_t groups = (rows + RW - 1) / RW, pgroups = (all + PW - 1) / PW, units = (max_len + KV_STEP - 1) / KV_STEP + 1;
-    p->both = all <= 16 && rows <= 16;
     // the requests' line, cut as kv_attention_plan says
     KvAttnPlan &o = p->own;
     const int64_t starts = R * Hkv * groups + (p->both ? Hkv * pgroups : 0);
@@ -596,7 +633,7 @@ bool kv_prefix_plan(int64_t R, int64_t M, int64_t Hkv, int64_t G, int64_t D, int
     // against 60.9, 2000 80.8 against 72.4; 8 of 300, heads of 256, behind
     // 131072 tokens (128 segments) 55 us against 25.
     KvAttnPlan &q = p->pre;
-    const int64_t pairs = Hkv * pgroups, fit = 256 * (w.many ? (w.NR == 1 && D == 128 ? 3 : 8 / w.RS) : w.NR == 1 && D <= 128 ? 3 : 2);
+    const int64_t pairs = Hkv * pgroups, fit = 256 * (w.NR == 1 && D == 128 ? 3 : 8 / w.WAVES);
     if (pairs * (steps + 1) >= (int64_t(1) << 31) - 65536) return false;
     const int split = v.NR == 1 && D <= 128 ? 8 : 4 / v.RS;  // waves that share a request's segments
     const bool whole = !p->both && starts <= 1024 && (max_len <= 1024 || (split == 8 && starts >= 128 && max_len <= 4096));
@@ -619,7 +656,7 @@ bool kv_prefix_plan(int64_t R, int64_t M, int64_t Hkv, int64_t G, int64_t D, int
     q.groups = (int)pgroups;
     q.whole = false;
     q.slots = (int)(p->both ? 0 : pairs * best);
-    q.min_run = w.many ? 1 : 4 / w.RS;
+    q.min_run = 1;
     q.part_rows = (int)(all < PW ? all : PW);
     q.aligned = true;
     q.part_slots = q.slots;

@@ -46,7 +46,7 @@ struct SampleArgs {
     int32_t *top_at;             // [M][chunks][SAMPLE_SUBS]: the first token that has it (-1: all are NaN)
     u32x2_t *lists;              // [M][SAMPLE_LIST]: (key, token) of undecided tokens
     int M, V, chunks;
-    bool few;  // workgroups than fill the GPU: read ahead of a row's settings
+    bool few;  // workgroups: they read ahead of a row's settings, and find its borders each
 };
 
 hipError_t launch_sample(const SampleArgs &a, bool x_f32, hipStream_t s);

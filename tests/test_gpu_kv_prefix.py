@@ -294,6 +294,15 @@ def test_a_large_call_by_some_of_its_rows():
     c.check(got[torch.tensor(pick, device=DEV)])
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("R", [1, 2, 3, 40])
+def test_a_call_that_allows_more_rows_than_it_has(R, D):
+    """max_q of 32 where the call's rows are few."""
+    c = Case(R + D, 700, [1 + 11 * i for i in range(R)], [1] * R, D=D)
+    c.run(max_q=32)
+    c.run(max_q=5, max_len=c.cols * c.page)
+
+
 # the one line of work; the requests' own kernel joins; a kernel joins
 PLANS = [dict(lens=[1, 40, 7], T=[1, 1, 1], G=4), dict(lens=[5 + i for i in range(40)], T=[1] * 40, G=4),
          dict(lens=[3000] * 3 + [5] * 3, T=[3] * 6, G=8, D=256)]
