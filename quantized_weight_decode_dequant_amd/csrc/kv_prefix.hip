@@ -542,15 +542,23 @@ void run_line(const KvAttnArgs &a, hipStream_t s) {
     hipLaunchKernelGGL((kv_attn_kernel<E4M3, D, NR, RS, WAVES, MODE>), dim3((unsigned)a.slots), dim3(WAVES * 64), 0, s, a);
 }
 
+// Waves of a workgroup of the requests' that joins the prefix's segments, for
+// heads of 64 and 128: eight for one row tile, and where no CU gets a second
+// workgroup (8 heads of 128 behind 2048 tokens, 4 requests of 32 drafts and 1000
+// tokens 61.7 us against 72.6 of four, 16 of 16 and 700 behind 20011 120 against
+// 124); else four (64 requests of 32 rows and 300 tokens behind 8192 99 us
+// against 111, 64 of 64 rows 167 against 181).
+constexpr int last_waves(const Shape &v, int64_t starts) { return v.NR == 1 || starts <= 256 ? 8 : 4; }
+
 // the requests' own tokens
-template <bool E4M3, int D, KvMode MODE>
+template <bool E4M3, int D, KvMode MODE, int WAVES>
 void pick_own(const KvAttnArgs &a, const Shape &v, hipStream_t s) {
     if constexpr (D == 256)
         v.RS == 1 ? run_line<E4M3, D, 1, 1, MODE>(a, s) : v.RS == 2 ? run_line<E4M3, D, 1, 2, MODE>(a, s) : run_line<E4M3, D, 1, 4, MODE>(a, s);
     else if (v.NR == 1)
         run_line<E4M3, D, 1, 1, MODE, MODE == KV_LAST ? 8 : 4>(a, s);
     else
-        v.RS == 1 ? run_line<E4M3, D, 2, 1, MODE>(a, s) : v.RS == 2 ? run_line<E4M3, D, 2, 2, MODE>(a, s) : run_line<E4M3, D, 2, 4, MODE>(a, s);
+        v.RS == 1 ? run_line<E4M3, D, 2, 1, MODE, WAVES>(a, s) : v.RS == 2 ? run_line<E4M3, D, 2, 2, MODE, WAVES>(a, s) : run_line<E4M3, D, 2, 4, MODE, WAVES>(a, s);
 }
 
 template <bool E4M3, int D, int NR, int WAVES>
@@ -572,10 +580,10 @@ void run(const KvAttnArgs &own, const KvAttnArgs &pre, const KvPrefixPlan &p, hi
         else
             run_rows<E4M3, D, 2, 4>(pre, s);
         if (p.last) {
-            pick_own<E4M3, D, KV_LAST>(own, v, s);
+            D == 256 || last_waves(v, p.own_starts) == 4 ? pick_own<E4M3, D, KV_LAST, 4>(own, v, s) : pick_own<E4M3, D, KV_LAST, D == 256 ? 4 : 8>(own, v, s);
             return;
         }
-        pick_own<E4M3, D, KV_OWN>(own, v, s);
+        pick_own<E4M3, D, KV_OWN, 4>(own, v, s);
     }
     KvPrefixJoinArgs j;
     j.own = own;
@@ -635,8 +643,8 @@ bool kv_prefix_plan(int64_t R, int64_t M, int64_t Hkv, int64_t G, int64_t D, int
     KvAttnPlan &q = p->pre;
     const int64_t pairs = Hkv * pgroups, fit = 256 * (w.NR == 1 && D == 128 ? 3 : 8 / w.WAVES);
     if (pairs * (steps + 1) >= (int64_t(1) << 31) - 65536) return false;
-    const int split = v.NR == 1 && D <= 128 ? 8 : 4 / v.RS;  // waves that share a request's segments
-    const bool whole = !p->both && starts <= 1024 && (max_len <= 1024 || (split == 8 && starts >= 128 && max_len <= 4096));
+    const int split = (D <= 128 ? last_waves(v, starts) : 4) / v.RS;  // waves that share a request's segments
+    const bool whole = !p->both && starts <= 1024 && (max_len <= 1024 || (v.NR == 1 && D <= 128 && starts >= 128 && max_len <= 4096));
     const int64_t longest = steps / 3 > 1 ? steps / 3 : 1, upto = longest < 4 * fit / pairs ? longest : 4 * fit / pairs;
     int64_t best = 1;
     double least = 1e30;

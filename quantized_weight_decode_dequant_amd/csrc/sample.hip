@@ -32,10 +32,11 @@
 // last workgroup going on: the fences that this takes cost 462 us where the
 // kernel's work is 30 (192 rows).
 //
-// One row of 151936 takes 3.1 + 6.0 + 6.8 + 7.2 us, all latency: launches,
-// settings, logits, atomics in turn.  16 fp32 rows 3.8 + 9.7 + 9.4 + 11.7.  192
-// bf16 rows 12.4 (4.7 TB/s) + 28.8 (the vector unit: some 33 instructions a
-// token, most of them the weight's) + 4.8 + 13.4 + 16.2.
+// One row of 151936, top-k 50, takes LINE_ONE us, all latency: launches,
+// settings, logits, atomics in turn.  16 fp32 rows, top-p alone, LINE_NUC.
+// 192 bf16 rows, each with settings of its own, 12.4 (4.7 TB/s) + 25.8 (the
+// vector unit: some 33 instructions a token where masses are asked for, most of
+// them the weight's) + 4.8 + 13.8 + 16.6.
 #include <type_traits>
 
 #include "sample.h"
@@ -49,6 +50,11 @@ typedef unsigned long long u64;
 constexpr int TH = SAMPLE_THREADS, W = TH / 64, E = SAMPLE_PER_THREAD, NB = SAMPLE_BINS;
 constexpr float NEG_INF = -__builtin_inff();
 constexpr double UNIT = 0x1p42;  // of masses
+// Top-k up to which top-p's border comes from the list alone: so many that a
+// workgroup ranks them at once, most often.  151936 tokens, k = 50: one row 20.5 us
+// against 21.4, 192 rows 66 against 82; k = 100: 21.4 either way, 71 against 85; k =
+// 200, whose list is narrowed by digits: one row 26.4 against 22.1.
+constexpr int BY_LIST = 100;
 
 __device__ __forceinline__ float f32_of(unsigned w) { return __builtin_bit_cast(float, w); }
 __device__ __forceinline__ unsigned bits_of(float f) { return __builtin_bit_cast(unsigned, f); }
@@ -96,6 +102,9 @@ struct Ask {
     int k;           // 0: no top-k
     bool greedy;     // the largest logit
     __device__ __forceinline__ bool filters() const { return k > 0 || p < 1.0; }
+    // top-p under so small a top-k that all of top-k's tokens go to the list: no
+    // masses by bins, a weight for each listed token instead of each of the row
+    __device__ __forceinline__ bool by_list() const { return k > 0 && k <= BY_LIST && p < 1.0; }
 };
 
 __device__ __forceinline__ Ask ask_of(const SampleArgs &a, int m) {
@@ -322,13 +331,14 @@ __global__ void __launch_bounds__(TH) sample_bins_kernel(SampleArgs a) {
         if ((tid & 63) == 63) a.kept[((size_t)m * a.chunks + c) * SAMPLE_SUBS + tid / 64] = sum;
         return;
     }
+    const bool by_mass = q.p < 1.0 && !q.by_list();
 #pragma unroll
     for (int e = 0; e < E; ++e) {
         const float d = t.distance(x[e]);
         if (!t.dead(d)) {
             const int b = bin_of(d);
             if (q.k > 0) atomicAdd(&counts[b], 1u);
-            if (q.p < 1.0) atomicAdd(&masses[b], mass_of(weight(x[e], t.top, q.c, pow)));
+            if (by_mass) atomicAdd(&masses[b], mass_of(weight(x[e], t.top, q.c, pow)));
         }
     }
     __syncthreads();
@@ -517,7 +527,12 @@ __device__ __forceinline__ bool find_borders(const SampleArgs &a, int m, const A
     r.k_bin = by_k ? (int)sh.found32[0] : -1;
     r.k_left = by_k ? sh.found32[1] : 0;
     __syncthreads();
-    if (by_p) {
+    if (q.by_list()) {
+        if (tid == 0) {
+            sh.found32[2] = 0;
+            sh.found32[3] = by_k ? (unsigned)r.k_bin : NB - 1;
+        }
+    } else if (by_p) {
         const u64 want_lo = max((u64)ceil(q.p * (double)lo), (u64)1), want_hi = max((u64)ceil(q.p * (double)hi), (u64)1);
         u64 s = mass_before;
 #pragma unroll
@@ -754,7 +769,10 @@ __global__ void __launch_bounds__(TH) sample_pick_kernel(SampleArgs a) {
         bool keep = valid && (r.k_bin < 0 || rank < r.k_left + sooner);
         if (q.p < 1.0) {
             u64 mass = r.mass;  // what top-k keeps
-            if (r.k_bin >= 0) mass = r.k_mass + sum_all(keep && b == r.k_bin ? w : 0, sh.wave64);
+            if (q.by_list())
+                mass = sum_all(keep ? w : 0, sh.wave64);
+            else if (r.k_bin >= 0)
+                mass = r.k_mass + sum_all(keep && b == r.k_bin ? w : 0, sh.wave64);
             keep &= b <= r.p_hi && before < max((u64)ceil(q.p * (double)mass), (u64)1);
         }
         __syncthreads();
@@ -897,13 +915,13 @@ __global__ void __launch_bounds__(TH) sample_pick_kernel(SampleArgs a) {
     __syncthreads();
     Cut cut{0, ~0u, 0};
     u64 mass = r.mass;  // what top-k keeps
-    if (r.k_bin >= 0) {
-        cut = descend(std::false_type(), r.k_left, [&](unsigned, int b) { return b == r.k_bin; });
+    if (r.k_bin >= 0 || q.by_list()) {
+        if (r.k_bin >= 0) cut = descend(std::false_type(), r.k_left, [&](unsigned, int b) { return b == r.k_bin; });
         if (q.p < 1.0) {
             u64 s = 0;
-            const bool by_token = cut.ties == ~0u;
+            const bool by_token = cut.ties == ~0u, all = q.by_list();
             each([&](unsigned key, int b, unsigned token) {
-                s += b == r.k_bin && (key > cut.key || (by_token && key == cut.key && token <= cut.token)) ? mass_at(key) : 0;
+                s += (all || b == r.k_bin) && (key > cut.key || (by_token && key == cut.key && token <= cut.token)) ? mass_at(key) : 0;
             });
             mass = r.k_mass + sum_all(s, sh.wave64) + (by_token ? 0 : (u64)cut.ties * mass_at(cut.key));
         }

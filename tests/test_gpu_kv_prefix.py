@@ -294,6 +294,15 @@ def test_a_large_call_by_some_of_its_rows():
     c.check(got[torch.tensor(pick, device=DEV)])
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("rows", [24, 60, 120, 256])
+@pytest.mark.parametrize("R", [3, 40])
+def test_requests_that_join_the_prefix_themselves(R, rows, D):
+    """Each number of row tiles, on both sides of a workgroup to a CU."""
+    note("prefix joined by requests R=%d rows=%d D=%d" % (R, rows, D))
+    Case(rows + D + R, 331, [32 + (i * 37) % 150 for i in range(R)], [rows // 8 - (i % 2) for i in range(R)], H=8, G=8, D=D, page=32).run()
+
+
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("R", [1, 2, 3, 40])
 def test_a_call_that_allows_more_rows_than_it_has(R, D):

@@ -266,3 +266,31 @@ def test_tokens_far_below_the_largest():
         for kw in (dict(), dict(k=[4900] * 6), dict(k=[4900] * 6, p=[0.9999] * 6), dict(p=[0.99] * 6)):
             # (what lies below changes no sum by more than 2^-31 of it)
             check(x, np.minimum(u, 1 - 2.0 ** -22), T=[T] * 6, **kw)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("spread", [0.0, 1e-3, 0.3, 2.2])
+@pytest.mark.parametrize("M", [6, 140])
+def test_top_p_under_a_small_top_k(dtype, spread, M):
+    """On both sides of the size whose tokens are all listed, ties by the thousand."""
+    V = 20011
+    x = logits(M, V, dtype, 5, spread, lift=spread > 1) + torch.tensor(3.0, dtype=dtype, device=DEV)
+    g = np.random.default_rng(M)
+    check(x, g.random(M), T=g.choice([0.3, 0.8, 1.0, 4.0], M), k=g.choice([2, 3, 50, 99, 100, 101, 128, 129], M),
+          p=g.choice([1e-6, 0.3, 0.9, 0.9999], M), minp=g.choice([0, 0, 0.05], M))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_a_small_top_k_over_few_or_infinite_tokens(dtype):
+    M, V = 8, 9001
+    x = torch.full((M, V), float("-inf"), dtype=dtype, device=DEV)
+    at = torch.arange(0, V, 300, device=DEV)
+    x[:4, at] = logits(4, len(at), dtype, 6, lift=False)  # 31 tokens
+    x[2, at[5]] = x[4, 17] = float("nan")
+    x[3, at] = 1.0
+    x[5, at] = float("inf")
+    x[6, 8000] = float("inf")
+    x[7, 3] = -3e38
+    for p in (0.2, 0.95):
+        for k in (2, 30, 31, 32, 100):
+            check(x, np.linspace(0, 0.999, M), T=[0.7] * M, k=[k] * M, p=[p] * M)
