@@ -10,15 +10,15 @@
 // rows times equal parts of the prefix.  What joins the segments is a kernel, or
 // the requests' own one (KV_LAST), whichever costs less (kv_prefix_plan).
 //
-// Measured (passes, 8 KV heads of 128 unless said): 4 requests of 4 rows behind
-// 8192 tokens 21.5 us (14.8 the line, 6.2 the join: latency, a chain of loads
-// before the first step and after the last); 48 behind 32768 73 us (47.9 the
-// prefix, 510 TFLOP/s; 27.5 the requests, up to 2000 own tokens); 256 drafts of
-// 16 requests, 1024 rows a head, behind 20011 113 us (93 the prefix, 720
-// TFLOP/s); 8 requests, 4 heads of 256, E4M3, behind 131072 87 us (62.5 the
-// prefix, 4.3 TB/s and 550 TFLOP/s; 11.6 and 13 the rest); 32 requests behind
-// 333 tokens 17.8 us.  Read for each request by kv_attention_run, 48 times
-// 32768 tokens are 3.2 GB.
+// Measured (passes, 8 KV heads of 128 unless said): 4 requests of 4 rows behind 8192
+// tokens 21.8 us (14.5 the line, 6.6 the join: latency, a chain of loads before the
+// first step and after the last); 48 behind 32768 73 us (47.6 the prefix, 510 TFLOP/s;
+// 28 the requests, up to 2000 own tokens); 256 drafts of 16 requests, 1024 rows a
+// head, behind 20011 109 us (93 the prefix, 720 TFLOP/s; 29 the requests, of which 6
+// join, latency); 8 requests, 4 heads of 256, E4M3, behind 131072 87 us (62 the
+// prefix, 4.3 TB/s and 550 TFLOP/s; 11.6 the requests, 13 the join, of 33 MB of
+// segments); 32 requests behind 333 tokens 17.8 us.  Read for each request by
+// kv_attention_run, 48 times 32768 tokens are 3.2 GB.
 #include "kv_attn_kernel.h"
 
 namespace qg {
@@ -163,15 +163,14 @@ __global__ void __launch_bounds__(512) kv_prefix_join_kernel(KvPrefixJoinArgs p)
 // the step before is on the vector unit.  Nothing is masked but what lies
 // behind the prefix's last token.
 //
-// Four waves of 32 rows, two workgroups a CU (1024 rows a head 95.4 us, one of
-// eight waves 99.6: all of them wait at every step's barrier); 16 rows a wave
-// where rows are few (prefix_shape); 64 rows a wave leave one wave a SIMD
-// (196 us).  What an unmasked step does besides its products
-// was most of its time: staging with branches 105 us, without 95; before the
-// first product 97, under the second 93.  A step of the two waves of a SIMD then
-// takes about 2050 clocks, of which the matrix unit is busy for half, and the clock is
-// near 1.5 GHz under such work (a library product of 8192 cubed reaches 1.4 of
-// the 2.5 PFLOP/s); keys read a step earlier changed nothing.
+// Four waves of 32 rows, two workgroups a CU (1024 rows a head 95.4 us, one of eight
+// waves 99.6: all of them wait at every step's barrier); 16 rows a wave where rows are
+// few (prefix_shape); 64 rows a wave leave one wave a SIMD (196 us).  What an unmasked
+// step does besides its products was most of its time: staging with branches 105 us,
+// without 95; before the first product 97, under the second 93.  A step of the two
+// waves of a SIMD then takes about 2050 clocks, of which the matrix unit is busy for
+// half, and the clock is near 1.5 GHz under such work (a library product of 8192 cubed
+// reaches 1.4 of the 2.5 PFLOP/s); keys read a step earlier changed nothing.
 template <bool E4M3, int D, int NR, int WAVES>
 __global__ void __launch_bounds__(WAVES * 64, 2) kv_prefix_rows_kernel(KvAttnArgs) {
     constexpr int KS = D / 32, DT = D / 16, KB = D / 32, TH = WAVES * 64;

@@ -16,10 +16,10 @@
 // way, and pass them on through LDS.  Few tokens are split over several waves
 // of as few heads as one load takes (`parts`), many take one wave each.
 //
-// Bound by latency for few tokens (1 of 32 + 8 heads of 128: 3.4 us, where an
-// empty launch takes 2.4; 32 fp32 tokens on three axes 4.1), by memory for
+// Bound by latency for few tokens (1 of 32 + 8 heads of 128: 3.6 us, where an
+// empty launch takes 2.4; 32 fp32 tokens on three axes 4.3), by memory for
 // many (5003 tokens 24 us, 4.3 TB/s; 1021 of 32 + 4 heads of 256, a quarter
-// rotated, no norm: 10.2 us, 3.7 TB/s).
+// rotated, no norm: 9.9 us, 3.8 TB/s).
 #include "qk_rope.h"
 
 namespace qg {

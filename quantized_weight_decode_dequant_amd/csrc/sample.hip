@@ -32,11 +32,11 @@
 // last workgroup going on: the fences that this takes cost 462 us where the
 // kernel's work is 30 (192 rows).
 //
-// One row of 151936, top-k 50, takes LINE_ONE us, all latency: launches,
-// settings, logits, atomics in turn.  16 fp32 rows, top-p alone, LINE_NUC.
-// 192 bf16 rows, each with settings of its own, 12.4 (4.7 TB/s) + 25.8 (the
-// vector unit: some 33 instructions a token where masses are asked for, most of
-// them the weight's) + 4.8 + 13.8 + 16.6.
+// One row of 151936, top-k 50, takes 3.1 + 4.4 + 6.7 + 8.0 us, all latency: launches,
+// settings, logits, atomics in turn.  16 fp32 rows, top-p alone, 3.8 + 9.0 + 9.8 +
+// 11.9. 192 bf16 rows, each with settings of its own, 12.4 (4.7 TB/s) + 25.4 (the
+// vector unit: some 33 instructions a token where masses are asked for, most of them
+// the weight's) + 4.8 + 13.9 + 16.5.
 #include <type_traits>
 
 #include "sample.h"
