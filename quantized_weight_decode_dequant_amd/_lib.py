@@ -443,10 +443,25 @@ def _rows(t, H, D, dtype, dev, name):
     return t.data_ptr(), (row if shape[0] > 1 else H * D)
 
 
+def _rows_of(t, shape, dtype, dev, name):
+    """_rows of a tensor that is to have this shape."""
+    if t.dtype is not dtype or t.shape != shape:
+        raise ValueError("%s must be a %s tensor of shape %s (got %s %s)"
+                         % (name, dtype, tuple(shape), t.dtype, tuple(t.shape)))
+    if t.get_device() != dev:
+        raise ValueError("%s must be a device tensor on device %d (got %s)" % (name, dev, t.device))
+    if t.is_contiguous():
+        return t.data_ptr(), shape[1] * shape[2]
+    row, head, dim = t.stride()
+    if dim != 1 or (shape[1] > 1 and head != shape[2]):
+        raise ValueError("%s: the heads and dimensions of a token must be dense" % name)
+    return t.data_ptr(), (row if shape[0] > 1 else shape[1] * shape[2])
+
+
 def _call(dev, stream, where, fn, *args):
     """fn(*args, stream) with `dev` current; stream: as given, or dev's current one."""
     torch = _torch()
-    if torch.cuda.current_device() != dev:
+    if torch._C._cuda_getDevice() != dev:
         with torch.cuda.device(dev):
             return _call(dev, stream, where, fn, *args)
     if stream is None:
@@ -517,38 +532,44 @@ def qk_norm_rope_run(q, k, positions, inv_freq, q_weight=None, k_weight=None, ep
     2] with several axes; q_weight, k_weight bf16 [D] (None: no norm).  Returns
     (q_out, k_out), bf16; q_out may be q and k_out k."""
     torch = _torch()
-    bf16 = torch.bfloat16
-    if q.dim() != 3:
+    bf16, i32, f32 = torch.bfloat16, torch.int32, torch.float32
+    shape, dtype = q.shape, q.dtype
+    if len(shape) != 3:
         raise ValueError("q must be [M, Hq, D]")
-    M, Hq, D = q.shape
-    xt, dev = _float_type(q, "q"), _device(q)
-    if k is not None and (k.dim() != 3 or k.shape[0] != M or k.shape[2] != D):
-        raise ValueError("k must be [%d, Hkv, %d] (got %s)" % (M, D, tuple(k.shape)))
-    if k is None and k_out is not None:
+    M, Hq, D = shape
+    xt = OUT_BF16 if dtype is bf16 else OUT_F32 if dtype is f32 else _float_type(q, "q")
+    dev = _device(q)
+    kshape, Hkv = None, 0
+    if k is not None:
+        kshape = k.shape
+        if len(kshape) != 3 or kshape[0] != M or kshape[2] != D:
+            raise ValueError("k must be [%d, Hkv, %d] (got %s)" % (M, D, tuple(kshape)))
+        Hkv = kshape[1]
+    elif k_out is not None:
         raise ValueError("k_out without k")
-    Hkv = k.shape[1] if k is not None else 0
     if q_out is None:
-        q_out = _empty((M, Hq, D), bf16, q.device, stream)
+        q_out = _empty(shape, bf16, q.device, stream)
     if k_out is None and k is not None:
-        k_out = _empty((M, Hkv, D), bf16, q.device, stream)
-    if q_out.shape != q.shape or (k is not None and k_out.shape != k.shape):
-        raise ValueError("q_out and k_out must have the shapes of q and k")
-    if positions.dim() not in (1, 2) or inv_freq.dim() != 1:
+        k_out = _empty(kshape, bf16, q.device, stream)
+    pshape, fshape = positions.shape, inv_freq.shape
+    if len(pshape) not in (1, 2) or len(fshape) != 1:
         raise ValueError("positions must be [M] or [axes, M], inv_freq [rotated / 2]")
-    axes, half = (1 if positions.dim() == 1 else positions.shape[0]), inv_freq.shape[0]
+    axes, half = (1 if len(pshape) == 1 else pshape[0]), fshape[0]
     if M == 0:
+        if q_out.shape != shape or (k is not None and k_out.shape != kshape):
+            raise ValueError("q_out and k_out must have the shapes of q and k")
         return q_out, k_out
-    qp, qs = _rows(q, Hq, D, q.dtype, dev, "q")
-    qo, qos = _rows(q_out, Hq, D, bf16, dev, "q_out")
+    qp, qs = _rows_of(q, shape, dtype, dev, "q")
+    qo, qos = _rows_of(q_out, shape, bf16, dev, "q_out")
     kp = ko = None
     ks = kos = 0
     if k is not None:
-        kp, ks = _rows(k, Hkv, D, q.dtype, dev, "k")
-        ko, kos = _rows(k_out, Hkv, D, bf16, dev, "k_out")
+        kp, ks = _rows_of(k, kshape, dtype, dev, "k")
+        ko, kos = _rows_of(k_out, kshape, bf16, dev, "k_out")
     _call(dev, stream, "qk_norm_rope_run", raw().qk_norm_rope_run, qp, qs, kp, ks, xt, M, Hq, Hkv, D,
           _arg(q_weight, bf16, (D,), dev, "q_weight"), _arg(k_weight, bf16, (D,), dev, "k_weight"), eps,
-          _arg(positions, torch.int32, (M,) if positions.dim() == 1 else (axes, M), dev, "positions"), axes,
-          _arg(axis, torch.uint8, (half,), dev, "axis"), _arg(inv_freq, torch.float32, (half,), dev, "inv_freq"),
+          _arg(positions, i32, (M,) if len(pshape) == 1 else (axes, M), dev, "positions"), axes,
+          _arg(axis, torch.uint8, (half,), dev, "axis"), _arg(inv_freq, f32, fshape, dev, "inv_freq"),
           2 * half, 1 if interleaved else 0, qo, qos, ko, kos)
     return q_out, k_out
 
