@@ -11,7 +11,7 @@
 // the requests' own one (KV_LAST), whichever costs less (kv_prefix_plan).
 //
 // Measured (passes, 8 KV heads of 128 unless said): 4 requests of 4 rows behind 8192
-// tokens 21.8 us (14.5 the line, 6.6 the join: latency, a chain of loads before the
+// tokens 18.5 us (12.8 the line, 6.2 the join: latency, a chain of loads before the
 // first step and after the last); 48 behind 32768 73 us (47.6 the prefix, 510 TFLOP/s;
 // 28 the requests, up to 2000 own tokens); 256 drafts of 16 requests, 1024 rows a
 // head, behind 20011 109 us (93 the prefix, 720 TFLOP/s; 29 the requests, of which 6
@@ -529,8 +529,8 @@ constexpr PrefixShape prefix_shape(int D, int64_t rows) {
     return {D == 128 && rows <= 192 ? 1 : 2, 4};
 }
 // Up to 16 rows the prefix lies on the requests' line, in one launch (4
-// requests, 8 heads of 128 behind 8192 tokens 19.6 us against 21.2 in a launch
-// of its own, 32768 tokens 27.4 against 38.7).
+// requests, 8 heads of 128 behind 8192 tokens 17.4 us against 21.2 in a launch
+// of its own, 32768 tokens 25.3 against 38.7).
 constexpr bool on_one_line(int64_t rows) { return rows <= 16; }
 
 // The requests' variant, for the rows that one of them can have.
@@ -611,18 +611,29 @@ bool kv_prefix_plan(int64_t R, int64_t M, int64_t Hkv, int64_t G, int64_t D, int
     p->both = on_one_line(all);
     const int64_t RW = 16 * v.NR * v.RS, PW = p->both ? RW : 16 * w.NR * w.WAVES;
     const int64_t groups = (rows + RW - 1) / RW, pgroups = (all + PW - 1) / PW, units = (max_len + KV_STEP - 1) / KV_STEP + 1;
-    // the requests' line, cut as kv_attention_plan says
+    // the requests' line
     KvAttnPlan &o = p->own;
-    const int64_t starts = R * Hkv * groups + (p->both ? Hkv * pgroups : 0);
+    // (on one line, cut on every start, only the starts of work count: of no more requests than rows)
+    const int64_t starts = p->both ? Hkv * ((R < M ? R : M) * groups + pgroups) : R * Hkv * groups;
     int64_t most = R * Hkv * groups * units + (p->both ? Hkv * pgroups * (steps + 1) : 0);
     if (most >= (int64_t(1) << 31) - 65536) return false;
     p->pre_rw = (int)PW;
     o.groups = (int)groups;
     o.whole = false;
     o.slots = 256 * (v.NR == 1 && D <= 128 ? 3 : 2);
+    // On one line a workgroup a CU, or as many more as leave four for each start,
+    // then two, and a cut falls on every start: fewer segments, and less to join (4
+    // requests, 8 heads of 128 behind 8192 tokens 17.4 us against 19.8 of three a
+    // CU, 131072 53.5 against 58.4; 12 requests of 16 heads behind 8192 22 against 31
+    // of equal runs over all starts, 16 of 32 heads 39 against 48).
+    if (p->both) o.slots = (int)(starts <= 64 ? 256 : starts <= 128 ? 512 : 2 * starts > o.slots ? 2 * starts : o.slots);
     o.min_run = 4 / v.RS;
     o.part_rows = (int)(p->both ? 16 : rows < RW ? rows : RW);
-    o.aligned = 4 * starts <= o.slots;
+    // Else a cut on every start up to one a CU (32 requests of up to 6000 tokens, 8
+    // heads of 128: 75 us against 80 of equal runs, of 8 drafts and 2000 86 against
+    // 101, heads of 256 92 against 101); above, lengths that differ make parts that
+    // do (48 of up to 16000: 171 against 159, 512 of up to 3000 385 against 351).
+    o.aligned = p->both || starts <= 256;
     if (!o.aligned) o.slots *= 2;
     o.part_slots = o.slots + (o.aligned ? 0 : starts);
     o.head_bytes = PART_HEAD;

@@ -312,6 +312,16 @@ def test_a_call_that_allows_more_rows_than_it_has(R, D):
     c.run(max_q=5, max_len=c.cols * c.page)
 
 
+@pytest.mark.parametrize("G", [1, 2, 4])
+def test_more_requests_than_rows(G):
+    """64 requests, of which few have a row: before, between and behind idle ones."""
+    T = [0] * 64
+    for r in (0, 7, 8, 63):
+        T[r] = 1
+    Case(G, 2003, [20 + 3 * i for i in range(64)], T, H=2, G=G).run()
+    Case(G, 2003, [20 + 3 * i for i in range(64)], [0] * 63 + [4], H=3, G=G).run()
+
+
 # the one line of work; the requests' own kernel joins; a kernel joins
 PLANS = [dict(lens=[1, 40, 7], T=[1, 1, 1], G=4), dict(lens=[5 + i for i in range(40)], T=[1] * 40, G=4),
          dict(lens=[3000] * 3 + [5] * 3, T=[3] * 6, G=8, D=256)]
