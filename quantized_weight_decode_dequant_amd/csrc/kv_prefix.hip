@@ -14,7 +14,7 @@
 // tokens 18.5 us (12.8 the line, 6.2 the join: latency, a chain of loads before the
 // first step and after the last); 48 behind 32768 73 us (47.6 the prefix, 510 TFLOP/s;
 // 28 the requests, up to 2000 own tokens); 256 drafts of 16 requests, 1024 rows a
-// head, behind 20011 109 us (93 the prefix, 720 TFLOP/s; 29 the requests, of which 6
+// head, behind 20011 110 us (93 the prefix, 720 TFLOP/s; 29 the requests, of which 6
 // join, latency); 8 requests, 4 heads of 256, E4M3, behind 131072 87 us (62 the
 // prefix, 4.3 TB/s and 550 TFLOP/s; 11.6 the requests, 13 the join, of 33 MB of
 // segments); 32 requests behind 333 tokens 17.8 us.  Read for each request by
