@@ -114,8 +114,9 @@ __device__ __forceinline__ Req req_of(Args &a, int r) {
         s.q0 = a.q_start[0];
         const int T = max((int)((unsigned)a.q_start[a.R] - (unsigned)s.q0), 0);
         s.T = s.q0 < 0 || s.q0 > a.M ? 0 : min(T, a.M - s.q0);
-        s.len = min(max(a.prefix_len[0], 0), a.prefix_blocks * a.page);
-        s.too_long = s.len > a.max_prefix;
+        const int held = max(a.prefix_len[0], 0);  // (of which the table may have fewer)
+        s.len = min(held, a.prefix_blocks * a.page);
+        s.too_long = held > a.max_prefix;
         s.start = 0;
         s.units = s.T == 0 ? 0 : s.too_long ? 1 : (s.len + KV_STEP - 1) / KV_STEP;
         s.groups = (s.T * a.G + RW - 1) / RW;
@@ -125,8 +126,9 @@ __device__ __forceinline__ Req req_of(Args &a, int r) {
     const int T = max((int)((unsigned)a.q_start[r + 1] - (unsigned)s.q0), 0);
     s.T = min(T, a.max_q);
     if (s.q0 < 0 || s.q0 > a.M - s.T) s.T = 0;
-    s.len = min(max(a.lens[r], 0), a.max_blocks * a.page);
-    s.too_long = s.len > a.max_len || T > a.max_q;
+    const int held = max(a.lens[r], 0);
+    s.len = min(held, a.max_blocks * a.page);
+    s.too_long = held > a.max_len || T > a.max_q;
     s.start = a.window > 0 ? max(s.len - s.T - a.window + 1, 0) & ~(KV_STEP - 1) : 0;
     s.units = s.T == 0 ? 0 : s.too_long ? 1 : max((s.len - s.start + KV_STEP - 1) / KV_STEP, 1);
     s.groups = (s.T * a.G + RW - 1) / RW;
