@@ -163,6 +163,13 @@ __global__ void __launch_bounds__(512) kv_prefix_join_kernel(KvPrefixJoinArgs p)
 // the step before is on the vector unit.  Nothing is masked but what lies
 // behind the prefix's last token.
 //
+// A score times its factor less the row's maximum is one FMA, exact where the maximum
+// is that product rounded: they differ by up to 2^-24 of it, which past LARGEST would
+// put the largest token's power outside f16 (at 2^28 rows were 0 or NaN).  Rows
+// that may have such scores round the product first, as the requests' kernel does, in
+// the masked steps; which rows those are goes by their own queries and the window's
+// key scales, so no other row's bits depend on it.
+//
 // Four waves of 32 rows, two workgroups a CU (1024 rows a head 95.4 us, one of eight
 // waves 99.6: all of them wait at every step's barrier); 16 rows a wave where rows are
 // few (prefix_shape); 64 rows a wave leave one wave a SIMD (196 us).  What an unmasked
@@ -177,7 +184,10 @@ __global__ void __launch_bounds__(WAVES * 64, 2) kv_prefix_rows_kernel(KvAttnArg
     constexpr int PW = 2 * KB / WAVES;  // kilobytes of codes that a wave brings of a step
     static_assert(PW >= 1 && PW * WAVES == 2 * KB, "half of the waves bring keys, half values");
     constexpr float UNIT = Code<E4M3>::unit, BIAS = Code<E4M3>::bias;
+    // a score is at most this times its factor: D codes times queries of up to 2^14
+    constexpr float REACH = D * 0x1p14f * (E4M3 ? 448.f : 128.f) / UNIT, LARGEST = 0x1p22f;
     __shared__ u32x4_t kbuf[2][2 * KB * 64], vbuf[2][2 * KB * 64];
+    __shared__ float reach[WAVES];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g = lane >> 4, c = lane & 15;
     constexpr int RW = 16 * NR * WAVES;
@@ -238,8 +248,15 @@ __global__ void __launch_bounds__(WAVES * 64, 2) kv_prefix_rows_kernel(KvAttnArg
             sum += __shfl_xor(sum, 32);
         }
         k0[n] = -(BIAS / UNIT) * sum;
-        cs[n] = ldexpf(fabsf(a.scale), -e2);
+        cs[n] = top > 0.f ? ldexpf(fabsf(a.scale), -e2) : 0.f;
     }
+    // the wave's largest factor
+    float most_cs = cs[0];
+#pragma unroll
+    for (int n = 1; n < NR; ++n) most_cs = fmaxf(most_cs, cs[n]);
+#pragma unroll
+    for (int d = 8; d; d >>= 1) most_cs = fmaxf(most_cs, __shfl_xor(most_cs, d));
+    if (lane == 0) reach[wave] = most_cs;
 
     f32x4_t o[NR][DT], s[NR][2];
     float m[NR], nm[NR], l[NR], ps[NR], vref = 0.f;
@@ -271,10 +288,14 @@ __global__ void __launch_bounds__(WAVES * 64, 2) kv_prefix_rows_kernel(KvAttnArg
             }
         }
         // vref: a power of two at least as large as every value scale so far
-        float up = fmaxf(my_vs, 0.f);
+        float up = fmaxf(my_vs, 0.f), most_ks = my_ks;
 #pragma unroll
-        for (int d = 32; d; d >>= 1) up = fmaxf(up, __shfl_xor(up, d));
+        for (int d = 32; d; d >>= 1) {
+            up = fmaxf(up, __shfl_xor(up, d));
+            most_ks = fmaxf(most_ks, __shfl_xor(most_ks, d));
+        }
         up = readlane_f(up, 0);
+        most_ks = readlane_f(most_ks, 0) * REACH;
         if (up > vref) {
             up = pow2_above(up);
             const float down = vref / up;
@@ -297,7 +318,7 @@ __global__ void __launch_bounds__(WAVES * 64, 2) kv_prefix_rows_kernel(KvAttnArg
         // vref leaves p in f16's range
         const bool plain = !__any(page0 + lane <= (w1 - 1) >> shift && !(my_rr > 0.f && my_rr <= 8.f));
         const auto page_of = [&](int i) { return ((w0 + min(i, steps - 1) * KV_STEP) >> shift) - page0; };
-        __syncthreads();  // LDS is free of the last window
+        __syncthreads();  // LDS is free of the last window (and every wave's reach is there)
         // this wave's part of step i (of the last one again where i is past it)
         const auto load = [&](u32x4_t(&to)[PW], int i) {
             const int page = page_of(i), t = w0 + min(i, steps - 1) * KV_STEP;
@@ -340,6 +361,7 @@ __global__ void __launch_bounds__(WAVES * 64, 2) kv_prefix_rows_kernel(KvAttnArg
         // lane's largest of each row
         float f[NR], top[NR];
         const auto sees = [&](int i, int e) { return w0 + i * KV_STEP + 4 * g + 16 * (e >> 2) + (e & 3) < rq.len; };
+        bool large = false;  // whether any of the workgroup's rows may have large scores
         const auto largest = [&](auto masked, int i) {
             const float ks = readlane_f(my_ks, page_of(i));
             const bool there = !decltype(masked)::value || __builtin_amdgcn_readlane(my_page, page_of(i)) >= 0;
@@ -351,6 +373,11 @@ __global__ void __launch_bounds__(WAVES * 64, 2) kv_prefix_rows_kernel(KvAttnArg
                 for (int e = 0; e < 8; ++e) v[e] = !decltype(masked)::value || sees(i, e) ? s[n][e >> 2][e & 3] : NEG_INF;
                 const float most = fmaxf(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])), fmaxf(fmaxf(v[4], v[5]), fmaxf(v[6], v[7])));
                 top[n] = !decltype(masked)::value || (there && most > NEG_INF) ? most * f[n] : NEG_INF;
+                if (decltype(masked)::value && large && !(cs[n] * most_ks <= LARGEST)) {
+                    s[n][0] *= f[n];
+                    s[n][1] *= f[n];
+                    f[n] = 1.f;
+                }
             }
         };
         // step i: keys of i + 1 and values of i are in LDS, scores of i in s.
@@ -466,6 +493,8 @@ __global__ void __launch_bounds__(WAVES * 64, 2) kv_prefix_rows_kernel(KvAttnArg
         u32x4_t st0[PW], st1[PW];
         load(st0, 0);
         load(st1, 1);
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) large |= !(readlane_f(reach[w], 0) * most_ks <= LARGEST);
         store(std::true_type(), st0, 0);
         if (!brings_v) store(std::true_type(), st1, 1);
         load(st0, brings_v ? 1 : 2);
@@ -477,7 +506,7 @@ __global__ void __launch_bounds__(WAVES * 64, 2) kv_prefix_rows_kernel(KvAttnArg
             for (int n = 0; n < NR; ++n)
                 s[n][q / KS] = __builtin_amdgcn_mfma_f32_16x16x32_f16(key(kbuf[0], q), qf[n][q % KS], q % KS == 0 ? start(n) : s[n][q / KS], 0, 0, 0);
         largest(std::true_type(), 0);
-        const int clear = plain ? (w1 - w0) / KV_STEP - 1 : 0;  // steps before a whole one
+        const int clear = plain && !large ? (w1 - w0) / KV_STEP - 1 : 0;  // steps before a whole one
         int i = 0;
         for (; i + 2 <= clear; i += 2) {
             step(std::false_type(), st0, i);
