@@ -32,3 +32,15 @@ def test_sizes_are_the_rules(seed):
         seen.add((want["kind"], want["shape"]))
         n += 1
     assert n > 300 and {k for k, _ in seen} == {"line", "last", "cut", "even"}
+
+
+@pytest.mark.parametrize("R,Hq,Hkv", [(1, 8, 1), (1, 32, 8), (24, 1, 1), (8, 64, 1), (48, 32, 8)])
+@pytest.mark.parametrize("max_prefix", [32768, 131072, 1 << 20])
+def test_sizes_cost_no_search_of_all_parts(R, Hq, Hkv, max_prefix):
+    """A call plans on the host each time, beside kernels of 20 us (trying each number of parts took up to 50)."""
+    f, best = pkg.raw().qg_kv_prefix_attention_workspace_bytes, 1.0
+    for _ in range(200):
+        t = time.perf_counter()
+        f(R, R, Hq, Hkv, 128, 64, 1, 4096, max_prefix)
+        best = min(best, time.perf_counter() - t)
+    assert best < 15e-6, best
