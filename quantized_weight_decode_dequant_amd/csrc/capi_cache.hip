@@ -1,7 +1,7 @@
 // C ABI of the operators between the products (declared in include/qgemv.h):
 // the norms, the rotation, the paged 8-bit cache with its tables, its append
-// and its attention, and the sampling behind the last product.  As in capi.hip, arguments are checked on the host before any
-// HIP call.
+// and its attention, and the sampling behind the last product.  As in capi.hip,
+// arguments are checked on the host before any HIP call.
 #include <cmath>
 #include <cstdint>
 
@@ -341,7 +341,9 @@ int kv_attention_run(const qg_kv_cache *cache, int64_t R, int64_t M, int64_t Hq,
     } catch (...) {
         return QG_EINTERNAL;
     }
-}size_t qg_kv_prefix_attention_workspace_bytes(int64_t R, int64_t M, int64_t Hq, int64_t Hkv, int64_t D,
+}
+
+size_t qg_kv_prefix_attention_workspace_bytes(int64_t R, int64_t M, int64_t Hq, int64_t Hkv, int64_t D,
                                               int64_t page, int64_t max_q, int64_t max_len,
                                               int64_t max_prefix) {
     KvPrefixPlan p;
@@ -436,8 +438,6 @@ int kv_prefix_attention_run(const qg_kv_cache *cache, int64_t R, int64_t M, int6
         return QG_EINTERNAL;
     }
 }
-
-
 
 size_t qg_sample_workspace_bytes(int64_t M, int64_t V) {
     SampleLayout l;

@@ -73,6 +73,7 @@ struct KvTablesArgs {
 hipError_t launch_kv_append(const KvAppendArgs &a, bool e4m3, hipStream_t s);
 hipError_t launch_kv_attention(const KvAttnArgs &a, int D, bool e4m3, hipStream_t s);
 hipError_t launch_kv_tables(const KvTablesArgs &a, hipStream_t s);
+
 // How an attention call is cut; false where its work does not fit 31 bits.
 struct KvAttnPlan {
     int groups;          // row groups of a request of max_q tokens

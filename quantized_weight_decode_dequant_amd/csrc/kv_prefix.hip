@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(512) kv_prefix_join_kernel(KvPrefixJoinArgs p)
 // reaches 1.4 of the 2.5 PFLOP/s); keys read a step earlier changed nothing.
 template <bool E4M3, int D, int NR, int WAVES>
 __global__ void __launch_bounds__(WAVES * 64, 2) kv_prefix_rows_kernel(KvAttnArgs) {
-    constexpr int KS = D / 32, DT = D / 16, KB = D / 32, TH = WAVES * 64;
+    constexpr int KS = D / 32, DT = D / 16, KB = D / 32;
     constexpr int PW = 2 * KB / WAVES;  // kilobytes of codes that a wave brings of a step
     static_assert(PW >= 1 && PW * WAVES == 2 * KB, "half of the waves bring keys, half values");
     constexpr float UNIT = Code<E4M3>::unit, BIAS = Code<E4M3>::bias;

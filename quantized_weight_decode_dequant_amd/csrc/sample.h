@@ -27,7 +27,6 @@ struct SampleRow {
     unsigned long long p_mass;  // mass of the bins below p_lo
     unsigned long long k_mass;  // mass of the bins below k_bin
     unsigned long long mass;    // of all bins
-    unsigned long long pad2;
 };
 
 struct SampleArgs {

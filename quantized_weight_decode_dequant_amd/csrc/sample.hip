@@ -549,7 +549,6 @@ __device__ __forceinline__ bool find_borders(const SampleArgs &a, int m, const A
     r.done = 0;
     r.listed = 0;
     r.top = top;
-    r.pad2 = 0;
     r.p_lo = by_p ? (int)sh.found32[2] : NB;
     r.p_hi = by_p ? (int)sh.found32[3] : -1;
     r.full = by_p ? r.p_lo : by_k ? r.k_bin : NB;
