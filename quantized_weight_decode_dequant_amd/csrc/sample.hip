@@ -115,7 +115,7 @@ __device__ __forceinline__ Ask ask_of(const SampleArgs &a, int m) {
     q.greedy = !(T > 0.f) || k == 1;
     q.c = 1.44269504088896340736 / (double)T;
     q.k = k > 0 && k < a.V ? k : 0;
-    q.p = p < 1.f ? (double)p : 1.0;  // (NaN: off)
+    q.p = p < 1.f ? fmax((double)p, 0.0) : 1.0;  // (NaN: off; its products become whole numbers, so none is negative)
     q.minp = minp > 0.f ? fmin((double)minp, 1.0) : 0.0;
     return q;
 }
