@@ -429,22 +429,8 @@ def _arg(t, dtype, shape, dev, name):
     return t.data_ptr()
 
 
-def _rows(t, H, D, dtype, dev, name):
-    """Address and row stride of a [M, H, D] tensor whose rows are dense."""
-    shape = t.shape
-    if t.dtype is not dtype or len(shape) != 3 or shape[1] != H or shape[2] != D:
-        raise ValueError("%s must be a %s tensor [M, %d, %d] (got %s %s)"
-                         % (name, dtype, H, D, t.dtype, tuple(shape)))
-    if t.get_device() != dev:
-        raise ValueError("%s must be a device tensor on device %d (got %s)" % (name, dev, t.device))
-    row, head, dim = t.stride()
-    if dim != 1 or (H > 1 and head != D):
-        raise ValueError("%s: the heads and dimensions of a token must be dense" % name)
-    return t.data_ptr(), (row if shape[0] > 1 else H * D)
-
-
-def _rows_of(t, shape, dtype, dev, name):
-    """_rows of a tensor that is to have this shape."""
+def _rows(t, shape, dtype, dev, name):
+    """Address and row stride of a tensor of this shape, [M, H, D], whose rows are dense."""
     if t.dtype is not dtype or t.shape != shape:
         raise ValueError("%s must be a %s tensor of shape %s (got %s %s)"
                          % (name, dtype, tuple(shape), t.dtype, tuple(t.shape)))
@@ -461,6 +447,8 @@ def _rows_of(t, shape, dtype, dev, name):
 def _call(dev, stream, where, fn, *args):
     """fn(*args, stream) with `dev` current; stream: as given, or dev's current one."""
     torch = _torch()
+    # (torch.cuda.current_device without its check that the device was initialized, 0.2 us
+    # of a call; a tensor on it says that it was)
     if torch._C._cuda_getDevice() != dev:
         with torch.cuda.device(dev):
             return _call(dev, stream, where, fn, *args)
@@ -559,13 +547,13 @@ def qk_norm_rope_run(q, k, positions, inv_freq, q_weight=None, k_weight=None, ep
         if q_out.shape != shape or (k is not None and k_out.shape != kshape):
             raise ValueError("q_out and k_out must have the shapes of q and k")
         return q_out, k_out
-    qp, qs = _rows_of(q, shape, dtype, dev, "q")
-    qo, qos = _rows_of(q_out, shape, bf16, dev, "q_out")
+    qp, qs = _rows(q, shape, dtype, dev, "q")
+    qo, qos = _rows(q_out, shape, bf16, dev, "q_out")
     kp = ko = None
     ks = kos = 0
     if k is not None:
-        kp, ks = _rows_of(k, kshape, dtype, dev, "k")
-        ko, kos = _rows_of(k_out, kshape, bf16, dev, "k_out")
+        kp, ks = _rows(k, kshape, dtype, dev, "k")
+        ko, kos = _rows(k_out, kshape, bf16, dev, "k_out")
     _call(dev, stream, "qk_norm_rope_run", raw().qk_norm_rope_run, qp, qs, kp, ks, xt, M, Hq, Hkv, D,
           _arg(q_weight, bf16, (D,), dev, "q_weight"), _arg(k_weight, bf16, (D,), dev, "k_weight"), eps,
           _arg(positions, i32, (M,) if len(pshape) == 1 else (axes, M), dev, "positions"), axes,
@@ -651,8 +639,8 @@ def kv_append_run(cache: KVCache, K, V, slots, stream=None):
     if M == 0:
         return
     dev, H, D, bf16 = cache.device, cache.Hkv, cache.D, torch.bfloat16
-    kp, ks = _rows(K, H, D, bf16, dev, "K")
-    vp, vs = _rows(V, H, D, bf16, dev, "V")
+    kp, ks = _rows(K, (M, H, D), bf16, dev, "K")
+    vp, vs = _rows(V, (M, H, D), bf16, dev, "V")
     _call(dev, stream, "kv_append_run", raw().kv_append_run, cache._ref, M, kp, ks, vp, vs,
           _arg(slots, torch.int32, (M,), dev, "slots"))
 
@@ -687,8 +675,8 @@ def kv_attention_run(cache: KVCache, q, q_start, lens, table, max_q: int, max_le
     if M == 0 or R == 0:
         return out
     dev, D = cache.device, cache.D
-    qp, qs = _rows(q, Hq, D, torch.bfloat16, dev, "q")
-    op, os_ = _rows(out, Hq, D, out.dtype, dev, "out")
+    qp, qs = _rows(q, (M, Hq, D), torch.bfloat16, dev, "q")
+    op, os_ = _rows(out, (M, Hq, D), out.dtype, dev, "out")
     lib = raw()
     if workspace is None:
         nbytes = lib.qg_kv_attention_workspace_bytes(R, M, Hq, cache.Hkv, D, cache.page, max_q, max_len, window)
@@ -736,8 +724,8 @@ def kv_prefix_attention_run(cache: KVCache, q, q_start, lens, table, prefix_tabl
     if M == 0 or R == 0:
         return out
     dev, D = cache.device, cache.D
-    qp, qs = _rows(q, Hq, D, torch.bfloat16, dev, "q")
-    op, os_ = _rows(out, Hq, D, out.dtype, dev, "out")
+    qp, qs = _rows(q, (M, Hq, D), torch.bfloat16, dev, "q")
+    op, os_ = _rows(out, (M, Hq, D), out.dtype, dev, "out")
     lib = raw()
     if workspace is None:
         nbytes = lib.qg_kv_prefix_attention_workspace_bytes(R, M, Hq, cache.Hkv, D, cache.page, max_q, max_len, max_prefix)
