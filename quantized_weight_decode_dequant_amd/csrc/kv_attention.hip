@@ -39,20 +39,15 @@
 namespace qg {
 
 // Joins the segments of a (query token, head), where there are several: W
-// waves for each.  D / 4 lanes take 4 dimensions each of one segment; the
-// waves' groups of them take the segments in turn, eight loads in flight a
-// lane, and join across lanes and in LDS.  Many rows take one wave each, few
-// rows eight.  The maximum runs along with the sums (read in a pass before
-// them: 128 rows 10.8 us against 10.2, 64 rows 7.8 against 7.4).  Bound by
+// waves for each (join_segments), one where rows are many, else eight.  Bound by
 // latency: request, head of the workspace, segments in turn.
 template <int D, int RW, int W>
 __global__ void __launch_bounds__(512) kv_attn_join_kernel(KvAttnArgs) {
-    constexpr int TD = D / 4, NG = W * 64 / TD, AHEAD = 8, ROWS = 8 / W;
-    __shared__ f32x4_t so[W > 1 ? W : 1][TD];
-    __shared__ float sl[W], smx[W];
+    constexpr int ROWS = 8 / W;
+    __shared__ JoinLds<D, W> lds;
     Args &a = args();
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wi = wave % W, tid = wi * 64 + lane, gi = tid / TD, d4 = tid % TD;
+    const int wi = wave % W;
     const int which = blockIdx.x * ROWS + wave / W;  // (request, token, head)
     const int r = which / (a.max_q * a.Hq), j = which / a.Hq % a.max_q, hq = which % a.Hq;
     if (r >= a.R) return;
@@ -74,78 +69,9 @@ __global__ void __launch_bounds__(512) kv_attn_join_kernel(KvAttnArgs) {
     // (never so, unless another call wrote to the workspace in between)
     if (slot < 0 || n < 1 || n > a.part_slots || slot > a.part_slots - n) return;
     const size_t at = (size_t)slot * a.part_rows + row % RW, step = a.part_rows;
-    // with a running maximum, so that values and maxima are loaded together
-    float mx = NEG_INF;
-    f32x4_t o = {0.f, 0.f, 0.f, 0.f};
-    float l = 0.f;
-    for (int c0 = gi; c0 < n; c0 += NG * AHEAD) {
-        f32x4_t v[AHEAD];
-        f32x2_t ml[AHEAD];
-#pragma unroll
-        for (int i = 0; i < AHEAD; ++i) {
-            const int c = min(c0 + i * NG, n - 1);
-            v[i] = *reinterpret_cast<const f32x4_t *>(a.part + (at + c * step) * D + 4 * d4);
-            ml[i] = *reinterpret_cast<const f32x2_t *>(a.part_ml + 2 * (at + c * step));
-        }
-        float mn = mx;
-#pragma unroll
-        for (int i = 0; i < AHEAD; ++i) mn = fmaxf(mn, ml[i][0]);
-        const float down = mn == NEG_INF ? 1.f : __builtin_amdgcn_exp2f(mx - mn);
-        mx = mn;
-        l *= down;
-        o *= down;
-#pragma unroll
-        for (int i = 0; i < AHEAD; ++i) {
-            // (a row of NaN scores has no maximum, but a NaN sum)
-            const float f = mx == NEG_INF ? 0.f : __builtin_amdgcn_exp2f(ml[i][0] - mx);
-            if (c0 + i * NG < n) {
-                l = fmaf(f, ml[i][1], l);
-                o += v[i] * f;
-            }
-        }
-    }
-    // the wave's groups of lanes, then the waves
-    float top = mx;
-#pragma unroll
-    for (int d = TD; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
-    const float down = top == NEG_INF ? 1.f : __builtin_amdgcn_exp2f(mx - top);
-    l *= down;
-    o *= down;
-#pragma unroll
-    for (int d = TD; d < 64; d <<= 1) {
-        l += __shfl_xor(l, d);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] += __shfl_xor(o[e], d);
-    }
-    if constexpr (W > 1) {
-        if (lane < TD) so[wi][lane] = o;
-        if (lane == 0) {
-            sl[wi] = l;
-            smx[wi] = top;
-        }
-        __syncthreads();
-        if (wi != 0) return;
-        const float mine = top;
-#pragma unroll
-        for (int k = 1; k < W; ++k) top = fmaxf(top, smx[k]);
-        const float own = top == NEG_INF ? 1.f : __builtin_amdgcn_exp2f(mine - top);
-        o *= own;
-        l *= own;
-#pragma unroll
-        for (int k = 1; k < W; ++k) {
-            const float f = top == NEG_INF ? 1.f : __builtin_amdgcn_exp2f(smx[k] - top);
-            o += so[k][lane % TD] * f;
-            l = fmaf(sl[k], f, l);
-        }
-    }
-    if (lane >= TD) return;
-    const float f = l == 0.f ? 0.f : 1.f / l;
-    const size_t to = (size_t)(rq.q0 + j) * a.out_stride + (size_t)hq * D + 4 * d4;
-    o *= f;
-    if (a.out_f32)
-        *reinterpret_cast<f32x4_t *>((float *)a.out + to) = o;
-    else
-        *reinterpret_cast<u32x2_t *>((uint16_t *)a.out + to) = bf16x4(o);
+    join_segments<D, W>(a, lds, n, rq.q0 + j, hq, wi, lane, [&](int c) {
+        return Part{a.part, a.part_ml, at + c * step};
+    });
 }
 
 namespace {

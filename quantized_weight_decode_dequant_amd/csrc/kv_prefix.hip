@@ -59,17 +59,15 @@ __device__ __forceinline__ Segments segments_of(const KvAttnArgs &a, const Req &
     return s;
 }
 
-// Joins the segments of a (query token, head): W waves for each, D / 4 lanes 4
-// dimensions each of one segment, as kv_attn_join_kernel does.
+// Joins the segments of a (query token, head), its request's and the prefix's: W waves for each.
 template <int D, int W>
 __global__ void __launch_bounds__(512) kv_prefix_join_kernel(KvPrefixJoinArgs p) {
-    constexpr int TD = D / 4, NG = W * 64 / TD, AHEAD = 8, ROWS = 8 / W;
-    __shared__ f32x4_t so[W > 1 ? W : 1][TD];
-    __shared__ float sl[W], smx[W];
+    constexpr int ROWS = 8 / W;
+    __shared__ JoinLds<D, W> lds;
     Args &a = *(Args *)__builtin_amdgcn_kernarg_segment_ptr();
     Args &b = *((Args *)__builtin_amdgcn_kernarg_segment_ptr() + 1);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wi = wave % W, tid = wi * 64 + lane, gi = tid / TD, d4 = tid % TD;
+    const int wi = wave % W;
     const int which = blockIdx.x * ROWS + wave / W;  // (request, token, head)
     const int r = which / (a.max_q * a.Hq), j = which / a.Hq % a.max_q, hq = which % a.Hq;
     if (r >= a.R) return;
@@ -81,79 +79,10 @@ __global__ void __launch_bounds__(512) kv_prefix_join_kernel(KvPrefixJoinArgs p)
                         : segments_of(p.pre, pq, 0, 0, pq.units > 0 ? max(b.head[0], 1) : 1, p.pre_rw, head, prow, true, 0);
     const float *part = p.both ? a.part : b.part, *part_ml = p.both ? a.part_ml : b.part_ml;
     const int n = s.n + t.n;
-    float mx = NEG_INF;
-    f32x4_t o = {0.f, 0.f, 0.f, 0.f};
-    float l = 0.f;
-    for (int c0 = gi; c0 < n; c0 += NG * AHEAD) {
-        f32x4_t v[AHEAD];
-        f32x2_t ml[AHEAD];
-#pragma unroll
-        for (int i = 0; i < AHEAD; ++i) {
-            const int c = min(c0 + i * NG, n - 1);
-            const bool own = c < s.n;
-            const size_t at = own ? s.at + c * s.step : t.at + (c - s.n) * t.step;
-            v[i] = *reinterpret_cast<const f32x4_t *>((own ? a.part : part) + at * D + 4 * d4);
-            ml[i] = *reinterpret_cast<const f32x2_t *>((own ? a.part_ml : part_ml) + 2 * at);
-        }
-        float mn = mx;
-#pragma unroll
-        for (int i = 0; i < AHEAD; ++i) mn = fmaxf(mn, ml[i][0]);
-        const float down = mn == NEG_INF ? 1.f : __builtin_amdgcn_exp2f(mx - mn);
-        mx = mn;
-        l *= down;
-        o *= down;
-#pragma unroll
-        for (int i = 0; i < AHEAD; ++i) {
-            // (a row of NaN scores has no maximum, but a NaN sum)
-            const float f = mx == NEG_INF ? 0.f : __builtin_amdgcn_exp2f(ml[i][0] - mx);
-            if (c0 + i * NG < n) {
-                l = fmaf(f, ml[i][1], l);
-                o += v[i] * f;
-            }
-        }
-    }
-    // the wave's groups of lanes, then the waves
-    float top = mx;
-#pragma unroll
-    for (int d = TD; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
-    const float down = top == NEG_INF ? 1.f : __builtin_amdgcn_exp2f(mx - top);
-    l *= down;
-    o *= down;
-#pragma unroll
-    for (int d = TD; d < 64; d <<= 1) {
-        l += __shfl_xor(l, d);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] += __shfl_xor(o[e], d);
-    }
-    if constexpr (W > 1) {
-        if (lane < TD) so[wi][lane] = o;
-        if (lane == 0) {
-            sl[wi] = l;
-            smx[wi] = top;
-        }
-        __syncthreads();
-        if (wi != 0) return;
-        const float mine = top;
-#pragma unroll
-        for (int k = 1; k < W; ++k) top = fmaxf(top, smx[k]);
-        const float own = top == NEG_INF ? 1.f : __builtin_amdgcn_exp2f(mine - top);
-        o *= own;
-        l *= own;
-#pragma unroll
-        for (int k = 1; k < W; ++k) {
-            const float f = top == NEG_INF ? 1.f : __builtin_amdgcn_exp2f(smx[k] - top);
-            o += so[k][lane % TD] * f;
-            l = fmaf(sl[k], f, l);
-        }
-    }
-    if (lane >= TD) return;
-    const float f = l == 0.f ? 0.f : 1.f / l;
-    const size_t to = (size_t)(rq.q0 + j) * a.out_stride + (size_t)hq * D + 4 * d4;
-    o *= f;
-    if (a.out_f32)
-        *reinterpret_cast<f32x4_t *>((float *)a.out + to) = o;
-    else
-        *reinterpret_cast<u32x2_t *>((uint16_t *)a.out + to) = bf16x4(o);
+    join_segments<D, W>(a, lds, n, rq.q0 + j, hq, wi, lane, [&](int c) {
+        const bool own = c < s.n;
+        return Part{own ? a.part : part, own ? a.part_ml : part_ml, own ? s.at + c * s.step : t.at + (c - s.n) * t.step};
+    });
 }
 
 // The prefix against many rows: a workgroup of WAVES waves takes 16 NR WAVES
