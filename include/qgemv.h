@@ -680,8 +680,8 @@ size_t qg_kv_attention_workspace_bytes(int64_t R, int64_t M, int64_t Hq, int64_t
  *  scale        of the scores, below 2^127 in magnitude; usually 1 / sqrt(D).
  *  max_q        1..32: no request has more new tokens; of one that has, the
  *               first max_q rows become NaN and the others are left.  R * max_q * Hq <= 2^26 - 8 (QG_ESHAPE).
- *  max_len      1..max_blocks * page: no request is longer; a longer one gets
- *               rows of NaN.  (The product of requests, heads, row groups and
+ *  max_len      1..max_blocks * page: no request is longer; a longer one (of
+ *               more tokens than its table holds, too) gets rows of NaN.  (The product of requests, heads, row groups and
  *               max_len / 32 has to stay below 2^31: QG_ESHAPE.)
  *  workspace    device buffer, 16-B, of qg_kv_attention_workspace_bytes; NULL
  *               if that is 0.  Scratch: calls that may overlap, or graphs
@@ -732,7 +732,8 @@ size_t qg_kv_prefix_attention_workspace_bytes(int64_t R, int64_t M, int64_t Hq, 
  *               not attended to.  prefix_blocks >= 1, * page <= 2^30.
  *  prefix_len   device int32 [1]: the prefix's tokens, 0 or more.
  *  max_prefix   0..prefix_blocks * page: the prefix is not longer; if it is,
- *               all rows become NaN.
+ *               all rows become NaN.  With max_len it chooses how the call is
+ *               cut, so bounds far above the lengths there are cost time.
  *  tree_mask    as in kv_attention_run (over the request's own tokens).
  *  workspace    device buffer, 16-B, of qg_kv_prefix_attention_workspace_bytes,
  *               always.  Scratch: calls that may overlap, or graphs that may

@@ -10,14 +10,15 @@
 // rows times equal parts of the prefix.  What joins the segments is a kernel, or
 // the requests' own one (KV_LAST), whichever costs less (kv_prefix_plan).
 //
-// Measured (passes, 8 KV heads of 128 unless said): 4 requests of 4 rows behind 8192
+// Measured (eager calls one after another, 8 KV heads of 128 unless said; the rules'
+// figures below are whole calls in a captured graph): 4 requests of 4 rows behind 8192
 // tokens 18.5 us (12.8 the line, 6.2 the join: latency, a chain of loads before the
-// first step and after the last); 48 behind 32768 73 us (47.6 the prefix, 510 TFLOP/s;
+// first step and after the last; 17.4 in a graph); 48 behind 32768 73 us (47.5 the prefix, 510 TFLOP/s;
 // 28 the requests, up to 2000 own tokens); 256 drafts of 16 requests, 1024 rows a
-// head, behind 20011 110 us (93 the prefix, 720 TFLOP/s; 29 the requests, of which 6
-// join, latency); 8 requests, 4 heads of 256, E4M3, behind 131072 87 us (62 the
-// prefix, 4.3 TB/s and 550 TFLOP/s; 11.6 the requests, 13 the join, of 33 MB of
-// segments); 32 requests behind 333 tokens 17.8 us.  Read for each request by
+// head, behind 20011 110 us (94 the prefix, 715 TFLOP/s; 29 the requests, of which 6
+// join, latency); 8 requests, 4 heads of 256, E4M3, behind 131072 87 us (61 the
+// prefix, 4.4 TB/s and 560 TFLOP/s; 11.7 the requests, 13 the join, of 33 MB of
+// segments); 32 requests behind 333 tokens 18.0 us.  Read for each request by
 // kv_attention_run, 48 times 32768 tokens are 3.2 GB.
 #include "kv_attn_kernel.h"
 
@@ -92,12 +93,12 @@ __global__ void __launch_bounds__(512) kv_prefix_join_kernel(KvPrefixJoinArgs p)
 // the step before is on the vector unit.  Nothing is masked but what lies
 // behind the prefix's last token.
 //
-// A score times its factor less the row's maximum is one FMA, exact where the maximum
-// is that product rounded: they differ by up to 2^-24 of it, which past LARGEST would
-// put the largest token's power outside f16 (at 2^28 rows were 0 or NaN).  Rows
-// that may have such scores round the product first, as the requests' kernel does, in
-// the masked steps; which rows those are goes by their own queries and the window's
-// key scales, so no other row's bits depend on it.
+// A score times its factor less the row's maximum is one FMA, whose product is exact
+// where the maximum's was rounded: by up to 2^-24 of the score the largest token's power
+// is not 1, which for scores past LARGEST would leave f16 (from about 2^27 on rows were 0
+// or NaN).  Rows that may have such scores round the product first, as the requests'
+// kernel does, in masked steps; which rows those are goes by their own queries and the
+// window's key scales, so no other row's bits depend on it.
 //
 // Four waves of 32 rows, two workgroups a CU (1024 rows a head 95.4 us, one of eight
 // waves 99.6: all of them wait at every step's barrier); 16 rows a wave where rows are

@@ -5,8 +5,8 @@
 //   angle_i = position[axis_i] * inv_freq_i   for each of `half` pairs
 //   (a, b) -> (a cos - b sin, b cos + a sin)  pairs (i, i + half) or (2i, 2i + 1)
 //
-// The angle is the exact product in fp64 (31 and 24 bits), taken in turns and
-// reduced to half a turn there, so a position of 2^30 is as good as one of 10;
+// The angle is an fp64 product in turns (two roundings, 2^-52 of it) reduced to
+// half a turn there, so a position of 2^30 is nearly as good as one of 10;
 // its sine and cosine, the norm and the rotation are fp32, and the one
 // rounding to fewer bits is the output's to bf16.
 //
