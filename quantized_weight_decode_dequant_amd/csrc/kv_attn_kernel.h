@@ -37,7 +37,9 @@ constexpr float OUT_UNIT = 0x1p-31f;
 
 // An int8 code c enters the MFMA as the f16 whose bits are c + 128: a
 // denormal (which the MFMA keeps), worth (c + 128) 2^-24.  The products'
-// accumulators are corrected by -128 times the other operand's sum.
+// accumulators are corrected by -128 times the other operand's sum, so their
+// fp32 roundings are those of sums of up to 255: an output is off by up to
+// about 2^-20 of 128 times its scale besides, also where all its codes are 0.
 template <bool E4M3>
 struct Code {
     static constexpr float unit = E4M3 ? 1.f : 0x1p24f;
