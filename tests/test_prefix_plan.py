@@ -37,10 +37,17 @@ def test_sizes_are_the_rules(seed):
 @pytest.mark.parametrize("R,Hq,Hkv", [(1, 8, 1), (1, 32, 8), (24, 1, 1), (8, 64, 1), (48, 32, 8)])
 @pytest.mark.parametrize("max_prefix", [32768, 131072, 1 << 20])
 def test_sizes_cost_no_search_of_all_parts(R, Hq, Hkv, max_prefix):
-    """A call plans on the host each time, beside kernels of 20 us (trying each number of parts took up to 50)."""
-    f, best = pkg.raw().qg_kv_prefix_attention_workspace_bytes, 1.0
-    for _ in range(200):
-        t = time.perf_counter()
-        f(R, R, Hq, Hkv, 128, 64, 1, 4096, max_prefix)
-        best = min(best, time.perf_counter() - t)
-    assert best < 15e-6, best
+    """A call plans on the host each time, beside kernels of 20 us: with a long
+    prefix no more than eight times what it takes with a page (trying each number
+    of parts: up to 13)."""
+    f = pkg.raw().qg_kv_prefix_attention_workspace_bytes
+
+    def least(P):
+        best = 1.0
+        for _ in range(300):
+            t = time.perf_counter()
+            f(R, R, Hq, Hkv, 128, 64, 1, 4096, P)
+            best = min(best, time.perf_counter() - t)
+        return best
+
+    assert least(max_prefix) < 8 * least(32)
